@@ -56,7 +56,7 @@ typedef int ea_status;
 #define EA_ERR_ARG 7         /* NULL pointer, bad count, bad enum value            */
 #define EA_ERR_UNSUPPORTED 8 /* valid join-agg the library has no kernel for      */
 #define EA_ERR_DEVICE 9      /* a kernel raised the device error flag (ea_check)   */
-#define EA_ERR_BOUNDS 10     /* a plan descriptor addresses memory outside its arena */
+#define EA_ERR_BOUNDS 10     /* a plan descriptor (or a batch of the paged cache) addresses memory outside its arena */
 
 typedef struct ea_relation_s *ea_relation; /* opaque handle */
 
@@ -223,7 +223,8 @@ const char *ea_last_error(void);
 
 /* Synchronise `stream`, then report (and clear) any asynchronous CUDA error
  * and the device error flag that kernels raise when a bounded wait runs out
- * or a bounds check fails.  Returns EA_ERR_CUDA or EA_ERR_DEVICE on error. */
+ * or a bounds check fails.  Returns EA_ERR_CUDA or EA_ERR_DEVICE on error,
+ * EA_ERR_BOUNDS when a batch of the paged cache was out of range. */
 ea_status ea_check(void *stream);
 
 /* Failure-detection self-test: launch a one-CTA kernel whose thread waits
@@ -376,6 +377,124 @@ typedef struct {
 ea_status ea_attention_run(const char *spec, ea_relation q, ea_relation k, ea_relation v, const ea_attn_opts *opts,
                            void *stream, ea_relation *out);
 
+/* ---------------------------------------------------------- paged cache */
+
+/* The keys and values of many sequences, kept between calls: a tensor
+ * relation [pages, heads, page positions, head dim] whose blocks are the
+ * pages (one page = `page` consecutive positions of one sequence, all
+ * key-value heads), joined with a batch of sequences through a table of page
+ * numbers.  The paper's Example 3.10 keeps K and V dense; the paged form has
+ * no counterpart there.
+ *   EA_CACHE_BF16  cells are bf16.
+ *   EA_CACHE_E4M3  cells are 8-bit floats (4 exponent bits, 3 fraction bits,
+ *                  largest 448) with one scale byte b per (page, head,
+ *                  position): value = code * 2^(b - 127); b = 255: the whole
+ *                  vector is NaN.  A power-of-two scale makes the division
+ *                  before the rounding and the product after it exact, so a
+ *                  code's rounding (2^-4 relative, 2^-10 * 2^(b - 127) where
+ *                  the code is subnormal) is the only one, and every cell is
+ *                  a bf16 value.  ea_cache_append writes no NaN code; a cache
+ *                  filled by other means must hold none either. */
+typedef struct ea_cache_s *ea_cache; /* opaque handle */
+
+typedef enum { EA_CACHE_BF16 = 0, EA_CACHE_E4M3 = 1 } ea_cache_format;
+
+/* A batch of sequences.  Row r of a dense relation belongs to sequence i when
+ * starts[i] <= r < starts[i + 1]; the n_i = starts[i + 1] - starts[i] rows of
+ * sequence i are the last n_i of its lens[i] positions (row starts[i] + j is
+ * position lens[i] - n_i + j), and position p lives in slot p % page of page
+ * pages[i * page_stride + p / page].  Rows before starts[0] or from
+ * starts[n_seqs] on belong to no sequence: they are not read and what a call
+ * would write there stays as it was.
+ * pages, starts and lens are device arrays that the kernels read, so one
+ * captured graph serves every batch that is copied into them; they are
+ * checked on the device: a sequence with starts decreasing, beyond the dense
+ * rows or more than max_new apart, or with lens negative or beyond max_pages
+ * * page, or with a needed page number outside the cache is left out (its
+ * rows unspecified for reads and attention, nothing written outside its own
+ * rows and pages) and the device error word is raised: ea_check reports
+ * EA_ERR_BOUNDS.  ea_cache_check_batch is the same check on the host. */
+typedef struct {
+    const int32_t *pages;   /* [n_seqs][page_stride], the first max_pages of a row in use */
+    const int32_t *starts;  /* [n_seqs + 1], nondecreasing */
+    const int32_t *lens;    /* [n_seqs] */
+    int64_t page_stride;    /* elements between the rows of pages, >= max_pages */
+    int32_t n_seqs;         /* 1 .. 65536 */
+    int32_t max_pages;      /* pages a sequence can have: lens[i] <= max_pages * page */
+    int32_t max_new;        /* an upper bound of n_i known to the caller; 0: the dense rows */
+    int32_t reserved;
+} ea_page_batch;
+
+/* A cache over `pages` pages of `page` positions (16, 32, 64 or 128), `heads`
+ * key-value heads and head dim 64 or 128.  k, v: device arrays [pages][heads]
+ * [page][dim] of bf16 or one-byte codes; k_scale, v_scale: [pages][heads]
+ * [page] scale bytes (e4m3 only, else NULL).  Borrowed: the caller keeps them
+ * alive; 16-byte aligned, on the current device, which stays the cache's
+ * device.  Errors: EA_ERR_ARG, EA_ERR_DTYPE (format), EA_ERR_UNSUPPORTED
+ * (page, dim, no tensor-map encoder). */
+ea_status ea_cache_create(ea_cache_format format, int64_t pages, int32_t page, int32_t heads, int32_t dim, void *k,
+                          void *v, void *k_scale, void *v_scale, ea_cache *out);
+ea_status ea_cache_destroy(ea_cache cache);
+
+/* Write the rows of K and V into the pages.  k, v: f32 or bf16 relations of
+ * the same dtype and extents whose last two dimensions are (heads, head dim),
+ * whole, and whose leading dimensions are the rows, stored in row order.
+ * bf16 cells are the rows rounded to nearest even.  e4m3: the scale of a
+ * vector is 2^e with the least e such that max|x| <= 448 * 2^e, kept in
+ * [-126, 120] (0 for a zero vector), the codes x / 2^e rounded to nearest
+ * even; a vector with an infinity or NaN is stored as NaN.
+ * Positions must be >= 0 (n_i <= lens[i]).  Two rows of one call must not
+ * share a slot (what the slot then holds is unspecified; no other slot is
+ * touched).  Errors: EA_ERR_ARG, EA_ERR_SHAPE, EA_ERR_PARTITION,
+ * EA_ERR_DTYPE, EA_ERR_UNSUPPORTED. */
+ea_status ea_cache_append(ea_cache cache, const ea_page_batch *batch, ea_relation k, ea_relation v, void *stream);
+
+/* Read the batch's positions out of the pages into the rows of k and v (f32
+ * or bf16 relations as in ea_cache_append, overwritten; exact for both
+ * formats).  Errors: as ea_cache_append. */
+ea_status ea_cache_read(ea_cache cache, const ea_page_batch *batch, ea_relation k, ea_relation v, void *stream);
+
+/* Options of ea_cache_attention; zero-initialise. */
+typedef struct {
+    float scale;             /* score scale, > 0; 0 = 1/sqrt(head dim)                          */
+    int32_t causal;          /* nonzero: a query at position p keeps only positions <= p        */
+    ea_relation m_out;       /* optional f32 relation: row maximum of the scaled scores         */
+    ea_relation l_out;       /* optional f32 relation: row sum of exp(score - maximum)          */
+    void *workspace;         /* device memory, 16-byte aligned; its content means nothing       */
+    size_t workspace_bytes;  /* at least what ea_cache_attention_workspace says                 */
+    int64_t reserved[4];
+} ea_cache_attn_opts;
+
+/* Bytes of workspace an ea_cache_attention of this shape needs (partial
+ * results of the splits along the positions).  The call reads nothing that
+ * another left there; calls that may run at the same time need one each. */
+ea_status ea_cache_attention_workspace(ea_cache cache, const ea_page_batch *batch, ea_relation q, size_t *bytes);
+
+/* Attention of the batch's rows over their sequences' pages.  q: bf16, last
+ * two dimensions (query heads, head dim), whole, leading dimensions the rows
+ * in storage order; query heads = g * heads (g <= 128), query head h reads
+ * key-value head floor(h / g).  For row r of sequence i at position p:
+ *   O = SUM_t softmax_t(scale Q.K_t) V_t over t < lens[i] and, if causal,
+ *   t <= p (a causal row with p < 0, and any row with lens[i] = 0, keeps no
+ *   key: O = 0, m = -inf, l = 0).  Without causal n_i may exceed lens[i].
+ * Cells at and beyond lens[i] and unlisted pages never reach a result,
+ * whatever they hold.  A kept position's infinity or NaN reaches every row
+ * of its sequence that shares a tile with a row that keeps it.
+ *   out    bf16, extents of q, not overlapping q; m_out, l_out (both or
+ *          neither): f32, extents of q without the head dim.
+ * Scores, statistics and sums are fp32; the probabilities enter the second
+ * product as bf16.  Results do not depend on what else is in the batch by
+ * more than the fp32 order of the sums.
+ * Errors: as ea_cache_append; EA_ERR_ARG for a missing or small workspace. */
+ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *batch, ea_relation q, const ea_cache_attn_opts *opts,
+                             void *stream, ea_relation out);
+
+/* The check of a batch on the host (no GPU needed): `batch` holds HOST
+ * pointers, rows is the dense row count, write nonzero checks for an append
+ * (positions >= 0, no slot named twice).  EA_OK, or EA_ERR_BOUNDS with a
+ * message that names the first offender. */
+ea_status ea_cache_check_batch(int64_t pages, int32_t page, const ea_page_batch *batch, int64_t rows, int write);
+
 /* ------------------------------------------------------------ exchange */
 
 /* Re-block `in` into the tiling new_parts[0..rank-1] (Section 5.3: the
@@ -404,8 +523,10 @@ ea_status ea_exchange_agg(ea_relation in, ea_agg agg, const ea_dim_part *new_par
 /* What the last ea_joinagg_run / ea_exchange of the calling host thread
  * launched: kernel class (0 exchange, 1 elementwise, 2 row reduction,
  * 3 SIMT contraction, 4 tcgen05 contraction, 5 attention, 6 exchange with
- * aggregation), kernel launches, work tiles,
- * aggregation groups and function specifications (tuples).  Any pointer
+ * aggregation, 7 cache append or read, 8 cache attention), kernel launches,
+ * work tiles (CTAs, for 7 and 8),
+ * aggregation groups and function specifications (tuples; 0 for 7 and 8,
+ * whose work list is made on the device).  Any pointer
  * may be NULL. */
 ea_status ea_last_plan(int32_t *kernel_class, int32_t *launches, int64_t *tiles, int64_t *groups, int64_t *tuples);
 

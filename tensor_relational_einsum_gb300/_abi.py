@@ -23,6 +23,7 @@ MAPS = {"product": 0, "identity": 1, "silu_mul": 2, "add": 3, "exp_sub": 4, "div
 STATUS = {0: "EA_OK", 1: "EA_ERR_SPEC", 2: "EA_ERR_SHAPE", 3: "EA_ERR_PARTITION", 4: "EA_ERR_DTYPE",
           5: "EA_ERR_ALLOC", 6: "EA_ERR_CUDA", 7: "EA_ERR_ARG", 8: "EA_ERR_UNSUPPORTED", 9: "EA_ERR_DEVICE",
           10: "EA_ERR_BOUNDS"}
+CACHE_FORMATS = {"bf16": 0, "e4m3": 1}
 
 
 class EaError(RuntimeError):
@@ -53,6 +54,18 @@ class AttnOpts(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("n_seq_ends", ctypes.c_int32),
                 ("reserved0", ctypes.c_int32), ("seq_ends", ctypes.c_void_p), ("m_out", ctypes.c_void_p),
                 ("l_out", ctypes.c_void_p), ("reserved", ctypes.c_int64 * 4)]
+
+
+class PageBatchArgs(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class CacheAttnOpts(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("m_out", ctypes.c_void_p),
+                ("l_out", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("reserved", ctypes.c_int64 * 4)]
 
 
 _lib = None
@@ -104,11 +117,23 @@ def lib():
         L.ea_selftest_wait_timeout.argtypes = [ctypes.c_int64, VP]
         L.ea_plan_check_exchange.argtypes = [P64, ctypes.c_int64, P64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]
         L.ea_attention_run.argtypes = [ctypes.c_char_p, VP, VP, VP, ctypes.POINTER(AttnOpts), VP, ctypes.POINTER(VP)]
+        L.ea_cache_create.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, VP,
+                                      VP, VP, VP, ctypes.POINTER(VP)]
+        L.ea_cache_destroy.argtypes = [VP]
+        L.ea_cache_append.argtypes = [VP, ctypes.POINTER(PageBatchArgs), VP, VP, VP]
+        L.ea_cache_read.argtypes = [VP, ctypes.POINTER(PageBatchArgs), VP, VP, VP]
+        L.ea_cache_attention_workspace.argtypes = [VP, ctypes.POINTER(PageBatchArgs), VP,
+                                                   ctypes.POINTER(ctypes.c_size_t)]
+        L.ea_cache_attention.argtypes = [VP, ctypes.POINTER(PageBatchArgs), VP, ctypes.POINTER(CacheAttnOpts), VP, VP]
+        L.ea_cache_check_batch.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(PageBatchArgs),
+                                           ctypes.c_int64, ctypes.c_int]
         for name in ("ea_check", "ea_plan_cache_clear", "ea_relation_create", "ea_relation_destroy",
                      "ea_relation_info", "ea_relation_block", "ea_relation_data", "ea_relation_bounds",
                      "ea_joinagg_run", "ea_exchange", "ea_plan_worklist", "ea_exchange_permutation",
                      "ea_overlay_atoms", "ea_last_plan", "ea_last_plan_cluster", "ea_exchange_noalloc", "ea_attention_run", "ea_exchange_agg",
-                     "ea_set_allocator", "ea_relation_copy_host", "ea_selftest_wait_timeout", "ea_plan_check_exchange"):
+                     "ea_set_allocator", "ea_relation_copy_host", "ea_selftest_wait_timeout", "ea_plan_check_exchange",
+                     "ea_cache_create", "ea_cache_destroy", "ea_cache_append", "ea_cache_read",
+                     "ea_cache_attention_workspace", "ea_cache_attention", "ea_cache_check_batch"):
             getattr(L, name).restype = ctypes.c_int
         if L.ea_abi_version() != 5:
             raise ImportError("libea.so ABI version mismatch")
@@ -169,7 +194,8 @@ def index_parts(parts: dict | None):
     return arr, len(parts), keep
 
 
-KERNEL_CLASS = {0: "exchange", 1: "elementwise", 2: "rowreduce", 3: "contract_simt", 4: "contract_tc", 5: "attention", 6: "exchange_agg"}
+KERNEL_CLASS = {0: "exchange", 1: "elementwise", 2: "rowreduce", 3: "contract_simt", 4: "contract_tc", 5: "attention", 6: "exchange_agg",
+                7: "cache_rows", 8: "cache_attention"}
 
 
 def last_plan():

@@ -24,6 +24,7 @@ enum DeviceErr : int {
     kDevTimeoutCorrection = 6,
     kDevTimeoutSelftest = 7,
     kDevTimeoutReduce = 8,
+    kDevBatch = 9,  // a batch of the paged cache out of range
 };
 
 // ---------------------------------------------------------------- exchange

@@ -1843,6 +1843,8 @@ ea_status ea_check(void *stream) {
     if (flag) {
         int zero = 0;
         cudaMemcpy(c->err, &zero, sizeof(int), cudaMemcpyHostToDevice);
+        if (flag == kDevBatch)
+            return set_error(EA_ERR_BOUNDS, "a batch of the paged cache named rows, positions or pages out of range");
         return set_error(EA_ERR_DEVICE, "a kernel raised device error %d (%s)", flag,
                          flag == kDevTimeoutProducer   ? "bounded wait ran out in the TMA producer"
                          : flag == kDevTimeoutMma      ? "bounded wait ran out in the MMA issuer"

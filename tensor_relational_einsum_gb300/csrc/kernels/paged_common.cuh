@@ -1,0 +1,48 @@
+// paged_common.cuh -- device helpers shared by the paged cache's kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "../paged.h"
+#include "dev_common.cuh"
+
+namespace ea {
+namespace pg {
+
+__device__ __forceinline__ void batch_fail(int *err) { atomicCAS(err, 0, (int)kDevBatch); }
+
+// Sequence i of the table; out of range: raises the error word, no rows.
+__device__ __forceinline__ PgSeq load_seq(const PgTable &t, int i, int page_log2, int *err) {
+    PgSeq s;
+    if (!pg_seq(__ldg(t.starts + i), __ldg(t.starts + i + 1), __ldg(t.lens + i), t.rows, t.max_new,
+                (int64_t)t.max_pages << page_log2, &s))
+        batch_fail(err);
+    return s;
+}
+
+// Page number x of sequence i.  Out of range: raises the error word and
+// names page 0, so that what follows stays inside the pool.
+__device__ __forceinline__ int32_t load_page(const PgTable &t, int64_t n_pages, int i, int x, int *err) {
+    const int32_t g = __ldg(t.pages + (int64_t)i * t.page_stride + x);
+    if (g >= 0 && g < n_pages) return g;
+    batch_fail(err);
+    return 0;
+}
+
+// The value of a scale byte: 2^(b - 127), NaN for 255.
+__device__ __forceinline__ float scale_value(uint32_t b) {
+    return b == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(b ? b << 23 : 0x00400000u);
+}
+
+// Scale byte of a vector whose largest magnitude has the fp32 bits `amax`:
+// the least e with |x| <= 448 * 2^e (448 = 1.75 * 2^8), kept in [-126, 120].
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+    if (amax >= 0x7f800000u) return 255u;  // an infinity or NaN
+    if (amax == 0u) return 127u;
+    const int e = (int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return (uint32_t)(max(-126, min(120, e)) + 127);
+}
+
+}  // namespace pg
+}  // namespace ea

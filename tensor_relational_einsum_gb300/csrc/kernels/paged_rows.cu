@@ -1,0 +1,228 @@
+// paged_rows.cu -- append to and read from the paged cache.
+//
+// One vector (a row's head, 64 or 128 values) is taken by D / 8 lanes, 8
+// values a lane: 16-byte loads and stores of bf16, two of them for fp32, 8
+// bytes for e4m3 codes.  Both operators move bytes and nothing else: the
+// bound is HBM, and for small calls the chain of dependent reads (sequence
+// bounds, page number) before a vector's address is known.  So
+//   - a thread takes the vectors of K and of V at the same place and asks
+//     for everything that does not depend on the table first;
+//   - the sequence bounds are staged in shared memory (one round trip for
+//     all of them) and searched there, not in global memory, where each of
+//     the log2(sequences) steps would wait for the last.
+// Quantising: the vector's largest magnitude over its lanes by shuffles on
+// the integer bits (an integer maximum orders fp32 magnitudes and puts
+// infinities and NaN on top), one power-of-two scale, codes rounded once by
+// the hardware conversion; the scaling itself is exact.
+#include "paged_common.cuh"
+
+namespace ea {
+namespace {
+
+using namespace pg;
+
+constexpr int kThreads = 256;
+constexpr int kStaged = 1024;  // sequence bounds staged in shared memory; longer batches are searched in global memory
+
+// The sequence that holds dense row r (starts[i] <= r < starts[i + 1]), or -1.
+__device__ __forceinline__ int find_seq(const int32_t *starts, int n_seqs, int32_t r) {
+    if (r < starts[0] || r >= starts[n_seqs]) return -1;
+    int a = 0, b = n_seqs - 1;  // the last i with starts[i] <= r
+    while (a < b) {
+        const int mid = (a + b + 1) >> 1;
+        if (starts[mid] <= r) a = mid;
+        else b = mid - 1;
+    }
+    return r < starts[a + 1] ? a : -1;
+}
+
+__device__ __forceinline__ void to_f32(const uint4 *raw, bool f32, float *x) {
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = __uint_as_float(reinterpret_cast<const uint32_t *>(raw)[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t w = reinterpret_cast<const uint32_t *>(raw)[i];
+            x[2 * i] = __uint_as_float(w << 16);
+            x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 to_bf16(const float *x) {
+    uint4 u;
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; i++) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    return u;
+}
+
+template <int D, bool F32, bool E4M3, bool READ>
+__global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_constant__ PgRows p) {
+    constexpr int LPV = D / 8;                // lanes of a vector
+    constexpr int VPB = kThreads / LPV;       // vectors of a pass
+    constexpr int U = 2;                      // passes of a CTA
+    constexpr int RAW = F32 ? 2 : 1;          // 16-byte words of a lane's dense values
+    __shared__ int32_t s_starts[kStaged + 1];
+    const int n_seqs = p.t.n_seqs;
+    const uint32_t total = (uint32_t)(p.t.rows * p.c.heads);
+    const int lane_v = threadIdx.x % LPV;
+    uint32_t vec[U];
+    uint4 kx[U][RAW], vx[U][RAW];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        vec[u] = (blockIdx.x * U + u) * VPB + threadIdx.x / LPV;
+        if (!READ && vec[u] < total) {
+            const int64_t at = ((int64_t)vec[u] * D + lane_v * 8) * (F32 ? 4 : 2);
+#pragma unroll
+            for (int i = 0; i < RAW; i++) {
+                kx[u][i] = __ldg(reinterpret_cast<const uint4 *>(p.k + at) + i);
+                vx[u][i] = __ldg(reinterpret_cast<const uint4 *>(p.v + at) + i);
+            }
+        }
+    }
+    const bool staged = n_seqs <= kStaged;
+    if (staged) {
+        for (int i = threadIdx.x; i <= n_seqs; i += kThreads) s_starts[i] = __ldg(p.t.starts + i);
+        __syncthreads();
+    }
+    const int32_t *starts = staged ? s_starts : p.t.starts;
+    // slot of each vector in the pool (-1: none), then the cells
+    int64_t cell[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        cell[u] = -1;
+        if (vec[u] >= total) continue;
+        const uint32_t row = vec[u] / (uint32_t)p.c.heads, head = vec[u] - row * (uint32_t)p.c.heads;
+        const int i = find_seq(starts, n_seqs, (int32_t)row);
+        if (i < 0) continue;
+        const PgSeq s = load_seq(p.t, i, p.c.page_log2, p.err);
+        if (s.n == 0) continue;
+        const int pos = s.len - s.n + ((int)row - s.first);
+        if (s.n > s.len || pos < 0) {
+            batch_fail(p.err);
+            continue;
+        }
+        const int32_t g = __ldg(p.t.pages + (int64_t)i * p.t.page_stride + (pos >> p.c.page_log2));
+        if (g < 0 || g >= p.c.n_pages) {
+            batch_fail(p.err);
+            continue;
+        }
+        cell[u] = pg_vec(p.c, g, (int)head, pos & ((1 << p.c.page_log2) - 1));
+    }
+    if constexpr (!READ) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+#pragma unroll
+            for (int w = 0; w < 2; w++) {  // K, then V; the shuffles need every lane of the vector
+                const uint4 *raw = w ? vx[u] : kx[u];
+                char *pool = w ? p.c.v : p.c.k;
+                if constexpr (!E4M3) {
+                    uint4 out = raw[0];
+                    if constexpr (F32) {
+                        float x[8];
+                        to_f32(raw, true, x);
+                        out = to_bf16(x);
+                    }
+                    if (cell[u] >= 0) *reinterpret_cast<uint4 *>(pool + (cell[u] * D + lane_v * 8) * 2) = out;
+                } else {
+                    float x[8];
+                    to_f32(raw, F32, x);
+                    uint32_t amax = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+                    for (int o = LPV / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    const uint32_t b = scale_byte(amax);
+                    // 2^-(b - 127): normal for every b that scale_byte makes; 0 where the vector is NaN
+                    const float inv = b == 255u ? 0.f : __uint_as_float((254u - b) << 23);
+                    uint32_t code[2];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv),
+                                                                    __NV_SATFINITE, __NV_E4M3);
+                        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv),
+                                                                    __NV_SATFINITE, __NV_E4M3);
+                        code[i] = lo | (hi << 16);
+                    }
+                    if (b == 255u) code[0] = code[1] = 0u;
+                    if (cell[u] >= 0) {
+                        *reinterpret_cast<uint2 *>(pool + cell[u] * D + lane_v * 8) = make_uint2(code[0], code[1]);
+                        if (lane_v == 0) (w ? p.c.vs : p.c.ks)[cell[u]] = (uint8_t)b;
+                    }
+                }
+            }
+        }
+    } else {
+        uint2 kc[U], vc[U];
+        uint32_t kb[U], vb[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (cell[u] < 0) continue;
+            if constexpr (E4M3) {
+                kc[u] = __ldg(reinterpret_cast<const uint2 *>(p.c.k + cell[u] * D + lane_v * 8));
+                vc[u] = __ldg(reinterpret_cast<const uint2 *>(p.c.v + cell[u] * D + lane_v * 8));
+                kb[u] = __ldg(p.c.ks + cell[u]);
+                vb[u] = __ldg(p.c.vs + cell[u]);
+            } else {
+                kx[u][0] = __ldg(reinterpret_cast<const uint4 *>(p.c.k + (cell[u] * D + lane_v * 8) * 2));
+                vx[u][0] = __ldg(reinterpret_cast<const uint4 *>(p.c.v + (cell[u] * D + lane_v * 8) * 2));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (cell[u] < 0) continue;
+#pragma unroll
+            for (int w = 0; w < 2; w++) {
+                char *dst = (w ? p.v : p.k) + ((int64_t)vec[u] * D + lane_v * 8) * (F32 ? 4 : 2);
+                float x[8];
+                if constexpr (E4M3) {
+                    const uint2 c = w ? vc[u] : kc[u];
+                    const float sc = scale_value(w ? vb[u] : kb[u]);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint32_t two = (i < 2 ? c.x : c.y) >> (16 * (i & 1));
+                        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
+                        const float2 f = __half22float2(h);
+                        x[2 * i] = f.x * sc;
+                        x[2 * i + 1] = f.y * sc;
+                    }
+                } else {
+                    to_f32(w ? vx[u] : kx[u], false, x);
+                }
+                if constexpr (F32) {
+                    reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+                    reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+                } else if constexpr (E4M3) {
+                    *reinterpret_cast<uint4 *>(dst) = to_bf16(x);
+                } else {
+                    *reinterpret_cast<uint4 *>(dst) = w ? vx[u][0] : kx[u][0];
+                }
+            }
+        }
+    }
+}
+
+template <int D, bool F32, bool E4M3>
+cudaError_t launch(const PgRows &p, int64_t *ctas, cudaStream_t st) {
+    constexpr int per = 2 * kThreads / (D / 8);  // vectors of a CTA
+    *ctas = (p.t.rows * p.c.heads + per - 1) / per;
+    if (p.read) cache_rows_kernel<D, F32, E4M3, true><<<(unsigned)*ctas, kThreads, 0, st>>>(p);
+    else cache_rows_kernel<D, F32, E4M3, false><<<(unsigned)*ctas, kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_rows(const PgRows &p, int64_t *ctas, cudaStream_t st) {
+    const bool e4m3 = p.c.fmt == EA_CACHE_E4M3;
+    if (p.c.dim == 64) {
+        if (p.f32) return e4m3 ? launch<64, true, true>(p, ctas, st) : launch<64, true, false>(p, ctas, st);
+        return e4m3 ? launch<64, false, true>(p, ctas, st) : launch<64, false, false>(p, ctas, st);
+    }
+    if (p.f32) return e4m3 ? launch<128, true, true>(p, ctas, st) : launch<128, true, false>(p, ctas, st);
+    return e4m3 ? launch<128, false, true>(p, ctas, st) : launch<128, false, false>(p, ctas, st);
+}
+
+}  // namespace ea

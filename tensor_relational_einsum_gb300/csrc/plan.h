@@ -38,7 +38,7 @@ struct Blob {
     }
 };
 
-enum PlanKind { kExchange = 0, kEwise, kRowReduce, kSimt, kTc, kAttn, kExchangeAgg };
+enum PlanKind { kExchange = 0, kEwise, kRowReduce, kSimt, kTc, kAttn, kExchangeAgg, kCacheRows, kCacheAttention };
 
 struct DevPlan {
     int kind = 0;
