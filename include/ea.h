@@ -489,6 +489,18 @@ ea_status ea_cache_attention_workspace(ea_cache cache, const ea_page_batch *batc
 ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *batch, ea_relation q, const ea_cache_attn_opts *opts,
                              void *stream, ea_relation out);
 
+/* The work list of the attention, computed on the host by the code that the
+ * kernels run (no GPU needed): `batch` holds HOST pointers; split = {heads,
+ * query heads of one, tokens of an item, keys of a unit, causal, least and
+ * most rows (tokens x query heads of one) of the sequences served}.  A
+ * sequence's items are its tokens in runs, for each head; an item has as
+ * many units as its last token keeps keys for (at least one), and each of
+ * `ctas` CTAs takes an equal run of all units.  parts[7 * i ..] = {CTA,
+ * sequence, head, item, first unit, unit beyond the last, units of the item},
+ * in order.  EA_ERR_ARG when more than `capacity` parts are needed. */
+ea_status ea_cache_attention_split(const ea_page_batch *batch, int32_t page, int64_t rows, const int32_t *split,
+                                   int32_t ctas, int64_t capacity, int64_t *parts, int64_t *n_parts);
+
 /* The check of a batch on the host (no GPU needed): `batch` holds HOST
  * pointers, rows is the dense row count, write nonzero checks for an append
  * (positions >= 0, no slot named twice).  EA_OK, or EA_ERR_BOUNDS with a

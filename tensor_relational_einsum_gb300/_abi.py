@@ -127,13 +127,16 @@ def lib():
         L.ea_cache_attention.argtypes = [VP, ctypes.POINTER(PageBatchArgs), VP, ctypes.POINTER(CacheAttnOpts), VP, VP]
         L.ea_cache_check_batch.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(PageBatchArgs),
                                            ctypes.c_int64, ctypes.c_int]
+        L.ea_cache_attention_split.argtypes = [ctypes.POINTER(PageBatchArgs), ctypes.c_int32, ctypes.c_int64, P32,
+                                               ctypes.c_int32, ctypes.c_int64, P64, P64]
         for name in ("ea_check", "ea_plan_cache_clear", "ea_relation_create", "ea_relation_destroy",
                      "ea_relation_info", "ea_relation_block", "ea_relation_data", "ea_relation_bounds",
                      "ea_joinagg_run", "ea_exchange", "ea_plan_worklist", "ea_exchange_permutation",
                      "ea_overlay_atoms", "ea_last_plan", "ea_last_plan_cluster", "ea_exchange_noalloc", "ea_attention_run", "ea_exchange_agg",
                      "ea_set_allocator", "ea_relation_copy_host", "ea_selftest_wait_timeout", "ea_plan_check_exchange",
                      "ea_cache_create", "ea_cache_destroy", "ea_cache_append", "ea_cache_read",
-                     "ea_cache_attention_workspace", "ea_cache_attention", "ea_cache_check_batch"):
+                     "ea_cache_attention_workspace", "ea_cache_attention", "ea_cache_check_batch",
+                     "ea_cache_attention_split"):
             getattr(L, name).restype = ctypes.c_int
         if L.ea_abi_version() != 5:
             raise ImportError("libea.so ABI version mismatch")

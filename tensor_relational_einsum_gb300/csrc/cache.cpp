@@ -186,6 +186,9 @@ extern "C" ea_status ea_cache_create(ea_cache_format format, int64_t pages, int3
         if (e != cudaSuccess) {
             cudaGetLastError();  // no device: the handle serves the host checks only
             c.device = -1;
+        } else {
+            e = cudaDeviceGetAttribute(&c.num_sms, cudaDevAttrMultiProcessorCount, c.device);
+            if (e != cudaSuccess) return cuda_error(e, "cudaDeviceGetAttribute");
         }
         *out = new ea_cache_s(c);
         return EA_OK;
@@ -225,6 +228,25 @@ ea_status attn_shape(ea_cache cache, const ea_page_batch *batch, ea_relation q, 
     return batch_args(batch, cache->page, *rows);
 }
 
+// The kernels of a call.  Sequences with few rows and the others are served
+// by kernels of their own, each leaving out the other's sequences; a kernel
+// that max_new rules out is not launched.
+struct AttnPlans {
+    PgPlan tokens;
+    bool chunks;    // sequences with more rows than the token kernel takes are possible
+    size_t bytes;
+};
+
+AttnPlans plans_of(const ea_cache_s *cache, const ea_page_batch *batch, int64_t rows, int64_t heads, int causal) {
+    AttnPlans a{};
+    const PgTable t = table_of(batch, rows);
+    const int group = (int)(heads / cache->heads);
+    a.tokens = plan_cache_tokens(t, pool_of(cache), group, causal, cache->num_sms);
+    a.chunks = (int64_t)t.max_new * group > (a.tokens.ctas ? a.tokens.split.max_rows : 0);
+    a.bytes = a.tokens.bytes;
+    return a;
+}
+
 }  // namespace
 }  // namespace ea
 
@@ -234,7 +256,7 @@ extern "C" ea_status ea_cache_attention_workspace(ea_cache cache, const ea_page_
         int64_t rows, heads;
         ea_status s = attn_shape(cache, batch, q, &rows, &heads);
         if (s) return s;
-        *bytes = 0;
+        *bytes = plans_of(cache, batch, rows, heads, 1).bytes;
         return EA_OK;
     });
 }
@@ -290,12 +312,65 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
         p.scale = o.scale == 0.0f ? (float)(1.0 / std::sqrt((double)cache->dim)) : o.scale;
         p.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
         p.err = c->err;
+        const AttnPlans a = plans_of(cache, batch, rows, heads, p.causal);
+        if (a.bytes > 0 && (!o.workspace || o.workspace_bytes < a.bytes || ((uintptr_t)o.workspace & 15) != 0))
+            return set_error(EA_ERR_ARG, "ea_cache_attention: workspace of %zu bytes, 16-byte aligned, needed", a.bytes);
         int64_t ctas = 0;
-        if (rows > 0) {
-            cudaError_t e = launch_cache_attention(p, &ctas, (cudaStream_t)stream);
+        int launches = 0;
+        if (a.tokens.ctas > 0) {
+            cudaError_t e = launch_cache_tokens(p, a.tokens, o.workspace, (cudaStream_t)stream);
             if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
+            ctas += a.tokens.ctas;
+            launches += 1;
         }
-        note_launch(kCacheAttention, ctas > 0, ctas);
+        if (rows > 0 && a.chunks) {
+            int64_t n = 0;
+            cudaError_t e = launch_cache_attention(p, &n, (cudaStream_t)stream, a.tokens.ctas ? a.tokens.split.max_rows + 1 : 0);
+            if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
+            ctas += n;
+            launches += 1;
+        }
+        note_launch(kCacheAttention, launches, ctas);
+        return EA_OK;
+    });
+}
+
+extern "C" ea_status ea_cache_attention_split(const ea_page_batch *batch, int32_t page, int64_t rows, const int32_t *split,
+                                              int32_t ctas, int64_t capacity, int64_t *parts, int64_t *n_parts) {
+    return entry([&]() -> ea_status {
+        if (!split || !parts || !n_parts || ctas < 1 || page < 1) return set_error(EA_ERR_ARG, "ea_cache_attention_split: arguments");
+        ea_status s = batch_args(batch, page, rows);
+        if (s) return s;
+        const PgTable t = table_of(batch, rows);
+        const PgSplit sp{split[0], split[1], split[2], split[3], split[4], split[5], split[6]};
+        if (sp.heads < 1 || sp.group < 1 || sp.tok < 1 || sp.kt < 1) return set_error(EA_ERR_ARG, "ea_cache_attention_split: split");
+        std::vector<PgSeq> seqs(t.n_seqs);
+        std::vector<int64_t> first(t.n_seqs + 1, 0);
+        for (int i = 0; i < t.n_seqs; i++) {
+            pg_seq(t.starts[i], t.starts[i + 1], t.lens[i], rows, t.max_new, (int64_t)t.max_pages * page, &seqs[i]);
+            first[i + 1] = first[i] + pg_seq_units(seqs[i], sp);
+        }
+        struct {
+            const std::vector<PgSeq> &v;
+            PgSeq operator()(int i) const { return v[i]; }
+            int count() const { return (int)v.size(); }
+        } get{seqs};
+        PgShare sh{};
+        sh.total = first[t.n_seqs];
+        sh.parts = pg_parts(sh.total, ctas);
+        *n_parts = 0;
+        for (int x = 0; x < sh.parts; x++) {
+            sh.w0 = pg_first(sh.total, sh.parts, x);
+            sh.count = pg_first(sh.total, sh.parts, x + 1) - sh.w0;
+            sh.seq = (int32_t)(std::upper_bound(first.begin(), first.end(), sh.w0) - first.begin()) - 1;
+            sh.off = sh.w0 - first[sh.seq];
+            PgWalk w;
+            for (w.begin(sh, sp, get); w.left > 0; w.step(w.part(), sp, get)) {
+                if (*n_parts == capacity) return set_error(EA_ERR_ARG, "ea_cache_attention_split: capacity");
+                const int64_t row[7] = {x, w.seq, w.head, w.item, w.u0, w.u0 + w.part(), w.units};
+                std::copy(row, row + 7, parts + 7 * (*n_parts)++);
+            }
+        }
         return EA_OK;
     });
 }

@@ -20,7 +20,7 @@ __device__ __forceinline__ float cell(const PgPool &c, const char *pool, const u
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(128) plain_kernel(const __grid_constant__ PgAttn p) {
+__global__ void __launch_bounds__(128) plain_kernel(const __grid_constant__ PgAttn p, int min_rows) {
     __shared__ float s_q[4][D];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t at = (int64_t)blockIdx.x * 4 + warp;
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(128) plain_kernel(const __grid_constant__ PgAt
         else b = mid - 1;
     }
     const PgSeq s = load_seq(p.t, a, p.c.page_log2, p.err);
-    if (row < s.first || row >= s.first + s.n) return;
+    if (row < s.first || row >= s.first + s.n || (int64_t)s.n * p.group < min_rows) return;
     const int pos = s.len - s.n + (row - s.first);
     const int end = p.causal ? min(s.len, pos + 1) : s.len;
     const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(p.q) + at * D;
@@ -75,16 +75,16 @@ __global__ void __launch_bounds__(128) plain_kernel(const __grid_constant__ PgAt
 
 }  // namespace
 
-cudaError_t launch_cache_attention(const PgAttn &p, int64_t *ctas, cudaStream_t st) {
+cudaError_t launch_cache_attention(const PgAttn &p, int64_t *ctas, cudaStream_t st, int min_rows) {
     *ctas = (p.t.rows * p.qheads + 3) / 4;
     const unsigned n = (unsigned)*ctas;
     const bool e4m3 = p.c.fmt == EA_CACHE_E4M3;
     if (p.c.dim == 64) {
-        if (e4m3) plain_kernel<64, true><<<n, 128, 0, st>>>(p);
-        else plain_kernel<64, false><<<n, 128, 0, st>>>(p);
+        if (e4m3) plain_kernel<64, true><<<n, 128, 0, st>>>(p, min_rows);
+        else plain_kernel<64, false><<<n, 128, 0, st>>>(p, min_rows);
     } else {
-        if (e4m3) plain_kernel<128, true><<<n, 128, 0, st>>>(p);
-        else plain_kernel<128, false><<<n, 128, 0, st>>>(p);
+        if (e4m3) plain_kernel<128, true><<<n, 128, 0, st>>>(p, min_rows);
+        else plain_kernel<128, false><<<n, 128, 0, st>>>(p, min_rows);
     }
     return cudaGetLastError();
 }

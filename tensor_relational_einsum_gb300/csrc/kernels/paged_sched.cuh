@@ -1,0 +1,97 @@
+// paged_sched.cuh -- a CTA's share of the attention's work list, and the
+// walk over it.  The batch's lengths are known on the device only, so every
+// CTA sums the units of all sequences (a block-wide scan, a thread a
+// sequence), takes its equal share and finds the sequence it begins in.
+#pragma once
+
+#include "paged_common.cuh"
+
+namespace ea {
+namespace pg {
+
+// NT threads, all of them; scratch: NT / 32 + 1 words of shared memory.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t u, int64_t *incl, int64_t *scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, u, o);
+        if (lane >= o) u += x;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = u;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; w++) {
+        const int64_t x = scratch[w];
+        if (w < warp) before += x;
+        all += x;
+    }
+    *incl = u + before;
+    return all;
+}
+
+template <int NT>
+__device__ __forceinline__ void take_share(const PgTable &t, const PgSplit &sp, int page_log2, int *err, int64_t *scratch,
+                                           PgShare *out) {
+    int64_t u = 0, incl, total = 0;
+    for (int base = 0; base < t.n_seqs; base += NT) {
+        const int i = base + threadIdx.x;
+        u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, page_log2, err), sp) : 0;
+        total += block_scan<NT>(u, &incl, scratch);
+    }
+    const int parts = pg_parts(total, gridDim.x), x = blockIdx.x;
+    const bool any = x < parts;
+    const int64_t w0 = any ? pg_first(total, parts, x) : 0;
+    if (threadIdx.x == 0) {
+        out->w0 = w0;
+        out->total = total;
+        out->parts = parts;
+        out->count = any ? pg_first(total, parts, x + 1) - w0 : 0;
+        out->seq = 0;
+        out->off = 0;
+    }
+    __syncthreads();
+    int64_t run = 0;
+    for (int base = 0; any && base < t.n_seqs; base += NT) {
+        if (t.n_seqs > NT) {
+            const int i = base + threadIdx.x;
+            u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, page_log2, err), sp) : 0;
+            total = block_scan<NT>(u, &incl, scratch);
+        }
+        if (u > 0 && run + incl - u <= w0 && w0 < run + incl) {
+            out->seq = base + threadIdx.x;
+            out->off = w0 - (run + incl - u);
+        }
+        run += total;
+    }
+    __syncthreads();
+}
+
+// Sequences of the batch for a PgWalk.
+struct Seqs {
+    const PgTable &t;
+    int page_log2;
+    int *err;
+    __device__ __forceinline__ PgSeq operator()(int i) const { return load_seq(t, i, page_log2, err); }
+    __device__ __forceinline__ int count() const { return t.n_seqs; }
+};
+
+// Say where this CTA's share begins, if that is inside an item.
+__device__ __forceinline__ void note_cut(const PgWork &w, const PgShare &sh, const PgWalk &k) {
+    PgCut c{};
+    c.total = sh.total;
+    c.parts = sh.parts;
+    if (sh.count > 0 && k.u0 > 0) {
+        c.wi = sh.w0 - k.u0;
+        c.we = c.wi + k.units;
+        c.seq = k.seq;
+        c.head = k.head;
+        c.item = k.item;
+    }
+    w.cut[blockIdx.x] = c;
+}
+
+}  // namespace pg
+}  // namespace ea

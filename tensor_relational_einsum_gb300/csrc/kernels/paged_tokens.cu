@@ -1,0 +1,529 @@
+// paged_tokens.cu -- attention over the paged cache for sequences with few
+// query rows (tokens x grouped heads <= 32 to a key-value head): single
+// tokens and short chunks.
+//
+// Every cached cell is used for at most 32 rows, so reading the pages bounds
+// the kernel: 2 bytes (1 byte) of a cell against 64 flops, an eighth of what
+// the tensor cores could do meanwhile.  What it needs is bytes in flight on
+// every SM all the time, so
+//   - the units of all items (64 keys of one key-value head) are shared out
+//     evenly over the CTAs, whatever the lengths are (paged.h);
+//   - a warp owns 16 keys of each 64-key block and loads them itself with
+//     16-byte cp.async into its part of a ring of blocks: no barrier between
+//     warps inside an item, the next blocks' loads run across items;
+//   - 16 keys lie in one page (pages hold a multiple of 16 positions), so a
+//     warp needs one page number a block, read one block ahead.
+// The products run on mma.sync m16n8k16: its 16-row tile is what a group of
+// heads fills (a tcgen05 tile has 128 rows), and the accumulators stay in the
+// warp's registers, next to the softmax.  The rows of an item are its tokens
+// times its heads, token-major; each warp keeps its own running maximum, sum
+// and output over its keys (the merge of (m, l, A) triples is associative),
+// and the four are merged through shared memory at the end of a part.
+//
+// 8-bit cells become bf16 in registers: sign and the 7 other bits moved to
+// bf16's places give value * 2^-120 (exponent biases 7 and 127; subnormals
+// too), one exact product with 2^120 puts that right.  The bytes of a 32-bit
+// word go to the fragments as pairs (0, 2) and (1, 3), the pairs that masks
+// and shifts give without a byte permutation: for the scores that is a fixed
+// order of the contracted dimension, applied to Q once; for the output it
+// only says which column an accumulator holds.  K's scales multiply the
+// scores' columns, V's the probabilities, both exact powers of two.
+#include "attn_common.cuh"
+#include "paged_sched.cuh"
+
+namespace ea {
+namespace {
+
+using namespace pg;
+using attn::ex2;
+using attn::pack_bf16;
+
+constexpr int kThreads = 128;
+constexpr int kBlock = 64;     // keys of a block: 16 a warp
+constexpr float kLazy = 8.f;   // a running maximum moves when it is exceeded by this much (log2): P stays below 2^8
+
+template <int D, bool E4M3, int MT>
+struct Cfg {
+    static constexpr int CELL = E4M3 ? 1 : 2;
+    static constexpr int ROWB = D * CELL;               // bytes of a key's vector
+    static constexpr int TILE = 16 * ROWB;              // a warp's K (or V) of a block
+    static constexpr int STAGE = 4 * 2 * TILE;          // a block
+    static constexpr int S = E4M3 ? 4 : D == 64 ? 5 : 3;
+    static constexpr int SCALES = E4M3 ? S * 4 * 32 : 0;  // 16 bytes of K and of V a warp and stage
+    static constexpr int SMEM = S * STAGE + SCALES;
+    static constexpr int CTAS = 2;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on) {
+    const int n = on ? 16 : 0;  // 0: the 16 bytes become zero, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Bytes 1 and 3 of w, e4m3, as two bf16 values.
+__device__ __forceinline__ uint32_t odd_bf16(uint32_t w) {
+    const uint32_t y = ((w & 0x7f007f00u) >> 4) | (w & 0x80008000u);
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));  // 2^120
+    return r;
+}
+// Bytes 0 and 2.
+__device__ __forceinline__ uint32_t even_bf16(uint32_t w) { return odd_bf16(w << 8); }
+
+// Byte offset of 16-byte chunk c of row r in a warp's tile.  bf16, and V's
+// 8-bit cells: ldmatrix reads one chunk of 8 rows, which must lie in 8
+// different 16-byte columns of 128 bytes.  K's 8-bit cells: 8 lanes read 4
+// chunks of 2 rows.
+template <int ROWB, bool K8>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+    if constexpr (K8) return r * ROWB + ((ROWB == 128 ? c ^ ((r & 1) << 2) : c) << 4);
+    else if constexpr (ROWB >= 128) return r * ROWB + ((c ^ (r & 7)) << 4);
+    else return r * ROWB + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// The loads of a warp's keys, block after block of the CTA's share.
+template <int D, bool E4M3, int MT>
+struct Loader {
+    using C = Cfg<D, E4M3, MT>;
+    PgWalk w;
+    int block, last;  // next block of the part, and its first one beyond
+    int end;          // keys of the item
+    int page;         // page of this warp's keys of the next block
+    bool more;
+
+    __device__ __forceinline__ void enter(const PgAttn &p, const PgSplit &sp, int warp) {
+        const int per = sp.kt / kBlock;
+        while (w.left > 0) {
+            end = pg_item_end(w.s, sp, w.item);
+            block = w.u0 * per;
+            last = min((w.u0 + w.part()) * per, (end + kBlock - 1) / kBlock);
+            if (block < last) break;
+            w.step(w.part(), sp, Seqs{p.t, p.c.page_log2, p.err});
+        }
+        more = w.left > 0;
+        look(p, warp);
+    }
+    __device__ __forceinline__ void look(const PgAttn &p, int warp) {
+        const int key0 = block * kBlock + warp * 16;
+        page = more && key0 < end ? load_page(p.t, p.c.n_pages, w.seq, key0 >> p.c.page_log2, p.err) : 0;
+    }
+    __device__ __forceinline__ void issue(const PgAttn &p, const PgSplit &sp, uint32_t stage, uint32_t scales, int warp,
+                                          int lane) {
+        if (!more) return;
+        const int key0 = block * kBlock + warp * 16, nv = end - key0;  // valid keys: the rest becomes zero
+        if (nv > 0) {
+            const int64_t vec = pg_vec(p.c, page, w.head, key0 & ((1 << p.c.page_log2) - 1));
+            const uint32_t ks = stage + warp * 2 * C::TILE, vs = ks + C::TILE;
+            const char *kp = p.c.k + vec * C::ROWB, *vp = p.c.v + vec * C::ROWB;
+            constexpr int CPR = C::ROWB / 16;  // chunks of a row
+#pragma unroll
+            for (int i = 0; i < C::TILE / 512; i++) {
+                const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
+                cp16(ks + chunk_at<C::ROWB, E4M3>(r, c), kp + x * 16, r < nv);
+            }
+#pragma unroll
+            for (int i = 0; i < C::TILE / 512; i++) {
+                const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
+                cp16(vs + chunk_at<C::ROWB, false>(r, c), vp + x * 16, r < nv);
+            }
+            if (E4M3 && lane < 2) cp16(scales + warp * 32 + lane * 16, (lane ? p.c.vs : p.c.ks) + vec, true);
+        }
+        if (++block < last) {
+            look(p, warp);
+        } else {
+            w.step(w.part(), sp, Seqs{p.t, p.c.page_log2, p.err});
+            enter(p, sp, warp);
+        }
+    }
+};
+
+template <int D, bool E4M3, int MT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, E4M3, MT>::CTAS)
+cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgSplit sp,
+                    const __grid_constant__ PgWork ws) {
+    using C = Cfg<D, E4M3, MT>;
+    constexpr int KS = D / 16, NT = D / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ PgShare share;
+    __shared__ int64_t scan[kThreads / 32];
+    __shared__ float4 s_ml[4][16 * MT];  // a warp's reference maximum, sum, maximum of its rows
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+    take_share<kThreads>(p.t, sp, p.c.page_log2, p.err, scan, &share);
+    Loader<D, E4M3, MT> ld;
+    ld.w.begin(share, sp, Seqs{p.t, p.c.page_log2, p.err});
+    PgWalk w = ld.w;
+    if (threadIdx.x == 0) note_cut(ws, share, w);
+    if (share.count == 0) return;
+    ld.enter(p, sp, warp);
+#pragma unroll
+    for (int s = 0; s < C::S - 1; s++) {
+        ld.issue(p, sp, base + s * C::STAGE, base + C::S * C::STAGE + s * 128, warp, lane);
+        cp_commit();
+    }
+    int slot = 0;  // ring slot of the next block to compute
+    bool first_part = true;
+    const float c = p.scale_log2;
+    const int per = sp.kt / kBlock;
+
+    while (w.left > 0) {
+        const int np = w.part();
+        const int end = pg_item_end(w.s, sp, w.item);
+        const int b0 = w.u0 * per, b1 = min((w.u0 + np) * per, (end + kBlock - 1) / kBlock);
+        const int tok0 = w.item * sp.tok, nrows = min(sp.tok, w.s.n - tok0) * sp.group;
+        // Q's fragments, and the keys that each of the thread's rows keeps
+        uint32_t q[MT][KS][4];
+        int lim[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int r = m * 16 + h * 8 + gid, tok = tok0 + r / sp.group;
+                const bool in = r < nrows;
+                lim[m][h] = !in ? 0 : sp.causal ? max(0, min(w.s.len, w.s.len - w.s.n + tok + 1)) : w.s.len;
+                const char *src = p.q + ((int64_t)(w.s.first + (in ? tok : 0)) * p.qheads + w.head * sp.group +
+                                         (in ? r % sp.group : 0)) * D * 2;
+                if constexpr (E4M3) {
+                    // logical k = (2 t, 2 t + 1, 2 t + 8, 2 t + 9) of step 4 x + s: columns 64 x + 16 t + 4 s + (0, 2, 1, 3)
+#pragma unroll
+                    for (int x = 0; x < D / 64; x++) {
+                        uint4 v[2] = {};
+                        if (in) {
+                            v[0] = __ldg(reinterpret_cast<const uint4 *>(src + (64 * x + 16 * tig) * 2));
+                            v[1] = __ldg(reinterpret_cast<const uint4 *>(src + (64 * x + 16 * tig) * 2) + 1);
+                        }
+                        const uint32_t *u = reinterpret_cast<const uint32_t *>(v);
+#pragma unroll
+                        for (int s = 0; s < 4; s++) {
+                            q[m][4 * x + s][h] = __byte_perm(u[2 * s], u[2 * s + 1], 0x5410);
+                            q[m][4 * x + s][h + 2] = __byte_perm(u[2 * s], u[2 * s + 1], 0x7632);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < KS; s++)
+#pragma unroll
+                        for (int x = 0; x < 2; x++)
+                            q[m][s][h + 2 * x] = in ? __ldg(reinterpret_cast<const uint32_t *>(src + (16 * s + 8 * x + 2 * tig) * 2)) : 0u;
+                }
+            }
+        float o[MT][NT][4] = {};
+        float mref[MT][2], mmax[MT][2], l[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                mref[m][h] = mmax[m][h] = -INFINITY;
+                l[m][h] = 0.f;
+            }
+
+        for (int b = b0; b < b1; b++) {
+            __syncwarp();  // every lane has read the slot that is filled next
+            const int fill = slot == 0 ? C::S - 1 : slot - 1;
+            ld.issue(p, sp, base + fill * C::STAGE, base + C::S * C::STAGE + fill * 128, warp, lane);
+            cp_commit();
+            cp_wait<C::S - 1>();
+            __syncwarp();
+            const int key0 = b * kBlock + warp * 16;
+            if (key0 < end) {
+                const uint32_t kt = base + slot * C::STAGE + warp * 2 * C::TILE, vt = kt + C::TILE;
+                float s[MT][2][4] = {};
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int x = 0; x < D / 64; x++)
+#pragma unroll
+                        for (int n = 0; n < 2; n++) {
+                            uint32_t u[4];
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                                         : "r"(kt + chunk_at<C::ROWB, true>(n * 8 + gid, 4 * x + tig)));
+#pragma unroll
+                            for (int y = 0; y < 4; y++) {
+                                const uint32_t e = even_bf16(u[y]), d = odd_bf16(u[y]);
+#pragma unroll
+                                for (int m = 0; m < MT; m++) mma(s[m][n], q[m][4 * x + y], e, d);
+                            }
+                        }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < KS; x++) {
+                        uint32_t u[4];
+                        ldsm4(kt + chunk_at<C::ROWB, false>((lane >> 4) * 8 + (lane & 7), 2 * x + ((lane >> 3) & 1)), u);
+#pragma unroll
+                        for (int m = 0; m < MT; m++) {
+                            mma(s[m][0], q[m][x], u[0], u[1]);
+                            mma(s[m][1], q[m][x], u[2], u[3]);
+                        }
+                    }
+                }
+                float vsc[2][2];
+                if constexpr (E4M3) {
+                    const uint8_t *sc = smem + C::S * C::STAGE + slot * 128 + warp * 32;
+#pragma unroll
+                    for (int n = 0; n < 2; n++) {
+                        const uint32_t kb = *reinterpret_cast<const uint16_t *>(sc + n * 8 + 2 * tig);
+                        const uint32_t vb = *reinterpret_cast<const uint16_t *>(sc + 16 + n * 8 + 2 * tig);
+                        const float k0 = scale_value(kb & 255u), k1 = scale_value(kb >> 8);
+                        vsc[n][0] = scale_value(vb & 255u);
+                        vsc[n][1] = scale_value(vb >> 8);
+#pragma unroll
+                        for (int m = 0; m < MT; m++)
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+                                s[m][n][2 * h] *= k0;
+                                s[m][n][2 * h + 1] *= k1;
+                            }
+                    }
+                }
+                uint32_t pf[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; m++) {
+                    float mx[2];
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int keep = lim[m][h] - key0 - 2 * tig;  // of the thread's keys 0, 1, 8, 9
+#pragma unroll
+                        for (int n = 0; n < 2; n++)
+#pragma unroll
+                            for (int e = 0; e < 2; e++)
+                                if (n * 8 + e >= keep) s[m][n][2 * h + e] = -INFINITY;
+                        mx[h] = fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]), fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1]));
+                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                        mmax[m][h] = fmaxf(mmax[m][h], mx[h]);
+                    }
+                    bool move = false;
+#pragma unroll
+                    for (int h = 0; h < 2; h++)
+                        move |= mx[h] != -INFINITY && (mref[m][h] == -INFINITY || (mx[h] - mref[m][h]) * c > kLazy);
+                    if (__any_sync(0xffffffffu, move)) {
+                        float f[2];
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const float to = mmax[m][h];
+                            f[h] = mref[m][h] == -INFINITY ? 0.f : ex2((mref[m][h] - to) * c);
+                            mref[m][h] = to;
+                            l[m][h] *= f[h];
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; n++) {
+                            o[m][n][0] *= f[0];
+                            o[m][n][1] *= f[0];
+                            o[m][n][2] *= f[1];
+                            o[m][n][3] *= f[1];
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const float nb = mref[m][h] == -INFINITY ? 0.f : -mref[m][h] * c;
+                        float e[2][2];
+#pragma unroll
+                        for (int n = 0; n < 2; n++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++) e[n][i] = ex2(fmaf(s[m][n][2 * h + i], c, nb));
+                        l[m][h] += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
+                        if constexpr (E4M3) {
+#pragma unroll
+                            for (int n = 0; n < 2; n++)
+#pragma unroll
+                                for (int i = 0; i < 2; i++)  // a dropped key's scale byte may hold anything
+                                    e[n][i] = e[n][i] == 0.f ? 0.f : e[n][i] * vsc[n][i];
+                        }
+                        pf[m][h] = pack_bf16(e[0][0], e[0][1]);
+                        pf[m][h + 2] = pack_bf16(e[1][0], e[1][1]);
+                    }
+                }
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int x = 0; x < D / 32; x++) {
+                        uint32_t u[4];
+                        ldsm4_t(vt + chunk_at<C::ROWB, false>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * x + (lane >> 4)), u);
+#pragma unroll
+                        for (int y = 0; y < 2; y++) {
+                            const uint32_t e0 = even_bf16(u[2 * y]), e1 = even_bf16(u[2 * y + 1]);
+                            const uint32_t d0 = odd_bf16(u[2 * y]), d1 = odd_bf16(u[2 * y + 1]);
+#pragma unroll
+                            for (int m = 0; m < MT; m++) {
+                                mma(o[m][4 * x + 2 * y], pf[m], e0, e1);
+                                mma(o[m][4 * x + 2 * y + 1], pf[m], d0, d1);
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 16; x++) {
+                        uint32_t u[4];
+                        ldsm4_t(vt + chunk_at<C::ROWB, false>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * x + (lane >> 4)), u);
+#pragma unroll
+                        for (int m = 0; m < MT; m++) {
+                            mma(o[m][2 * x], pf[m], u[0], u[1]);
+                            mma(o[m][2 * x + 1], pf[m], u[2], u[3]);
+                        }
+                    }
+                }
+            }
+            slot = slot + 1 == C::S ? 0 : slot + 1;
+        }
+
+        // ---- the four warps' results: scaled to the item's maximum and summed through shared memory.  The scratch is
+        // the ring slot that was computed last: it is refilled after this part's barriers.
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 1);
+                l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 2);
+                if (tig == 0) s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h], l[m][h], mmax[m][h], 0.f);
+            }
+        const bool whole = w.u0 == 0 && np == w.units;
+        const int64_t part = 2 * (int64_t)blockIdx.x + (first_part ? 0 : 1);
+        constexpr int H = E4M3 ? 2 : 1, DH = D / H;  // an 8-bit slot holds half of the columns at a time
+        float *scratch = reinterpret_cast<float *>(smem + (slot == 0 ? C::S - 1 : slot - 1) * C::STAGE);
+        const int row = threadIdx.x / 8, col = (threadIdx.x % 8) * 4;
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+#pragma unroll
+            for (int half = 0; half < H; half++) {
+                __syncthreads();  // the slot (or the scratch of the pass before) has been read by every warp
+                float *mine = scratch + warp * 16 * DH;
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int r = h * 8 + gid, sw = (r << 3) & (DH - 8);
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int x = 0; x < DH / 16; x++) {
+                            const int n = 2 * (half * (DH / 16) + x);
+                            *reinterpret_cast<float4 *>(mine + r * DH + ((16 * x + 4 * tig) ^ sw)) =
+                                make_float4(o[m][n][2 * h], o[m][n + 1][2 * h], o[m][n][2 * h + 1], o[m][n + 1][2 * h + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NT; n++)
+                            *reinterpret_cast<float2 *>(mine + r * DH + ((8 * n + 2 * tig) ^ sw)) =
+                                make_float2(o[m][n][2 * h], o[m][n][2 * h + 1]);
+                    }
+                }
+                __syncthreads();
+                const int r = m * 16 + row;
+                float f[4], top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; i++) top = fmaxf(top, s_ml[i][r].z);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float4 v = s_ml[i][r];
+                    f[i] = v.x == -INFINITY ? 0.f : ex2((v.x - top) * c);
+                    sum = fmaf(f[i], v.y, sum);
+                }
+                if (r < nrows) {
+                    const int64_t at = ((int64_t)(w.s.first + tok0 + r / sp.group) * p.qheads + w.head * sp.group + r % sp.group);
+                    const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+#pragma unroll
+                    for (int x = 0; x < DH / 32; x++) {
+                        const int d = 32 * x + col;
+                        float a[4] = {};
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const float4 v = *reinterpret_cast<const float4 *>(scratch + (i * 16 + row) * DH + (d ^ ((row << 3) & (DH - 8))));
+                            a[0] = fmaf(f[i], v.x, a[0]);
+                            a[1] = fmaf(f[i], v.y, a[1]);
+                            a[2] = fmaf(f[i], v.z, a[2]);
+                            a[3] = fmaf(f[i], v.w, a[3]);
+                        }
+                        if (whole) {
+                            *reinterpret_cast<uint2 *>(p.o + (at * D + half * DH + d) * 2) =
+                                make_uint2(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[2] * inv, a[3] * inv));
+                        } else {
+                            *reinterpret_cast<float4 *>(ws.acc + (part * 16 * MT + r) * D + half * DH + d) =
+                                make_float4(a[0], a[1], a[2], a[3]);
+                        }
+                    }
+                    if (half == 0 && threadIdx.x % 8 == 0) {
+                        if (!whole) ws.ml[part * 16 * MT + r] = make_float2(top, sum);
+                        else if (p.m_out) {
+                            p.m_out[at] = top * p.scale;
+                            p.l_out[at] = sum;
+                        }
+                    }
+                }
+            }
+        }
+        __syncthreads();  // the scratch and s_ml are free
+        first_part = false;
+        w.step(np, sp, Seqs{p.t, p.c.page_log2, p.err});
+    }
+    cp_wait<0>();
+}
+
+template <int D, bool E4M3, int MT>
+cudaError_t launch(const PgAttn &p, const PgPlan &pl, const PgWork &w, cudaStream_t st) {
+    using C = Cfg<D, E4M3, MT>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(cache_tokens_kernel<D, E4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    cache_tokens_kernel<D, E4M3, MT><<<pl.ctas, kThreads, C::SMEM, st>>>(p, pl.split, w);
+    return cudaGetLastError();
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_m(const PgAttn &p, const PgPlan &pl, const PgWork &w, cudaStream_t st) {
+    return pl.rows == 16 ? launch<D, E4M3, 1>(p, pl, w, st) : launch<D, E4M3, 2>(p, pl, w, st);
+}
+
+}  // namespace
+
+PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causal, int num_sms) {
+    PgPlan pl{};
+    if (group > kPgTokenRows || t.rows == 0) return pl;
+    pl.rows = (int64_t)t.max_new * group <= 16 ? 16 : 32;
+    PgSplit &sp = pl.split;
+    sp.heads = c.heads;
+    sp.group = group;
+    sp.tok = pl.rows / group;
+    sp.causal = causal;
+    sp.min_rows = 1;
+    sp.max_rows = pl.rows;
+    // Short sequences are not cut: another block adds less than the merge's launch.
+    const int64_t longest = (int64_t)t.max_pages << c.page_log2;
+    sp.kt = longest <= 512 ? 512 : kBlock;
+    const int64_t units = (longest + sp.kt - 1) / sp.kt * t.n_seqs * c.heads;
+    pl.ctas = (int)std::min<int64_t>(units, (int64_t)num_sms * 2);
+    pl.bytes = pg_work_bytes(pl.ctas, pl.rows, c.dim);
+    return pl;
+}
+
+cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st) {
+    const PgWork w = pg_work(pl, p.c.dim, ws);
+    cudaError_t e;
+    if (p.c.fmt == EA_CACHE_E4M3) e = p.c.dim == 64 ? launch_m<64, true>(p, pl, w, st) : launch_m<128, true>(p, pl, w, st);
+    else e = p.c.dim == 64 ? launch_m<64, false>(p, pl, w, st) : launch_m<128, false>(p, pl, w, st);
+    if (e != cudaSuccess || pl.split.kt > kBlock) return e;
+    return launch_cache_merge(p, pl, ws, st);
+}
+
+}  // namespace ea

@@ -27,7 +27,7 @@ struct ea_cache_s {
     int32_t page = 0, page_log2 = 0, heads = 0, dim = 0;
     char *k = nullptr, *v = nullptr;
     uint8_t *ks = nullptr, *vs = nullptr;
-    int device = -1;
+    int device = -1, num_sms = 0;
 };
 
 namespace ea {
@@ -66,7 +66,56 @@ struct PgAttn {
     float scale, scale_log2;  // scale * log2(e)
     int *err;
 };
-cudaError_t launch_cache_attention(const PgAttn &p, int64_t *ctas, cudaStream_t st);
+
+// Where a batch's attention is cut, and the partial results of the cuts.
+struct PgSplit {
+    int32_t heads, group;        // key-value heads, query heads of one
+    int32_t tok;                 // tokens of an item
+    int32_t kt;                  // keys of a unit
+    int32_t causal;
+    int32_t min_rows, max_rows;  // the sequences served: min_rows <= n * group <= max_rows
+};
+
+// What a CTA whose range begins inside an item says to the merge.
+struct PgCut {
+    int64_t wi, we;              // the item's units [wi, we); we = 0: the range begins with an item, or is empty
+    int64_t total;               // units of the batch
+    int32_t seq, head, item;
+    int32_t parts;               // CTAs with units
+};
+
+struct PgWork {                  // the call's workspace
+    PgCut *cut;                  // [ctas]
+    float2 *ml;                  // [2 * ctas][rows]: maximum score and sum of a partial result
+    float *acc;                  // [2 * ctas][rows][dim]: its unnormalised output
+};
+
+struct PgPlan {                  // a kernel of the call and its grid
+    PgSplit split;
+    int32_t ctas;                // 0: not launched
+    int32_t rows;                // rows of an item
+    int32_t variant;
+    size_t bytes;                // workspace
+};
+
+// Workspace of a plan, and its parts in it.
+inline size_t pg_work_bytes(int ctas, int rows, int dim) {
+    const size_t n = (size_t)2 * ctas * rows;
+    return ((size_t)ctas * sizeof(PgCut) + 255) / 256 * 256 + (n * sizeof(float2) + 255) / 256 * 256 + n * dim * sizeof(float);
+}
+inline PgWork pg_work(const PgPlan &pl, int dim, void *ws) {
+    char *b = (char *)ws;
+    const size_t cut = ((size_t)pl.ctas * sizeof(PgCut) + 255) / 256 * 256;
+    const size_t ml = ((size_t)2 * pl.ctas * pl.rows * sizeof(float2) + 255) / 256 * 256;
+    return PgWork{(PgCut *)b, (float2 *)(b + cut), (float *)(b + cut + ml)};
+}
+
+// Token kernel: few rows a sequence, bound by reading the pages.
+constexpr int kPgTokenRows = 32;     // the most rows of a sequence (tokens x group) that it takes
+PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causal, int num_sms);
+cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st);
+cudaError_t launch_cache_merge(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st);
+cudaError_t launch_cache_attention(const PgAttn &p, int64_t *ctas, cudaStream_t st, int min_rows);
 
 // ------------------------------------------------------------- sequences
 
@@ -84,6 +133,147 @@ EA_HD bool pg_seq(int32_t a, int32_t b, int32_t len, int64_t rows, int32_t max_n
     s->len = len;
     return true;
 }
+
+// ------------------------------------------------------------- work list
+
+// SUM_{i < n} floor((a i + b) / m) for a, b >= 0, m > 0 (Euclid's way: whole
+// parts of a / m and b / m are summed in closed form, then i and the value
+// change places).
+EA_HD int64_t pg_floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t s = 0;
+    while (n > 0) {
+        if (a >= m) {
+            s += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            s += n * (b / m);
+            b %= m;
+        }
+        const int64_t y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+    return s;
+}
+
+EA_HD bool pg_served(const PgSeq &s, const PgSplit &sp) {
+    const int64_t r = (int64_t)s.n * sp.group;
+    return s.n > 0 && r >= sp.min_rows && r <= sp.max_rows;
+}
+
+EA_HD int pg_items(const PgSeq &s, const PgSplit &sp) { return (int)(((int64_t)s.n + sp.tok - 1) / sp.tok); }
+
+// Keys [0, e) that item j's last token keeps.
+EA_HD int pg_item_end(const PgSeq &s, const PgSplit &sp, int j) {
+    if (!sp.causal) return s.len;
+    const int64_t last = (int64_t)(j + 1) * sp.tok;
+    const int64_t e = (int64_t)s.len - s.n + (last < s.n ? last : s.n);
+    return e > 0 ? (int)e : 0;
+}
+
+EA_HD int pg_item_units(const PgSeq &s, const PgSplit &sp, int j) {
+    const int u = (int)(((int64_t)pg_item_end(s, sp, j) + sp.kt - 1) / sp.kt);
+    return u > 0 ? u : 1;
+}
+
+// Units of the items before item j of one key-value head (j < items).
+EA_HD int64_t pg_units_before(const PgSeq &s, const PgSplit &sp, int j) {
+    if (j <= 0) return 0;
+    if (!sp.causal) return (int64_t)j * pg_item_units(s, sp, 0);
+    const int64_t c = (int64_t)s.len - s.n;
+    int64_t none = c < 0 ? -c / sp.tok : 0;  // items whose tokens all stand before position 0: one unit each
+    if (none > j) none = j;
+    return none + pg_floor_sum(j - none, sp.kt, sp.tok, c + (none + 1) * sp.tok + sp.kt - 1);
+}
+
+EA_HD int64_t pg_head_units(const PgSeq &s, const PgSplit &sp) {
+    const int j = pg_items(s, sp) - 1;
+    return pg_units_before(s, sp, j) + pg_item_units(s, sp, j);
+}
+
+EA_HD int64_t pg_seq_units(const PgSeq &s, const PgSplit &sp) {
+    return pg_served(s, sp) ? sp.heads * pg_head_units(s, sp) : 0;
+}
+
+// The item that holds unit u of one key-value head.
+EA_HD int pg_item_of(const PgSeq &s, const PgSplit &sp, int64_t u) {
+    int a = 0, b = pg_items(s, sp) - 1;
+    while (a < b) {
+        const int mid = a + (b - a + 1) / 2;
+        if (pg_units_before(s, sp, mid) <= u) a = mid;
+        else b = mid - 1;
+    }
+    return a;
+}
+
+// Units [pg_first(x), pg_first(x + 1)) of CTA x, of `parts` with work.
+EA_HD int64_t pg_first(int64_t total, int parts, int x) { return total / parts * x + total % parts * x / parts; }
+EA_HD int pg_parts(int64_t total, int ctas) { return (int)(total < ctas ? total : ctas); }
+
+// A CTA's share of the units.
+struct PgShare {
+    int64_t w0, off;   // first unit of the batch; the same within its sequence
+    int64_t total;     // units of the batch
+    int64_t count;     // units of this CTA
+    int32_t seq, parts;
+};
+
+// The parts of items in a CTA's share, in order (Seqs: seqs(i) is sequence i,
+// seqs.count() their number).
+struct PgWalk {
+    PgSeq s;
+    int64_t left;            // units not taken yet
+    int32_t seq, head, item;
+    int32_t u0;              // first unit of the current item not taken yet
+    int32_t units;           // units of the current item
+
+    template <class Seqs>
+    EA_HD void begin(const PgShare &sh, const PgSplit &sp, const Seqs &seqs) {
+        left = sh.count;
+        seq = sh.seq;
+        head = item = u0 = units = 0;
+        if (left <= 0) return;
+        s = seqs(seq);
+        if (pg_items(s, sp) == 1) {  // one item a head: no search
+            units = pg_item_units(s, sp, 0);
+            head = (int)(sh.off / units);
+            u0 = (int)(sh.off - (int64_t)head * units);
+            return;
+        }
+        const int64_t hu = pg_head_units(s, sp);
+        head = (int)(sh.off / hu);
+        const int64_t u = sh.off - head * hu;
+        item = pg_item_of(s, sp, u);
+        u0 = (int)(u - pg_units_before(s, sp, item));
+        units = pg_item_units(s, sp, item);
+    }
+
+    // Units of the current part (0: none left).
+    EA_HD int part() const { return (int)(left < units - u0 ? left : units - u0); }
+
+    // Leave `n` units of the current part behind (n <= part()).
+    template <class Seqs>
+    EA_HD void step(int n, const PgSplit &sp, const Seqs &seqs) {
+        left -= n;
+        u0 += n;
+        if (u0 < units || left <= 0) return;
+        u0 = 0;
+        if (++item == pg_items(s, sp)) {
+            item = 0;
+            if (++head == sp.heads) {
+                head = 0;
+                do s = seqs(++seq);
+                while (!pg_served(s, sp) && seq + 1 < seqs.count());
+            }
+        }
+        units = pg_item_units(s, sp, item);
+    }
+};
 
 // Element offset of a vector (page, head, slot) / dim in the pool.
 EA_HD int64_t pg_vec(const PgPool &c, int64_t page, int head, int slot) {

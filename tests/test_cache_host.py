@@ -193,3 +193,59 @@ def test_reference_attention_closed_forms():
         assert np.allclose(out[i], v[:end].mean(0)) and np.isclose(l[i], end)
     out, m, l, *_ = cu.softmax_attention(rng.normal(size=(2, 4)), k[:1], v[:1], np.array([-1, 0]), 1.0, True)
     assert not out[0].any() and m[0] == -np.inf and l[0] == 0 and np.allclose(out[1], v[0])
+
+
+def split(L, b, heads, group, tok, kt, causal, lo, hi, ctas):
+    a, keep = host_batch(b)
+    sp = (ctypes.c_int32 * 7)(heads, group, tok, kt, causal, lo, hi)
+    cap = 1 << 16
+    parts, n = np.zeros((cap, 7), dtype=np.int64), ctypes.c_int64()
+    _abi.check_status(L.ea_cache_attention_split(ctypes.byref(a), b.page, b.rows, sp, ctas, cap,
+                                                 parts.ctypes.data_as(_abi.P64), ctypes.byref(n)))
+    return parts[:n.value]
+
+
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("group,tok,kt,lo,hi", [(4, 8, 64, 1, 32), (1, 256, 128, 33, 1 << 30), (3, 42, 128, 1, 1 << 30),
+                                                (7, 36, 128, 0, 1 << 30), (128, 2, 128, 0, 1 << 30), (16, 16, 512, 1, 256)])
+@pytest.mark.parametrize("ctas", [1, 7, 152, 304])
+def test_work_list_against_enumeration(L, causal, group, tok, kt, lo, hi, ctas):
+    """Every unit of every item exactly once and in order, shares equal to within one unit, whatever the lengths."""
+    rng = np.random.default_rng(ctas + 10 * group + causal)
+    seqs = [(1, 1), (0, 9), (5, 0), (300, 120), (7, 7), (64, 700), (33, 33), (1, 900), (257, 999), (0, 0), (40, 3)]
+    seqs += [(int(rng.integers(0, 60)), int(rng.integers(0, 400))) for _ in range(20)]
+    heads = 3
+    want = []
+    for i, (n, t) in enumerate(seqs):
+        if n == 0 or not lo <= n * group <= hi:
+            continue
+        for h in range(heads):
+            for j in range(-(-n // tok)):
+                last = min(n, (j + 1) * tok)
+                e = max(0, t - n + last) if causal else t
+                units = max(1, -(-e // kt))
+                want += [(i, h, j, u, units) for u in range(units)]
+    parts = split(L, cu.Batch(seqs, 16), heads, group, tok, kt, causal, lo, hi, ctas)
+    got = [(s, h, j, u, units) for _, s, h, j, u0, u1, units in parts.tolist() for u in range(u0, u1)]
+    assert got == want
+    share = np.bincount(parts[:, 0], weights=parts[:, 5] - parts[:, 4])
+    assert len(share) == min(ctas, len(want)) and share.max() - share.min() <= 1
+    # at most the first and the last part of a CTA are pieces of an item
+    for x in range(len(share)):
+        mine = parts[parts[:, 0] == x]
+        cut = (mine[:, 4] > 0) | (mine[:, 5] < mine[:, 6])
+        assert not cut[1:-1].any()
+
+
+def test_work_list_of_long_sequences(L):
+    """Sums in closed form at lengths where an enumeration by unit is out of reach: units add up, items tile the tokens."""
+    b = cu.Batch([(1, 1)], 16)
+    b.seqs, b.lens = [(1 << 20, 1 << 24)], np.array([1 << 24], dtype=np.int32)
+    b.starts, b.rows, b.max_pages = np.array([0, 1 << 20], dtype=np.int32), 1 << 20, 1 << 20
+    b.pages = np.zeros((1, 1), dtype=np.int32)
+    parts = split(L, b, 1, 3, 84, 128, 1, 0, (1 << 31) - 1, 152)
+    items = -(-(1 << 20) // 84)
+    ends = (1 << 24) - (1 << 20) + np.minimum(1 << 20, (np.arange(items) + 1) * 84)
+    assert (parts[:, 5] - parts[:, 4]).sum() == (-(-ends // 128)).sum()
+    for j, (a, z) in zip(parts[:, 3], parts[:, 4:7:2]):
+        assert z == -(-ends[j] // 128)
