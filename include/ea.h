@@ -431,7 +431,7 @@ typedef struct {
  * [page] scale bytes (e4m3 only, else NULL).  Borrowed: the caller keeps them
  * alive; 16-byte aligned, on the current device, which stays the cache's
  * device.  Errors: EA_ERR_ARG, EA_ERR_DTYPE (format), EA_ERR_UNSUPPORTED
- * (page, dim, no tensor-map encoder). */
+ * (page, dim, pages * heads * page of 2^31 or more). */
 ea_status ea_cache_create(ea_cache_format format, int64_t pages, int32_t page, int32_t heads, int32_t dim, void *k,
                           void *v, void *k_scale, void *v_scale, ea_cache *out);
 ea_status ea_cache_destroy(ea_cache cache);

@@ -166,8 +166,9 @@ extern "C" ea_status ea_cache_create(ea_cache_format format, int64_t pages, int3
             return set_error(EA_ERR_ARG, "ea_cache_create: scales belong to the e4m3 format, and only to it");
         for (const void *x : {k, v, k_scale, v_scale})
             if (((uintptr_t)x & 15) != 0) return set_error(EA_ERR_ARG, "ea_cache_create: arrays must be 16-byte aligned");
-        if ((double)pages * heads * page * dim * 2 > 9.0e18) return set_error(EA_ERR_ARG, "ea_cache_create: too large");
-        ea_cache_s c;
+        if ((double)pages * heads * page > (double)INT32_MAX)
+            return set_error(EA_ERR_UNSUPPORTED, "ea_cache_create: more than 2^31 - 1 vectors");
+        ea_cache_s c{};
         c.format = format;
         c.n_pages = pages;
         c.page = page;
@@ -233,7 +234,7 @@ ea_status attn_shape(ea_cache cache, const ea_page_batch *batch, ea_relation q, 
 // that max_new rules out is not launched.
 struct AttnPlans {
     PgPlan tokens;
-    bool chunks;    // sequences with more rows than the token kernel takes are possible
+    PgPlan chunks;
     size_t bytes;
 };
 
@@ -242,9 +243,39 @@ AttnPlans plans_of(const ea_cache_s *cache, const ea_page_batch *batch, int64_t 
     const PgTable t = table_of(batch, rows);
     const int group = (int)(heads / cache->heads);
     a.tokens = plan_cache_tokens(t, pool_of(cache), group, causal, cache->num_sms);
-    a.chunks = (int64_t)t.max_new * group > (a.tokens.ctas ? a.tokens.split.max_rows : 0);
-    a.bytes = a.tokens.bytes;
+    a.chunks = plan_cache_chunks(t, pool_of(cache), group, causal, cache->num_sms,
+                                 a.tokens.ctas ? a.tokens.split.max_rows + 1 : 1);
+    a.bytes = std::max(a.tokens.bytes, a.chunks.bytes);  // one after the other on the stream
     return a;
+}
+
+ea_status encode(DevCtx *c, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2, CUtensorMap *m) {
+    if (!c->encode) return set_error(EA_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t gdim[3] = {d0, d1, d2}, gstr[2] = {d0 * 2, d0 * d1 * 2};
+    cuuint32_t box[3] = {64, b1, b2}, estr[3] = {1, 1, 1};
+    CUresult r = c->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), gdim, gstr, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? EA_OK : set_error(EA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+// Tensor maps of a chunk launch: a tile of Q is the group's heads of `tok / 2`
+// tokens; a page of K or V is `page` vectors.
+ea_status chunk_maps(DevCtx *c, ea_cache_s *cache, const ea_relation_s *q, int64_t heads, int64_t rows, const PgSplit &sp,
+                     PgMaps *m) {
+    memset(m, 0, sizeof *m);
+    ea_status s = encode(c, q->arena, cache->dim, heads, rows, sp.group, sp.tok / 2, &m->q);
+    if (s || cache->format != EA_CACHE_BF16) return s;
+    if (!cache->mapped) {
+        const uint64_t vecs = (uint64_t)cache->n_pages * cache->heads * cache->page;
+        s = encode(c, cache->k, cache->dim, vecs, 1, cache->page, 1, &cache->k_map);
+        if (!s) s = encode(c, cache->v, cache->dim, vecs, 1, cache->page, 1, &cache->v_map);
+        if (s) return s;
+        cache->mapped = true;
+    }
+    m->k = cache->k_map;
+    m->v = cache->v_map;
+    return EA_OK;
 }
 
 }  // namespace
@@ -323,11 +354,13 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
             ctas += a.tokens.ctas;
             launches += 1;
         }
-        if (rows > 0 && a.chunks) {
-            int64_t n = 0;
-            cudaError_t e = launch_cache_attention(p, &n, (cudaStream_t)stream, a.tokens.ctas ? a.tokens.split.max_rows + 1 : 0);
+        if (a.chunks.ctas > 0) {
+            PgMaps maps;
+            s = chunk_maps(c, cache, q, heads, rows, a.chunks.split, &maps);
+            if (s) return s;
+            cudaError_t e = launch_cache_chunks(p, a.chunks, maps, o.workspace, (cudaStream_t)stream);
             if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
-            ctas += n;
+            ctas += a.chunks.ctas;
             launches += 1;
         }
         note_launch(kCacheAttention, launches, ctas);

@@ -1,0 +1,658 @@
+// paged_chunks.cu -- attention over the paged cache on the sm_103a tensor
+// cores, for sequences with more query rows than the token kernel takes:
+// chunks of a prompt, whole prompts, many grouped heads.
+//
+// The rows of an item are 2 x `tpt` tokens times the heads of a group,
+// token-major, in two tiles of up to 128 rows that share their key tiles
+// (128 keys): each K and V tile is read once for 256 rows, which keeps the
+// L2 traffic at half of what the products could take in.  The units of all
+// items (a key tile of an item) are shared out evenly over the CTAs, one CTA
+// per SM, whatever the lengths are; an item that falls into several CTAs is
+// merged from its partial (m, l, A) triples.
+//
+// Key tiles come page by page.  bf16 pages are copied by TMA straight into
+// the swizzled operand tiles (a box of up to 128 positions x 64 columns: a
+// page is contiguous for a head, so a page is one box per 64 columns).
+// 8-bit pages are copied with bulk copies into a ring of 64-key half tiles
+// and rewritten as bf16 operands by a warpgroup of their own: sign and the
+// other 7 bits moved to bf16's places give value * 2^-120, one product with
+// 2^120 times the scale (exact) puts that right, so that nothing behind the
+// tiles knows of the format.
+//
+// Keys at and beyond the sequence's end lie in the last tile only.  Their
+// scores are dropped by position whatever they are; the second product stops
+// at the next multiple of 16 keys, and the up to 15 rows of V before it are
+// cleared in shared memory (a probability of 0 times a stale NaN is NaN).
+//
+// Roles (one CTA per SM; bf16: 384 threads, e4m3: 512):
+//   warps 0-3, 4-7  softmax of tile X = 0, 1: a query row per thread (TMEM
+//              lane = row), its 128 scores in registers: mask by position,
+//              row maximum, p = 2^(c s - c m), row sum, P as bf16 over the
+//              scores; A is rescaled in TMEM when the reference maximum moves
+//              by more than 2^64 (fp32 and bf16 have the same 8 exponent
+//              bits, so P, l and A stay in range and their relative rounding
+//              is the same at any magnitude); at the part's end A / l to the
+//              output, or (m, l, A) to the workspace.
+//   warp 8     copies: Q tiles; K and V pages (or the raw half tiles).
+//   warp 9     TMEM and MMA issue: per key tile and X, A_X (+)= P_X V, then
+//              S_X = Q_X K^T of the next key tile, so that one tile's products
+//              run while the other's softmax does.
+//   warps 12-15 (e4m3) rewrite the half tiles as bf16.
+// Every mbarrier wait is bounded (2 s); on time-out the kernel raises the
+// device error word, all roles leave their loops, the copies and MMAs in
+// flight are waited for and TMEM is freed before the CTA exits.
+#include "attn_common.cuh"
+#include "paged_sched.cuh"
+#include "tc_common.cuh"
+
+namespace ea {
+namespace {
+
+using namespace tc;
+using namespace attn;
+using namespace pg;
+
+constexpr int kRows = 128;        // rows of a tile (TMEM lanes)
+constexpr int kKeys = 128;        // keys of a key tile
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 256;   // S_0 [0, 128), S_1 [128, 256), A_0 [256, 256 + D), A_1 [256 + D, ..)
+constexpr float kLazy = 64.0f;
+constexpr int kStages = 2;        // K/V ring: a stage is K and V of one key tile
+constexpr int kRaw = 4;           // e4m3: ring of raw half tiles
+
+// Register split (setmaxnreg): the softmax threads keep a row of 128 scores.
+// The shares add up to the launch's registers exactly.
+template <bool E4M3>
+struct Regs {
+    static constexpr int THREADS = E4M3 ? 512 : 384;
+    static constexpr int LAUNCH = E4M3 ? 128 : 168;
+    static constexpr int SOFTMAX = E4M3 ? 192 : 208;
+    static constexpr int CTL = E4M3 ? 64 : 88;
+    static constexpr int CONV = 64;
+    static_assert(128 * (2 * SOFTMAX + CTL + (E4M3 ? CONV : 0)) <= THREADS * LAUNCH, "register split");
+};
+
+struct Ctl {
+    uint64_t q_full[2], q_empty[2];
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t raw_full[kRaw], raw_empty[kRaw];
+    uint64_t s_full[2], p_full[2], o_fin[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort;
+    PgShare share;
+    int64_t scan[16];
+};
+
+template <int D, bool E4M3>
+struct Cfg {
+    static constexpr int CH = D / 64;                       // 64-column (128-byte) chunks of the head dim
+    static constexpr int TILE = kRows * D * 2;
+    static constexpr int K_OFF = 2 * TILE;                  // Q_0, Q_1, then K of each stage, V of each stage
+    static constexpr int V_OFF = K_OFF + kStages * TILE;
+    static constexpr int RAW_OFF = V_OFF + kStages * TILE;
+    static constexpr int RAW = E4M3 ? 64 * D + 64 : 0;      // 64 keys' codes, then their scale bytes
+    static constexpr int CTL_OFF = RAW_OFF + kRaw * RAW;
+    static constexpr int SMEM = 1024 + CTL_OFF + (int)sizeof(Ctl);
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The part of an item that a CTA works on next.
+struct Part {
+    int n[2];      // key tiles of X = 0, 1 (X runs the part's first n[X] tiles)
+    int tiles;     // the larger of them
+    int u0;        // first key tile
+    int tok0;      // the item's first token (within the sequence's new tokens)
+    int end;       // keys of the item
+    bool whole;
+};
+
+__device__ __forceinline__ Part part_of(const PgWalk &w, const PgSplit &sp) {
+    Part q;
+    const int np = w.part(), half = sp.tok / 2;
+    q.u0 = w.u0;
+    q.whole = w.u0 == 0 && np == w.units;
+    q.tok0 = w.item * sp.tok;
+    q.end = pg_item_end(w.s, sp, w.item);
+    const int units = (q.end + kKeys - 1) / kKeys;
+    int e0 = q.end;  // keys of tile 0: up to its own last token
+    const bool two = q.tok0 + half < w.s.n;
+    if (two && sp.causal) e0 = max(0, w.s.len - w.s.n + q.tok0 + half);
+    const int u1 = w.u0 + np;
+    q.n[0] = max(0, min(u1, (e0 + kKeys - 1) / kKeys) - w.u0);
+    q.n[1] = two ? max(0, min(u1, units) - w.u0) : 0;
+    q.tiles = max(q.n[0], q.n[1]);
+    return q;
+}
+
+// Two e4m3 bytes at bits 8..15 and 24..31 of x as bf16 times 2^-120.
+__device__ __forceinline__ uint32_t as_bf16(uint32_t x) { return ((x & 0x7f007f00u) >> 4) | (x & 0x80008000u); }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Regs<E4M3>::THREADS, 1)
+cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgSplit sp,
+                    const __grid_constant__ PgWork ws, const __grid_constant__ CUtensorMap q_map,
+                    const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using C = Cfg<D, E4M3>;
+    using R = Regs<E4M3>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::CTL_OFF);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    volatile int *abort = &ctl->abort;
+    const Seqs seqs{p.t, p.c.page_log2, p.err};
+    const int half_tok = sp.tok / 2;      // tokens of a tile
+    const int half_rows = half_tok * sp.group;
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < 2; b++) {
+            mbar_init(&ctl->q_full[b], 1);
+            mbar_init(&ctl->q_empty[b], 1);
+            mbar_init(&ctl->s_full[b], 1);
+            mbar_init(&ctl->p_full[b], 4);
+            mbar_init(&ctl->o_fin[b], 1);
+        }
+        for (int b = 0; b < kStages; b++) {
+            mbar_init(&ctl->kv_full[b], E4M3 ? 4 : 1);
+            mbar_init(&ctl->kv_empty[b], 1);
+        }
+        for (int b = 0; b < kRaw; b++) {
+            mbar_init(&ctl->raw_full[b], 1);
+            mbar_init(&ctl->raw_empty[b], 4);
+        }
+        mbar_init(&ctl->mma_done, 1);
+        ctl->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == 9) tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
+    tc_fence_before();
+    take_share<R::THREADS>(p.t, sp, p.c.page_log2, p.err, ctl->scan, &ctl->share);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+
+    if (warp >= 8 && warp < 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::CTL));
+    if (warp == 8) {
+        if (lane == 0) {
+            // ------------------------------------------------ copies
+            PgWalk w;
+            w.begin(ctl->share, sp, seqs);
+            note_cut(ws, ctl->share, w);
+            uint32_t ct = 0, rt = 0, qx0 = 0, qx1 = 0;  // key tiles, raw half tiles, items per X
+            uint32_t q_armed = 0, q_par = 0, kv_armed = 0, kv_par = 0, raw_armed = 0, raw_par = 0;
+            bool ok = true;
+            for (; w.left > 0 && ok; w.step(w.part(), sp, seqs)) {
+                const Part P = part_of(w, sp);
+                for (int x = 0; x < 2 && ok; x++) {
+                    if (P.n[x] == 0) continue;
+                    const uint32_t qn = x == 0 ? qx0 : qx1;
+                    if (!mbar_wait(&ctl->q_empty[x], (qn & 1) ^ 1, abort, p.err, kDevTimeoutProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t qs = smem_u32(smem + x * C::TILE);
+                    mbar_expect_tx(&ctl->q_full[x], half_rows * D * 2);
+#pragma unroll
+                    for (int c = 0; c < C::CH; c++)
+                        tma_load_3d(qs + c * (kRows * 128), &q_map, &ctl->q_full[x], 64 * c, w.head * sp.group,
+                                    w.s.first + P.tok0 + x * half_tok);
+                    q_armed |= 1u << x;
+                    q_par = (q_par & ~(1u << x)) | ((qn & 1) << x);
+                    if (x == 0) qx0++;
+                    else qx1++;
+                }
+                const int lg = p.c.page_log2, page = 1 << lg;
+                for (int j = 0; j < P.tiles && ok; j++) {
+                    const int key0 = (P.u0 + j) * kKeys, nv = min(kKeys, P.end - key0);
+                    if constexpr (!E4M3) {
+                        const int st = ct % kStages;
+                        const uint32_t ph = (ct / kStages) & 1;
+                        if (!mbar_wait(&ctl->kv_empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t ks = smem_u32(smem + C::K_OFF + st * C::TILE);
+                        const uint32_t vs = smem_u32(smem + C::V_OFF + st * C::TILE);
+                        const int np = (nv + page - 1) >> lg;  // pages hold at most 128 positions
+                        mbar_expect_tx(&ctl->kv_full[st], 2 * np * page * D * 2);
+                        for (int i = 0; i < np; i++) {
+                            const int32_t g = load_page(p.t, p.c.n_pages, w.seq, (key0 >> lg) + i, p.err);
+                            const int row = (int)pg_vec(p.c, g, w.head, 0);
+#pragma unroll
+                            for (int c = 0; c < C::CH; c++)
+                                tma_load_3d(ks + c * (kKeys * 128) + i * page * 128, &k_map, &ctl->kv_full[st], 64 * c, row, 0);
+#pragma unroll
+                            for (int c = 0; c < C::CH; c++)
+                                tma_load_3d(vs + c * (kKeys * 128) + i * page * 128, &v_map, &ctl->kv_full[st], 64 * c, row, 0);
+                        }
+                        kv_armed |= 1u << st;
+                        kv_par = (kv_par & ~(1u << st)) | (ph << st);
+                    } else {
+                        for (int h = 0; h < 4 && ok; h++) {  // K's halves, then V's
+                            const int k0 = (h & 1) * 64, nh = min(64, nv - k0);
+                            if (nh <= 0) continue;
+                            const int st = rt % kRaw;
+                            const uint32_t ph = (rt / kRaw) & 1;
+                            if (!mbar_wait(&ctl->raw_empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) {
+                                ok = false;
+                                break;
+                            }
+                            const int run = min(page, 64), np = (nh + run - 1) / run;
+                            const uint32_t dst = smem_u32(smem + C::RAW_OFF + st * C::RAW);
+                            const char *cells = h < 2 ? p.c.k : p.c.v;
+                            const uint8_t *scales = h < 2 ? p.c.ks : p.c.vs;
+                            mbar_expect_tx(&ctl->raw_full[st], np * run * (D + 1));
+                            for (int i = 0; i < np; i++) {
+                                const int key = key0 + k0 + i * run;
+                                const int32_t g = load_page(p.t, p.c.n_pages, w.seq, key >> lg, p.err);
+                                const int64_t vec = pg_vec(p.c, g, w.head, key & (page - 1));
+                                bulk_load(dst + i * run * D, cells + vec * D, run * D, &ctl->raw_full[st]);
+                                bulk_load(dst + 64 * D + i * run, scales + vec, run, &ctl->raw_full[st]);
+                            }
+                            raw_armed |= 1u << st;
+                            raw_par = (raw_par & ~(1u << st)) | (ph << st);
+                            rt++;
+                        }
+                    }
+                    ct++;
+                }
+            }
+            if (*abort) {
+                // Let our own copies land before the CTA can exit.
+                for (int s = 0; s < 2; s++)
+                    if (q_armed & (1u << s)) mbar_wait(&ctl->q_full[s], (q_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
+                for (int s = 0; s < kStages; s++)
+                    if (kv_armed & (1u << s)) mbar_wait(&ctl->kv_full[s], (kv_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
+                for (int s = 0; s < kRaw; s++)
+                    if (raw_armed & (1u << s)) mbar_wait(&ctl->raw_full[s], (raw_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
+            }
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------ MMA issue (the whole warp; one elected lane issues)
+        const uint32_t idesc_s = make_idesc(kRows, kKeys, 0, 0);  // Q (K-major) x K (K-major)
+        const uint32_t idesc_o = make_idesc(kRows, D, 0, 1);      // P (TMEM) x V (MN-major)
+        uint32_t ct = 0, qx0 = 0, qx1 = 0, tx0 = 0, tx1 = 0;
+        bool ok = true;
+        auto mma_s = [&](int x, uint32_t t) {
+            const uint64_t qd = sdesc(smem_u32(smem + x * C::TILE), 16, 1024);
+            const uint64_t kd = sdesc(smem_u32(smem + C::K_OFF + (t % kStages) * C::TILE), 16, 1024);
+            const uint32_t d = tmem + (uint32_t)(x * kKeys);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; kk++)
+                    umma_bf16(d, qd + (uint64_t)sdesc_off((kk >> 2) * (kRows * 128) + (kk & 3) * 32),
+                              kd + (uint64_t)sdesc_off((kk >> 2) * (kKeys * 128) + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+                umma_commit(&ctl->s_full[x]);
+            }
+            __syncwarp();
+        };
+        // A_x (+)= P_x V_t over the first `steps` runs of 16 keys
+        auto mma_o = [&](int x, uint32_t t, bool first, int steps) {
+            const uint64_t vd = sdesc(smem_u32(smem + C::V_OFF + (t % kStages) * C::TILE), kKeys * 128, 1024);
+            const uint32_t pa = tmem + (uint32_t)(x * kKeys);
+            const uint32_t d = tmem + kOCol + (uint32_t)(x * D);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; kk++)
+                    if (kk < steps)
+                        umma_bf16_ts(d, pa + kk * 8, vd + (uint64_t)sdesc_off(kk * 2048), idesc_o, (!first || kk > 0) ? 1u : 0u);
+            }
+            __syncwarp();
+        };
+        auto commit1 = [&](uint64_t *b) {
+            if (elect_one()) umma_commit(b);
+            __syncwarp();
+        };
+        // K and V of tile t are there; the last rows of a partial V are cleared
+        auto kv_wait = [&](uint32_t t, int nv) {
+            if (!warp_wait(&ctl->kv_full[t % kStages], (t / kStages) & 1, abort, p.err, kDevTimeoutMma)) return false;
+            const int to = (nv + 15) & ~15;
+            if (!E4M3 && nv < to) {
+                uint8_t *v = smem + C::V_OFF + (t % kStages) * C::TILE;
+                for (int i = lane; i < (to - nv) * 8; i += 32)
+#pragma unroll
+                    for (int c = 0; c < C::CH; c++)
+                        *reinterpret_cast<uint4 *>(v + c * (kKeys * 128) + (nv + i / 8) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async();
+                __syncwarp();
+            }
+            return true;
+        };
+        PgWalk w;
+        w.begin(ctl->share, sp, seqs);
+        for (; w.left > 0 && ok; w.step(w.part(), sp, seqs)) {
+            const Part P = part_of(w, sp);
+            const int n = P.tiles, nt0 = P.n[0], nt1 = P.n[1];
+            if (n == 0) continue;
+            const int last_nv = P.end - (P.u0 + n - 1) * kKeys;  // keys of the part's last tile (may be more than 128)
+            auto keys_of = [&](int j) { return j == n - 1 ? min(kKeys, last_nv) : kKeys; };
+            if (!kv_wait(ct, keys_of(0))) break;
+            for (int x = 0; x < 2 && ok; x++) {
+                const int ntx = x == 0 ? nt0 : nt1;
+                if (ntx == 0) continue;
+                if (!warp_wait(&ctl->q_full[x], (x == 0 ? qx0 : qx1) & 1, abort, p.err, kDevTimeoutMma)) {
+                    ok = false;
+                    break;
+                }
+                if (x == 0) qx0++;
+                else qx1++;
+                tc_fence_after();
+                mma_s(x, ct);
+                if (ntx == 1) commit1(&ctl->q_empty[x]);
+            }
+            for (int j = 0; j < n && ok; j++) {
+                const uint32_t t = ct + j;
+                bool kv_next = false;  // K and V of tile t + 1 have landed
+                for (int x = 0; x < 2; x++) {
+                    const int ntx = x == 0 ? nt0 : nt1;
+                    if (j >= ntx) continue;  // the rest of the part is beyond what x keeps
+                    if (!warp_wait(&ctl->p_full[x], ((x == 0 ? tx0 : tx1) + j) & 1, abort, p.err, kDevTimeoutMma)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    mma_o(x, t, j == 0, (keys_of(j) + 15) >> 4);
+                    if (j == ntx - 1) commit1(&ctl->o_fin[x]);
+                    if (j + 1 < ntx) {
+                        if (!kv_next) {
+                            if (!kv_wait(t + 1, keys_of(j + 1))) {
+                                ok = false;
+                                break;
+                            }
+                            kv_next = true;
+                        }
+                        mma_s(x, t + 1);
+                        if (j + 1 == ntx - 1) commit1(&ctl->q_empty[x]);
+                    }
+                }
+                if (!ok) break;
+                commit1(&ctl->kv_empty[t % kStages]);  // K and V of tile t are done
+            }
+            ct += n;
+            tx0 += nt0;
+            tx1 += nt1;
+        }
+        // Every MMA this thread issued has completed once mma_done flips.
+        commit1(&ctl->mma_done);
+        if (lane == 0) mbar_wait(&ctl->mma_done, 0, abort, p.err, kDevTimeoutMma, kTimeoutNs, false);
+        __syncwarp();
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::SOFTMAX));
+        // ------------------------------------------------ softmax and output
+        const int x = warp >> 2;
+        const int row = threadIdx.x & (kRows - 1);
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t srow = lane_base + (uint32_t)(x * kKeys);
+        const uint32_t orow = lane_base + kOCol + (uint32_t)(x * D);
+        const float c = p.scale_log2;
+        const int rtok = row / sp.group, rhead = row - rtok * sp.group;  // the row's token and head of the tile
+        uint32_t ci = 0, ct = 0;  // parts and key tiles of this X
+        bool ok = true, first_part = true;
+        PgWalk w;
+        w.begin(ctl->share, sp, seqs);
+        for (; w.left > 0 && ok; w.step(w.part(), sp, seqs), first_part = false) {
+            const Part P = part_of(w, sp);
+            const int tok0 = P.tok0 + x * half_tok, ntok = min(half_tok, w.s.n - tok0);
+            if (ntok <= 0) continue;
+            const int n = x == 0 ? P.n[0] : P.n[1];
+            const bool mine = row < half_rows && rtok < ntok;
+            // last key the row keeps; a row without a token goes along with the tile's last one
+            const int pos = w.s.len - w.s.n + tok0 + min(rtok, ntok - 1);
+            const int hi = sp.causal ? min(pos, w.s.len - 1) : w.s.len - 1;
+            float m_ref = -INFINITY, m_max = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; j++) {
+                if (!warp_wait(&ctl->s_full[x], (ct + j) & 1, abort, p.err, kDevTimeoutSoftmax)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t u[kKeys];
+                float hm0, hm1, hm2, hm3;
+                tmem_ld32_max(srow, u, hm0);
+                tmem_ld32_max(srow + 32, u + 32, hm1);
+                tmem_ld32_max(srow + 64, u + 64, hm2);
+                tmem_ld32_max(srow + 96, u + 96, hm3);
+                tmem_wait_ld();
+                const int jhi = hi - (P.u0 + j) * kKeys;
+                float mx = fmaxf(max3(hm0, hm1, hm2), hm3);
+                if (jhi < kKeys - 1) {
+                    mx = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < kKeys; q += 32) mx = fmaxf(mx, mask_chunk(u + q, q, 0, jhi));
+                }
+                m_max = fmaxf(m_max, mx);
+                float alpha = 1.f;
+                if (mx != -INFINITY && (m_ref == -INFINITY || (mx - m_ref) * c > kLazy)) {
+                    alpha = m_ref == -INFINITY ? 0.f : ex2((m_ref - mx) * c);
+                    m_ref = mx;
+                }
+                const float base = m_ref == -INFINITY ? 0.f : m_ref * c;
+                const uint64_t c2 = pack_f32x2(c, c), nb2 = pack_f32x2(-base, -base);
+                uint64_t ls[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int q = 0; q < kKeys / 2; q++) {
+                    const uint64_t y = fma_f32x2(pack_u32x2(u[2 * q], u[2 * q + 1]), c2, nb2);
+                    const float e0 = ex2(lo_f32(y)), e1 = ex2(hi_f32(y));
+                    ls[q & 3] = add_f32x2(ls[q & 3], pack_f32x2(e0, e1));
+                    u[q] = pack_bf16(e0, e1);
+                }
+                const uint64_t s01 = add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3]));
+                l = fmaf(l, alpha, lo_f32(s01) + hi_f32(s01));
+                tmem_st32(srow, u);
+                tmem_st32(srow + 32, u + 32);
+                // The previous A += P V of this tile has completed: these scores were computed after it, in order.
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; cc++) {
+                        uint32_t o[32];
+                        tmem_ld32(orow + 32 * cc, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(orow + 32 * cc, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->p_full[x]);
+            }
+            if (!ok) break;
+            if (n > 0) {
+                if (!warp_wait(&ctl->o_fin[x], ci & 1, abort, p.err, kDevTimeoutSoftmax)) {
+                    ok = false;
+                    break;
+                }
+                ct += n;
+                ci++;
+            }
+            tc_fence_after();
+            // whole item: A / l as bf16; a part of one: (m, l, A) with the true maximum as reference
+            const float to_max = m_max == -INFINITY ? 0.f : ex2((m_ref - m_max) * c);
+            const float f = !P.whole ? to_max : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+            const int64_t at = (int64_t)(w.s.first + tok0 + (mine ? rtok : 0)) * p.qheads + w.head * sp.group + rhead;
+            const int64_t prow = (2 * (int64_t)blockIdx.x + (first_part ? 0 : 1)) * (2 * half_rows) + x * half_rows + row;
+#pragma unroll
+            for (int cc = 0; cc < D / 32; cc++) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(orow + 32 * cc, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i++) o[i] = 0u;
+                }
+                if (!mine) continue;
+                if (P.whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + (at * D + 32 * cc) * 2);
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const float *g = reinterpret_cast<const float *>(o + 8 * q);
+                        dst[q] = make_uint4(pack_bf16(g[0] * f, g[1] * f), pack_bf16(g[2] * f, g[3] * f),
+                                            pack_bf16(g[4] * f, g[5] * f), pack_bf16(g[6] * f, g[7] * f));
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(ws.acc + prow * D + 32 * cc);
+#pragma unroll
+                    for (int q = 0; q < 8; q++) {
+                        const float *g = reinterpret_cast<const float *>(o + 4 * q);
+                        dst[q] = make_float4(g[0] * f, g[1] * f, g[2] * f, g[3] * f);
+                    }
+                }
+            }
+            tc_fence_before();
+            if (mine) {
+                if (!P.whole) ws.ml[prow] = make_float2(m_max, l * to_max);
+                else if (p.m_out) {
+                    p.m_out[at] = m_max * p.scale;
+                    p.l_out[at] = l * to_max;
+                }
+            }
+        }
+    } else if (E4M3 && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::CONV));
+        // ------------------------------------------------ raw half tiles to bf16 operands
+        PgWalk w;
+        w.begin(ctl->share, sp, seqs);
+        const int tid = threadIdx.x - 384;
+        constexpr int CPR = D / 16;  // 16-byte chunks (16 codes) of a row
+        uint32_t ct = 0, rt = 0;
+        bool ok = true;
+        for (; w.left > 0 && ok; w.step(w.part(), sp, seqs)) {
+            const Part P = part_of(w, sp);
+            for (int j = 0; j < P.tiles && ok; j++, ct++) {
+                const int nv = min(kKeys, P.end - (P.u0 + j) * kKeys);
+                const int st = ct % kStages;
+                if (!warp_wait(&ctl->kv_empty[st], ((ct / kStages) & 1) ^ 1, abort, p.err, kDevTimeoutProducer)) {
+                    ok = false;
+                    break;
+                }
+                for (int h = 0; h < 4; h++) {
+                    const int k0 = (h & 1) * 64;
+                    if (nv - k0 <= 0) continue;
+                    const int rs = rt % kRaw;
+                    if (!warp_wait(&ctl->raw_full[rs], (rt / kRaw) & 1, abort, p.err, kDevTimeoutProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint8_t *raw = smem + C::RAW_OFF + rs * C::RAW;
+                    uint8_t *dst = smem + (h < 2 ? C::K_OFF : C::V_OFF) + st * C::TILE;
+#pragma unroll
+                    for (int i = 0; i < 64 * CPR / 128; i++) {
+                        const int id = i * 128 + tid, r = id / CPR, ch = id % CPR;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(raw + id * 16);
+                        const uint32_t b = raw[64 * D + r];
+                        // 2^120 times the scale; 2^(b - 7) is beyond bf16 for the largest scales: the rest goes into a
+                        // second product
+                        const uint32_t b1 = min(b, 134u), m1 = b == 255u ? 0x7fff7fffu : (b1 + 120u) * 0x00800080u;
+                        uint32_t o[8];
+#pragma unroll
+                        for (int q = 0; q < 4; q++) {
+                            const uint32_t wd = reinterpret_cast<const uint32_t *>(&v)[q];
+                            o[2 * q] = mul_bf16x2(as_bf16(__byte_perm(wd, 0, 0x1404)), m1);
+                            o[2 * q + 1] = mul_bf16x2(as_bf16(__byte_perm(wd, 0, 0x3424)), m1);
+                        }
+                        if (b > 134u && b != 255u) {
+                            const uint32_t m2 = (b - 134u + 127u) * 0x00800080u;
+#pragma unroll
+                            for (int q = 0; q < 8; q++) o[q] = mul_bf16x2(o[q], m2);
+                        }
+                        if (k0 + r >= nv) {
+#pragma unroll
+                            for (int q = 0; q < 8; q++) o[q] = 0u;
+                        }
+                        // columns 16 ch .. + 15 of row k0 + r: two 16-byte chunks of the 128-byte swizzled row; the lanes
+                        // of the second 64 columns store theirs in the other order (their banks are the same)
+                        uint8_t *rowp = dst + (ch / 4) * (kKeys * 128) + (k0 + r) * 128;
+                        const int s = (k0 + r) & 7, a = 2 * (ch & 3), flip = D == 128 ? ch >> 2 : r & 1;
+                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
+                        *reinterpret_cast<uint4 *>(rowp + (((a + flip) ^ s) << 4)) = flip ? hi4 : lo;
+                        *reinterpret_cast<uint4 *>(rowp + (((a + 1 - flip) ^ s) << 4)) = flip ? lo : hi4;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->raw_empty[rs]);
+                    rt++;
+                }
+                if (!ok) break;
+                fence_proxy_async();  // the operand tiles are read by the tensor cores (async proxy)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->kv_full[st]);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, bool E4M3>
+cudaError_t launch(const PgAttn &p, const PgPlan &pl, const PgWork &w, const PgMaps &maps, cudaStream_t st) {
+    using C = Cfg<D, E4M3>;
+    using R = Regs<E4M3>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        // The register split assumes the block starts with LAUNCH a thread: with fewer, setmaxnreg.inc would wait for
+        // registers that never come, so such a build is refused before it can launch.
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, cache_chunks_kernel<D, E4M3>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != R::LAUNCH) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(cache_chunks_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    cache_chunks_kernel<D, E4M3><<<pl.ctas, R::THREADS, C::SMEM, st>>>(p, pl.split, w, maps.q, maps.k, maps.v);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causal, int num_sms, int min_rows) {
+    PgPlan pl{};
+    if ((int64_t)t.max_new * group < min_rows) return pl;
+    const int tpt = kRows / group;
+    PgSplit &sp = pl.split;
+    sp.heads = c.heads;
+    sp.group = group;
+    sp.tok = 2 * tpt;
+    sp.kt = kKeys;
+    sp.causal = causal;
+    sp.min_rows = min_rows;
+    sp.max_rows = INT32_MAX;
+    pl.rows = sp.tok * group;
+    const int64_t items = std::min<int64_t>((int64_t)t.n_seqs * ((t.max_new + sp.tok - 1) / sp.tok), t.rows / sp.tok + t.n_seqs);
+    const int64_t units = ((((int64_t)t.max_pages << c.page_log2) + kKeys - 1) / kKeys) * items * c.heads;
+    pl.ctas = (int)std::min<int64_t>(units, num_sms);
+    pl.bytes = pg_work_bytes(pl.ctas, pl.rows, c.dim);
+    return pl;
+}
+
+cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, void *ws, cudaStream_t st) {
+    const PgWork w = pg_work(pl, p.c.dim, ws);
+    cudaError_t e;
+    if (p.c.fmt == EA_CACHE_E4M3) e = p.c.dim == 64 ? launch<64, true>(p, pl, w, maps, st) : launch<128, true>(p, pl, w, maps, st);
+    else e = p.c.dim == 64 ? launch<64, false>(p, pl, w, maps, st) : launch<128, false>(p, pl, w, maps, st);
+    if (e != cudaSuccess) return e;
+    return launch_cache_merge(p, pl, ws, st);
+}
+
+}  // namespace ea

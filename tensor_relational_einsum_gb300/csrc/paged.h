@@ -13,6 +13,8 @@
 // units fall into several CTAs is merged from their partial results.
 #pragma once
 
+#include <cuda.h>
+
 #include "host.h"
 
 #ifdef __CUDACC__
@@ -28,6 +30,8 @@ struct ea_cache_s {
     char *k = nullptr, *v = nullptr;
     uint8_t *ks = nullptr, *vs = nullptr;
     int device = -1, num_sms = 0;
+    bool mapped = false;
+    CUtensorMap k_map, v_map;  // bf16: the pools for the chunk kernel's copies, made on first use
 };
 
 namespace ea {
@@ -115,7 +119,12 @@ constexpr int kPgTokenRows = 32;     // the most rows of a sequence (tokens x gr
 PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causal, int num_sms);
 cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st);
 cudaError_t launch_cache_merge(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st);
-cudaError_t launch_cache_attention(const PgAttn &p, int64_t *ctas, cudaStream_t st, int min_rows);
+// Chunk kernel: tiles of 128 rows on the tensor cores.
+struct PgMaps {                  // tensor maps: Q's rows; the pools as [vectors][dim] (bf16)
+    CUtensorMap q, k, v;
+};
+PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causal, int num_sms, int min_rows);
+cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, void *ws, cudaStream_t st);
 
 // ------------------------------------------------------------- sequences
 
