@@ -24,9 +24,10 @@ __all__ = ["Relation", "joinagg", "exchange", "check", "EaError", "lib", "plan_c
 
 def __getattr__(name):
     if name in ("Relation", "joinagg", "exchange", "check", "plan_cache_clear", "output_layout"):
-        from . import relation
-        return getattr(relation, name)
-    if name in ("PagedCache", "PageBatch", "cache_append", "cache_read", "cache_attention"):
-        from . import cache
-        return getattr(cache, name)
-    raise AttributeError(name)
+        from . import relation as module
+    elif name in ("PagedCache", "PageBatch", "cache_append", "cache_read", "cache_attention"):
+        from . import cache as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)  # later look-ups find it at once
+    return value

@@ -17,7 +17,7 @@ import torch
 
 from . import _abi
 from ._abi import CACHE_FORMATS, check_status, lib
-from .relation import Relation, _stream_ptr
+from .relation import Relation
 
 _CELLS = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
 
@@ -98,7 +98,10 @@ class PageBatch:
         if starts.device != pages.device or lens.device != pages.device:
             raise ValueError("the batch's tensors lie on different devices")
         self.pages, self.starts, self.lens, self.max_new = pages, starts, lens, int(max_new)
+        self.device = pages.device
         self.args = _abi.PageBatchArgs()
+        self.ref = ctypes.byref(self.args)
+        self._workspace = {}  # bytes of an attention call's workspace, by everything they depend on besides the batch
         self.args.pages, self.args.starts, self.args.lens = pages.data_ptr(), starts.data_ptr(), lens.data_ptr()
         self.args.page_stride = pages.stride(0) if n > 1 else pages.shape[1]
         self.args.n_seqs, self.args.max_pages, self.args.max_new = n, pages.shape[1], self.max_new
@@ -114,17 +117,26 @@ class PageBatch:
         check_status(lib().ea_cache_check_batch(cache.pages, cache.page, ctypes.byref(a), int(rows), 1 if write else 0))
 
 
+def _raw_stream(device, stream) -> ctypes.c_void_p:
+    """The CUDA stream of a call: ``stream``, or the device's current one."""
+    return ctypes.c_void_p(stream.cuda_stream if stream is not None else
+                           torch._C._cuda_getCurrentRawStream(device.index))
+
+
 def _same_device(cache: PagedCache, batch: PageBatch, *relations):
-    if batch.pages.device != cache.device or any(r is not None and r.storage.device != cache.device for r in relations):
-        raise ValueError("the cache, the batch and the relations must lie on one device")
+    if batch.device != cache.device:
+        raise ValueError("the cache and the batch lie on different devices")
+    for r in relations:
+        if r is not None and r.storage.device != cache.device:
+            raise ValueError("the cache and a relation lie on different devices")
 
 
 def cache_append(cache: PagedCache, batch: PageBatch, k: Relation, v: Relation, stream=None):
     """Write the batch's rows of ``k`` and ``v`` (relations [rows.., heads,
     dim], f32 or bf16) into the pages, rounded to the cache's format."""
     _same_device(cache, batch, k, v)
-    check_status(lib().ea_cache_append(cache.handle, ctypes.byref(batch.args), k.handle, v.handle,
-                                       ctypes.c_void_p(_stream_ptr(stream))))
+    check_status(lib().ea_cache_append(cache.handle, batch.ref, k.handle, v.handle,
+                                       _raw_stream(cache.device, stream)))
 
 
 def cache_read(cache: PagedCache, batch: PageBatch, k: Relation | None = None, v: Relation | None = None,
@@ -140,8 +152,8 @@ def cache_read(cache: PagedCache, batch: PageBatch, k: Relation | None = None, v
     if k is None or v is None:
         raise ValueError("give both k and v or neither")
     _same_device(cache, batch, k, v)
-    check_status(lib().ea_cache_read(cache.handle, ctypes.byref(batch.args), k.handle, v.handle,
-                                     ctypes.c_void_p(_stream_ptr(stream))))
+    check_status(lib().ea_cache_read(cache.handle, batch.ref, k.handle, v.handle,
+                                     _raw_stream(cache.device, stream)))
     return k, v
 
 
@@ -158,23 +170,26 @@ def cache_attention(q: Relation, cache: PagedCache, batch: PageBatch, scale: flo
     call's stream, one per call."""
     _same_device(cache, batch, q, out, m_out, l_out)
     L = lib()
-    need = ctypes.c_size_t()
-    check_status(L.ea_cache_attention_workspace(cache.handle, ctypes.byref(batch.args), q.handle, ctypes.byref(need)))
+    shape = (cache.pages, cache.page, cache.heads, cache.dim, q.dims)
+    need = batch._workspace.get(shape)
+    if need is None:
+        n = ctypes.c_size_t()
+        check_status(L.ea_cache_attention_workspace(cache.handle, batch.ref, q.handle, ctypes.byref(n)))
+        need = batch._workspace[shape] = n.value
     work = None
-    if out is None or need.value:
-        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(cache.device):
+    if stream is None:
+        if out is None:
+            out = Relation("bf16", q.dims, q.bounds, device=cache.device)
+        if need:
+            work = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    else:
+        with torch.cuda.stream(stream):
             if out is None:
                 out = Relation("bf16", q.dims, q.bounds, device=cache.device)
-            if need.value:
-                work = torch.empty(need.value, dtype=torch.uint8, device=cache.device)
-    o = _abi.CacheAttnOpts()
-    o.scale, o.causal = scale, 1 if causal else 0
-    if m_out is not None:
-        o.m_out = m_out.handle.value
-    if l_out is not None:
-        o.l_out = l_out.handle.value
-    if work is not None:
-        o.workspace, o.workspace_bytes = work.data_ptr(), need.value
-    check_status(L.ea_cache_attention(cache.handle, ctypes.byref(batch.args), q.handle, ctypes.byref(o),
-                                      ctypes.c_void_p(_stream_ptr(stream)), out.handle))
+            if need:
+                work = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    o = _abi.CacheAttnOpts(scale, 1 if causal else 0, m_out.handle if m_out is not None else None,
+                           l_out.handle if l_out is not None else None, work.data_ptr() if work is not None else None, need)
+    check_status(L.ea_cache_attention(cache.handle, batch.ref, q.handle, ctypes.byref(o),
+                                      _raw_stream(cache.device, stream), out.handle))
     return out

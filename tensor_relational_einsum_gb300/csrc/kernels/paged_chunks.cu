@@ -37,6 +37,7 @@
 //   warp 9     TMEM and MMA issue: per key tile and X, A_X (+)= P_X V, then
 //              S_X = Q_X K^T of the next key tile, so that one tile's products
 //              run while the other's softmax does.
+//   warp 10    hands the CTA's parts of items to the others through a ring.
 //   warps 12-15 (e4m3) rewrite the half tiles as bf16.
 // Every mbarrier wait is bounded (2 s); on time-out the kernel raises the
 // device error word, all roles leave their loops, the copies and MMAs in
@@ -57,8 +58,9 @@ constexpr int kKeys = 128;        // keys of a key tile
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;   // S_0 [0, 128), S_1 [128, 256), A_0 [256, 256 + D), A_1 [256 + D, ..)
 constexpr float kLazy = 64.0f;
-constexpr int kStages = 2;        // K/V ring: a stage is K and V of one key tile
 constexpr int kRaw = 4;           // e4m3: ring of raw half tiles
+constexpr int kParts = 4;         // ring of parts
+constexpr int kMaxStages = 4;
 
 // Register split (setmaxnreg): the softmax threads keep a row of 128 scores.
 // The shares add up to the launch's registers exactly.
@@ -72,25 +74,68 @@ struct Regs {
     static_assert(128 * (2 * SOFTMAX + CTL + (E4M3 ? CONV : 0)) <= THREADS * LAUNCH, "register split");
 };
 
+// The part of an item that a CTA works on, as warp 10 hands it to the others.
+struct Part {
+    int n[2];       // key tiles of X = 0, 1 (X runs the part's first n[X] tiles)
+    int tiles;      // the larger of them; -1: no more parts
+    int u0;         // first key tile
+    int tok0;       // the item's first token (within the sequence's new tokens)
+    int end;        // keys of the item
+    int whole, seq, head;
+    int row0;       // dense row of token tok0
+    int ntok;       // the sequence's tokens from tok0 on
+    int pos0, len;  // position of token tok0, length of the sequence
+};
+
+__device__ __forceinline__ Part part_of(const PgWalk &w, const PgSplit &sp) {
+    Part q;
+    const int np = w.part(), half = sp.tok / 2;
+    q.u0 = w.u0;
+    q.whole = w.u0 == 0 && np == w.units;
+    q.tok0 = w.item * sp.tok;
+    q.end = pg_item_end(w.s, sp, w.item);
+    q.seq = w.seq;
+    q.head = w.head;
+    q.row0 = w.s.first + q.tok0;
+    q.ntok = w.s.n - q.tok0;
+    q.len = w.s.len;
+    q.pos0 = w.s.len - w.s.n + q.tok0;
+    const int units = (q.end + kKeys - 1) / kKeys, u1 = w.u0 + np;
+    const bool two = half < q.ntok;
+    // keys of tile 0: up to its own last token's
+    const int e0 = two && sp.causal ? max(0, q.pos0 + half) : q.end;
+    q.n[0] = max(0, min(u1, (e0 + kKeys - 1) / kKeys) - w.u0);
+    q.n[1] = two ? max(0, min(u1, units) - w.u0) : 0;
+    q.tiles = max(q.n[0], q.n[1]);
+    return q;
+}
+
 struct Ctl {
     uint64_t q_full[2], q_empty[2];
-    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t s_full[2], p_full[2], o_fin[2];
+    uint64_t part_full[kParts], part_empty[kParts];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
     PgShare share;
     int64_t scan[16];
+    Part part[kParts];
 };
 
 template <int D, bool E4M3>
 struct Cfg {
     static constexpr int CH = D / 64;                       // 64-column (128-byte) chunks of the head dim
     static constexpr int TILE = kRows * D * 2;
+    // Rings of K and of V tiles, each freed by its own product: K of tile t + 2 can arrive from the end of S(t) on and
+    // is needed for S(t + 2), more than a tile's time, which is longer than a copy takes.  (With K and V freed
+    // together there was half of that, and a tile took 4000 cycles instead of 3000.)  At D = 64 a tile takes half the
+    // time, and there is room for four.
+    static constexpr int ST = D == 64 ? 4 : 2;
     static constexpr int K_OFF = 2 * TILE;                  // Q_0, Q_1, then K of each stage, V of each stage
-    static constexpr int V_OFF = K_OFF + kStages * TILE;
-    static constexpr int RAW_OFF = V_OFF + kStages * TILE;
+    static constexpr int V_OFF = K_OFF + ST * TILE;
+    static constexpr int RAW_OFF = V_OFF + ST * TILE;
     static constexpr int RAW = E4M3 ? 64 * D + 64 : 0;      // 64 keys' codes, then their scale bytes
     static constexpr int CTL_OFF = RAW_OFF + kRaw * RAW;
     static constexpr int SMEM = 1024 + CTL_OFF + (int)sizeof(Ctl);
@@ -101,34 +146,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
-}
-
-// The part of an item that a CTA works on next.
-struct Part {
-    int n[2];      // key tiles of X = 0, 1 (X runs the part's first n[X] tiles)
-    int tiles;     // the larger of them
-    int u0;        // first key tile
-    int tok0;      // the item's first token (within the sequence's new tokens)
-    int end;       // keys of the item
-    bool whole;
-};
-
-__device__ __forceinline__ Part part_of(const PgWalk &w, const PgSplit &sp) {
-    Part q;
-    const int np = w.part(), half = sp.tok / 2;
-    q.u0 = w.u0;
-    q.whole = w.u0 == 0 && np == w.units;
-    q.tok0 = w.item * sp.tok;
-    q.end = pg_item_end(w.s, sp, w.item);
-    const int units = (q.end + kKeys - 1) / kKeys;
-    int e0 = q.end;  // keys of tile 0: up to its own last token
-    const bool two = q.tok0 + half < w.s.n;
-    if (two && sp.causal) e0 = max(0, w.s.len - w.s.n + q.tok0 + half);
-    const int u1 = w.u0 + np;
-    q.n[0] = max(0, min(u1, (e0 + kKeys - 1) / kKeys) - w.u0);
-    q.n[1] = two ? max(0, min(u1, units) - w.u0) : 0;
-    q.tiles = max(q.n[0], q.n[1]);
-    return q;
 }
 
 // Two e4m3 bytes at bits 8..15 and 24..31 of x as bf16 times 2^-120.
@@ -163,13 +180,19 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             mbar_init(&ctl->p_full[b], 4);
             mbar_init(&ctl->o_fin[b], 1);
         }
-        for (int b = 0; b < kStages; b++) {
-            mbar_init(&ctl->kv_full[b], E4M3 ? 4 : 1);
-            mbar_init(&ctl->kv_empty[b], 1);
+        for (int b = 0; b < C::ST; b++) {
+            mbar_init(&ctl->k_full[b], E4M3 ? 4 : 1);
+            mbar_init(&ctl->k_empty[b], 1);
+            mbar_init(&ctl->v_full[b], E4M3 ? 4 : 1);
+            mbar_init(&ctl->v_empty[b], 1);
         }
         for (int b = 0; b < kRaw; b++) {
             mbar_init(&ctl->raw_full[b], 1);
             mbar_init(&ctl->raw_empty[b], 4);
+        }
+        for (int b = 0; b < kParts; b++) {
+            mbar_init(&ctl->part_full[b], 1);
+            mbar_init(&ctl->part_empty[b], E4M3 ? 14 : 10);  // the warps that read parts
         }
         mbar_init(&ctl->mma_done, 1);
         ctl->abort = 0;
@@ -182,102 +205,125 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
+    // The next part (whole warp): false when there is none, or a role gave up.
+    uint32_t pi = 0;
+    auto next_part = [&](Part &P, int code) {
+        const int b = pi % kParts;
+        if (!warp_wait(&ctl->part_full[b], (pi / kParts) & 1, abort, p.err, code)) return false;
+        P = ctl->part[b];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->part_empty[b]);
+        pi++;
+        return P.tiles >= 0;
+    };
 
     if (warp >= 8 && warp < 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::CTL));
     if (warp == 8) {
-        if (lane == 0) {
-            // ------------------------------------------------ copies
-            PgWalk w;
-            w.begin(ctl->share, sp, seqs);
-            note_cut(ws, ctl->share, w);
-            uint32_t ct = 0, rt = 0, qx0 = 0, qx1 = 0;  // key tiles, raw half tiles, items per X
-            uint32_t q_armed = 0, q_par = 0, kv_armed = 0, kv_par = 0, raw_armed = 0, raw_par = 0;
-            bool ok = true;
-            for (; w.left > 0 && ok; w.step(w.part(), sp, seqs)) {
-                const Part P = part_of(w, sp);
-                for (int x = 0; x < 2 && ok; x++) {
-                    if (P.n[x] == 0) continue;
-                    const uint32_t qn = x == 0 ? qx0 : qx1;
-                    if (!mbar_wait(&ctl->q_empty[x], (qn & 1) ^ 1, abort, p.err, kDevTimeoutProducer)) {
-                        ok = false;
-                        break;
-                    }
+        // ------------------------------------------------ copies (the whole warp; a lane looks up and copies a page)
+        uint32_t ct = 0, rt = 0, qx0 = 0, qx1 = 0;  // key tiles, raw half tiles, items per X
+        uint32_t q_armed = 0, q_par = 0, k_armed = 0, k_par = 0, v_armed = 0, v_par = 0, raw_armed = 0, raw_par = 0;
+        bool ok = true;
+        const int lg = p.c.page_log2, page = 1 << lg;
+        Part P;
+        while (ok && next_part(P, kDevTimeoutProducer)) {
+            // The number of this lane's page of tile j, read a tile ahead: the reads of a tile's pages do not wait for
+            // one another, nor the copies for them.
+            auto look = [&](int j) {
+                const int key = (P.u0 + j) * kKeys + (lane << lg);
+                return j < P.tiles && (lane << lg) < kKeys && key < P.end
+                           ? __ldg(p.t.pages + (int64_t)P.seq * p.t.page_stride + (key >> lg)) : 0;
+            };
+            int32_t next = look(0);
+            for (int x = 0; x < 2 && ok; x++) {
+                if (P.n[x] == 0) continue;
+                const uint32_t qn = x == 0 ? qx0 : qx1;
+                if (!warp_wait(&ctl->q_empty[x], (qn & 1) ^ 1, abort, p.err, kDevTimeoutProducer)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
                     const uint32_t qs = smem_u32(smem + x * C::TILE);
                     mbar_expect_tx(&ctl->q_full[x], half_rows * D * 2);
 #pragma unroll
                     for (int c = 0; c < C::CH; c++)
-                        tma_load_3d(qs + c * (kRows * 128), &q_map, &ctl->q_full[x], 64 * c, w.head * sp.group,
-                                    w.s.first + P.tok0 + x * half_tok);
-                    q_armed |= 1u << x;
-                    q_par = (q_par & ~(1u << x)) | ((qn & 1) << x);
-                    if (x == 0) qx0++;
-                    else qx1++;
+                        tma_load_3d(qs + c * (kRows * 128), &q_map, &ctl->q_full[x], 64 * c, P.head * sp.group,
+                                    P.row0 + x * half_tok);
                 }
-                const int lg = p.c.page_log2, page = 1 << lg;
-                for (int j = 0; j < P.tiles && ok; j++) {
-                    const int key0 = (P.u0 + j) * kKeys, nv = min(kKeys, P.end - key0);
-                    if constexpr (!E4M3) {
-                        const int st = ct % kStages;
-                        const uint32_t ph = (ct / kStages) & 1;
-                        if (!mbar_wait(&ctl->kv_empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) {
+                q_armed |= 1u << x;
+                q_par = (q_par & ~(1u << x)) | ((qn & 1) << x);
+                if (x == 0) qx0++;
+                else qx1++;
+            }
+            for (int j = 0; j < P.tiles && ok; j++, ct++) {
+                const int key0 = (P.u0 + j) * kKeys, nv = min(kKeys, P.end - key0);
+                const int32_t g = check_page(next, p.c.n_pages, p.err);
+                next = look(j + 1);
+                if constexpr (!E4M3) {
+                    const int st = ct % C::ST;
+                    const uint32_t ph = (ct / C::ST) & 1;
+                    const int np = (nv + page - 1) >> lg;
+                    const int row = (int)pg_vec(p.c, g, P.head, 0);
+                    auto load = [&](const CUtensorMap *map, uint32_t off, uint64_t *full, uint64_t *empty) {
+                        if (!warp_wait(&empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) return false;
+                        if (lane == 0) mbar_expect_tx(&full[st], np * page * D * 2);
+                        __syncwarp();
+                        if (lane < np) {
+                            const uint32_t dst = smem_u32(smem + off + st * C::TILE) + lane * page * 128;
+#pragma unroll
+                            for (int c = 0; c < C::CH; c++) tma_load_3d(dst + c * (kKeys * 128), map, &full[st], 64 * c, row, 0);
+                        }
+                        return true;
+                    };
+                    if (!load(&k_map, C::K_OFF, ctl->k_full, ctl->k_empty)) {
+                        ok = false;
+                        break;
+                    }
+                    k_armed |= 1u << st;
+                    k_par = (k_par & ~(1u << st)) | (ph << st);
+                    if (!load(&v_map, C::V_OFF, ctl->v_full, ctl->v_empty)) {
+                        ok = false;
+                        break;
+                    }
+                    v_armed |= 1u << st;
+                    v_par = (v_par & ~(1u << st)) | (ph << st);
+                } else {
+                    for (int h = 0; h < 4; h++) {  // K's halves, then V's
+                        const int k0 = (h & 1) * 64, nh = min(64, nv - k0);
+                        if (nh <= 0) continue;
+                        const int st = rt % kRaw;
+                        const uint32_t ph = (rt / kRaw) & 1;
+                        if (!warp_wait(&ctl->raw_empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) {
                             ok = false;
                             break;
                         }
-                        const uint32_t ks = smem_u32(smem + C::K_OFF + st * C::TILE);
-                        const uint32_t vs = smem_u32(smem + C::V_OFF + st * C::TILE);
-                        const int np = (nv + page - 1) >> lg;  // pages hold at most 128 positions
-                        mbar_expect_tx(&ctl->kv_full[st], 2 * np * page * D * 2);
-                        for (int i = 0; i < np; i++) {
-                            const int32_t g = load_page(p.t, p.c.n_pages, w.seq, (key0 >> lg) + i, p.err);
-                            const int row = (int)pg_vec(p.c, g, w.head, 0);
-#pragma unroll
-                            for (int c = 0; c < C::CH; c++)
-                                tma_load_3d(ks + c * (kKeys * 128) + i * page * 128, &k_map, &ctl->kv_full[st], 64 * c, row, 0);
-#pragma unroll
-                            for (int c = 0; c < C::CH; c++)
-                                tma_load_3d(vs + c * (kKeys * 128) + i * page * 128, &v_map, &ctl->kv_full[st], 64 * c, row, 0);
-                        }
-                        kv_armed |= 1u << st;
-                        kv_par = (kv_par & ~(1u << st)) | (ph << st);
-                    } else {
-                        for (int h = 0; h < 4 && ok; h++) {  // K's halves, then V's
-                            const int k0 = (h & 1) * 64, nh = min(64, nv - k0);
-                            if (nh <= 0) continue;
-                            const int st = rt % kRaw;
-                            const uint32_t ph = (rt / kRaw) & 1;
-                            if (!mbar_wait(&ctl->raw_empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) {
-                                ok = false;
-                                break;
-                            }
-                            const int run = min(page, 64), np = (nh + run - 1) / run;
+                        // a run: a page, or the half of one of 128 positions
+                        const int run = min(page, 64), np = (nh + run - 1) / run;
+                        const int32_t gi = __shfl_sync(0xffffffffu, g, (k0 + lane * run) >> lg);
+                        if (lane == 0) mbar_expect_tx(&ctl->raw_full[st], np * run * (D + 1));
+                        __syncwarp();
+                        if (lane < np) {
                             const uint32_t dst = smem_u32(smem + C::RAW_OFF + st * C::RAW);
-                            const char *cells = h < 2 ? p.c.k : p.c.v;
-                            const uint8_t *scales = h < 2 ? p.c.ks : p.c.vs;
-                            mbar_expect_tx(&ctl->raw_full[st], np * run * (D + 1));
-                            for (int i = 0; i < np; i++) {
-                                const int key = key0 + k0 + i * run;
-                                const int32_t g = load_page(p.t, p.c.n_pages, w.seq, key >> lg, p.err);
-                                const int64_t vec = pg_vec(p.c, g, w.head, key & (page - 1));
-                                bulk_load(dst + i * run * D, cells + vec * D, run * D, &ctl->raw_full[st]);
-                                bulk_load(dst + 64 * D + i * run, scales + vec, run, &ctl->raw_full[st]);
-                            }
-                            raw_armed |= 1u << st;
-                            raw_par = (raw_par & ~(1u << st)) | (ph << st);
-                            rt++;
+                            const int64_t vec = pg_vec(p.c, gi, P.head, (k0 + lane * run) & (page - 1));
+                            bulk_load(dst + lane * run * D, (h < 2 ? p.c.k : p.c.v) + vec * D, run * D, &ctl->raw_full[st]);
+                            bulk_load(dst + 64 * D + lane * run, (h < 2 ? p.c.ks : p.c.vs) + vec, run, &ctl->raw_full[st]);
                         }
+                        raw_armed |= 1u << st;
+                        raw_par = (raw_par & ~(1u << st)) | (ph << st);
+                        rt++;
                     }
-                    ct++;
                 }
             }
-            if (*abort) {
-                // Let our own copies land before the CTA can exit.
-                for (int s = 0; s < 2; s++)
-                    if (q_armed & (1u << s)) mbar_wait(&ctl->q_full[s], (q_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
-                for (int s = 0; s < kStages; s++)
-                    if (kv_armed & (1u << s)) mbar_wait(&ctl->kv_full[s], (kv_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
-                for (int s = 0; s < kRaw; s++)
-                    if (raw_armed & (1u << s)) mbar_wait(&ctl->raw_full[s], (raw_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
+        }
+        if (*abort && lane == 0) {
+            // Let our own copies land before the CTA can exit.
+            for (int s = 0; s < 2; s++)
+                if (q_armed & (1u << s)) mbar_wait(&ctl->q_full[s], (q_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
+            for (int s = 0; s < C::ST; s++) {
+                if (k_armed & (1u << s)) mbar_wait(&ctl->k_full[s], (k_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
+                if (v_armed & (1u << s)) mbar_wait(&ctl->v_full[s], (v_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
             }
+            for (int s = 0; s < kRaw; s++)
+                if (raw_armed & (1u << s)) mbar_wait(&ctl->raw_full[s], (raw_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
         }
     } else if (warp == 9) {
         // ------------------------------------------------ MMA issue (the whole warp; one elected lane issues)
@@ -287,7 +333,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         bool ok = true;
         auto mma_s = [&](int x, uint32_t t) {
             const uint64_t qd = sdesc(smem_u32(smem + x * C::TILE), 16, 1024);
-            const uint64_t kd = sdesc(smem_u32(smem + C::K_OFF + (t % kStages) * C::TILE), 16, 1024);
+            const uint64_t kd = sdesc(smem_u32(smem + C::K_OFF + (t % C::ST) * C::TILE), 16, 1024);
             const uint32_t d = tmem + (uint32_t)(x * kKeys);
             if (elect_one()) {
 #pragma unroll
@@ -300,7 +346,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         };
         // A_x (+)= P_x V_t over the first `steps` runs of 16 keys
         auto mma_o = [&](int x, uint32_t t, bool first, int steps) {
-            const uint64_t vd = sdesc(smem_u32(smem + C::V_OFF + (t % kStages) * C::TILE), kKeys * 128, 1024);
+            const uint64_t vd = sdesc(smem_u32(smem + C::V_OFF + (t % C::ST) * C::TILE), kKeys * 128, 1024);
             const uint32_t pa = tmem + (uint32_t)(x * kKeys);
             const uint32_t d = tmem + kOCol + (uint32_t)(x * D);
             if (elect_one()) {
@@ -315,12 +361,13 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             if (elect_one()) umma_commit(b);
             __syncwarp();
         };
-        // K and V of tile t are there; the last rows of a partial V are cleared
-        auto kv_wait = [&](uint32_t t, int nv) {
-            if (!warp_wait(&ctl->kv_full[t % kStages], (t / kStages) & 1, abort, p.err, kDevTimeoutMma)) return false;
+        auto k_wait = [&](uint32_t t) { return warp_wait(&ctl->k_full[t % C::ST], (t / C::ST) & 1, abort, p.err, kDevTimeoutMma); };
+        // V of tile t is there, with the last rows of a partial tile cleared
+        auto v_wait = [&](uint32_t t, int nv) {
+            if (!warp_wait(&ctl->v_full[t % C::ST], (t / C::ST) & 1, abort, p.err, kDevTimeoutMma)) return false;
             const int to = (nv + 15) & ~15;
             if (!E4M3 && nv < to) {
-                uint8_t *v = smem + C::V_OFF + (t % kStages) * C::TILE;
+                uint8_t *v = smem + C::V_OFF + (t % C::ST) * C::TILE;
                 for (int i = lane; i < (to - nv) * 8; i += 32)
 #pragma unroll
                     for (int c = 0; c < C::CH; c++)
@@ -330,15 +377,12 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             }
             return true;
         };
-        PgWalk w;
-        w.begin(ctl->share, sp, seqs);
-        for (; w.left > 0 && ok; w.step(w.part(), sp, seqs)) {
-            const Part P = part_of(w, sp);
+        Part P;
+        while (ok && next_part(P, kDevTimeoutMma)) {
             const int n = P.tiles, nt0 = P.n[0], nt1 = P.n[1];
             if (n == 0) continue;
             const int last_nv = P.end - (P.u0 + n - 1) * kKeys;  // keys of the part's last tile (may be more than 128)
-            auto keys_of = [&](int j) { return j == n - 1 ? min(kKeys, last_nv) : kKeys; };
-            if (!kv_wait(ct, keys_of(0))) break;
+            if (!k_wait(ct)) break;
             for (int x = 0; x < 2 && ok; x++) {
                 const int ntx = x == 0 ? nt0 : nt1;
                 if (ntx == 0) continue;
@@ -352,33 +396,39 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 mma_s(x, ct);
                 if (ntx == 1) commit1(&ctl->q_empty[x]);
             }
+            if (!ok) break;
+            commit1(&ctl->k_empty[ct % C::ST]);
             for (int j = 0; j < n && ok; j++) {
                 const uint32_t t = ct + j;
-                bool kv_next = false;  // K and V of tile t + 1 have landed
+                const int nv = j == n - 1 ? min(kKeys, last_nv) : kKeys;
+                bool v_now = false, k_next = false;  // V of tile t, K of tile t + 1 have landed
                 for (int x = 0; x < 2; x++) {
                     const int ntx = x == 0 ? nt0 : nt1;
                     if (j >= ntx) continue;  // the rest of the part is beyond what x keeps
+                    if (!v_now && !v_wait(t, nv)) {
+                        ok = false;
+                        break;
+                    }
+                    v_now = true;
                     if (!warp_wait(&ctl->p_full[x], ((x == 0 ? tx0 : tx1) + j) & 1, abort, p.err, kDevTimeoutMma)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    mma_o(x, t, j == 0, (keys_of(j) + 15) >> 4);
+                    mma_o(x, t, j == 0, (nv + 15) >> 4);
                     if (j == ntx - 1) commit1(&ctl->o_fin[x]);
+                    if (x == 1 || j >= nt1) commit1(&ctl->v_empty[t % C::ST]);  // the tile's last product
                     if (j + 1 < ntx) {
-                        if (!kv_next) {
-                            if (!kv_wait(t + 1, keys_of(j + 1))) {
-                                ok = false;
-                                break;
-                            }
-                            kv_next = true;
+                        if (!k_next && !k_wait(t + 1)) {
+                            ok = false;
+                            break;
                         }
+                        k_next = true;
                         mma_s(x, t + 1);
                         if (j + 1 == ntx - 1) commit1(&ctl->q_empty[x]);
+                        if (x == 1 || j + 1 >= nt1) commit1(&ctl->k_empty[(t + 1) % C::ST]);
                     }
                 }
-                if (!ok) break;
-                commit1(&ctl->kv_empty[t % kStages]);  // K and V of tile t are done
             }
             ct += n;
             tx0 += nt0;
@@ -388,6 +438,26 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         commit1(&ctl->mma_done);
         if (lane == 0) mbar_wait(&ctl->mma_done, 0, abort, p.err, kDevTimeoutMma, kTimeoutNs, false);
         __syncwarp();
+    } else if (warp == 10) {
+        if (lane == 0) {
+            // ------------------------------------------------ parts
+            PgWalk w;
+            w.begin(ctl->share, sp, seqs);
+            note_cut(ws, ctl->share, w);
+            for (uint32_t i = 0;; i++) {
+                const int b = i % kParts;
+                if (!mbar_wait(&ctl->part_empty[b], ((i / kParts) & 1) ^ 1, abort, p.err, kDevTimeoutProducer)) break;
+                if (w.left > 0) {
+                    ctl->part[b] = part_of(w, sp);
+                    w.step(w.part(), sp, seqs);
+                } else {
+                    ctl->part[b].tiles = -1;
+                }
+                const bool last = ctl->part[b].tiles < 0;
+                mbar_arrive(&ctl->part_full[b]);
+                if (last) break;
+            }
+        }
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::SOFTMAX));
         // ------------------------------------------------ softmax and output
@@ -399,18 +469,28 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         const float c = p.scale_log2;
         const int rtok = row / sp.group, rhead = row - rtok * sp.group;  // the row's token and head of the tile
         uint32_t ci = 0, ct = 0;  // parts and key tiles of this X
-        bool ok = true, first_part = true;
-        PgWalk w;
-        w.begin(ctl->share, sp, seqs);
-        for (; w.left > 0 && ok; w.step(w.part(), sp, seqs), first_part = false) {
-            const Part P = part_of(w, sp);
-            const int tok0 = P.tok0 + x * half_tok, ntok = min(half_tok, w.s.n - tok0);
-            if (ntok <= 0) continue;
-            const int n = x == 0 ? P.n[0] : P.n[1];
-            const bool mine = row < half_rows && rtok < ntok;
-            // last key the row keeps; a row without a token goes along with the tile's last one
-            const int pos = w.s.len - w.s.n + tok0 + min(rtok, ntok - 1);
-            const int hi = sp.causal ? min(pos, w.s.len - 1) : w.s.len - 1;
+        bool ok = true;
+        while (ok) {
+            int n, u0, slot, whole;  // what the loop over key tiles needs of the part
+            int hi;                  // last key the row keeps
+            int64_t at;              // the row's place in O; -1: no token of the sequence
+            {
+                Part P;
+                const bool first_part = pi == 0;
+                if (!next_part(P, kDevTimeoutSoftmax)) break;
+                const int ntok = min(half_tok, P.ntok - x * half_tok);
+                if (ntok <= 0) continue;
+                n = x == 0 ? P.n[0] : P.n[1];
+                u0 = P.u0;
+                whole = P.whole;
+                slot = 2 * blockIdx.x + (first_part ? 0 : 1);
+                // a row without a token goes along with the tile's last one
+                const int pos = P.pos0 + x * half_tok + min(rtok, ntok - 1);
+                hi = sp.causal ? min(pos, P.len - 1) : P.len - 1;
+                at = row < half_rows && rtok < ntok
+                         ? (int64_t)(P.row0 + x * half_tok + rtok) * p.qheads + P.head * sp.group + rhead : -1;
+            }
+            const bool mine = at >= 0;
             float m_ref = -INFINITY, m_max = -INFINITY, l = 0.f;
             for (int j = 0; j < n; j++) {
                 if (!warp_wait(&ctl->s_full[x], (ct + j) & 1, abort, p.err, kDevTimeoutSoftmax)) {
@@ -425,7 +505,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 tmem_ld32_max(srow + 64, u + 64, hm2);
                 tmem_ld32_max(srow + 96, u + 96, hm3);
                 tmem_wait_ld();
-                const int jhi = hi - (P.u0 + j) * kKeys;
+                const int jhi = hi - (u0 + j) * kKeys;
                 float mx = fmaxf(max3(hm0, hm1, hm2), hm3);
                 if (jhi < kKeys - 1) {
                     mx = -INFINITY;
@@ -481,9 +561,8 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             tc_fence_after();
             // whole item: A / l as bf16; a part of one: (m, l, A) with the true maximum as reference
             const float to_max = m_max == -INFINITY ? 0.f : ex2((m_ref - m_max) * c);
-            const float f = !P.whole ? to_max : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-            const int64_t at = (int64_t)(w.s.first + tok0 + (mine ? rtok : 0)) * p.qheads + w.head * sp.group + rhead;
-            const int64_t prow = (2 * (int64_t)blockIdx.x + (first_part ? 0 : 1)) * (2 * half_rows) + x * half_rows + row;
+            const float f = !whole ? to_max : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+            const int64_t prow = (int64_t)slot * (2 * half_rows) + x * half_rows + row;
 #pragma unroll
             for (int cc = 0; cc < D / 32; cc++) {
                 uint32_t o[32];
@@ -495,7 +574,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     for (int i = 0; i < 32; i++) o[i] = 0u;
                 }
                 if (!mine) continue;
-                if (P.whole) {
+                if (whole) {
                     uint4 *dst = reinterpret_cast<uint4 *>(p.o + (at * D + 32 * cc) * 2);
 #pragma unroll
                     for (int q = 0; q < 4; q++) {
@@ -514,7 +593,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             }
             tc_fence_before();
             if (mine) {
-                if (!P.whole) ws.ml[prow] = make_float2(m_max, l * to_max);
+                if (!whole) ws.ml[prow] = make_float2(m_max, l * to_max);
                 else if (p.m_out) {
                     p.m_out[at] = m_max * p.scale;
                     p.l_out[at] = l * to_max;
@@ -524,23 +603,22 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     } else if (E4M3 && warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::CONV));
         // ------------------------------------------------ raw half tiles to bf16 operands
-        PgWalk w;
-        w.begin(ctl->share, sp, seqs);
         const int tid = threadIdx.x - 384;
         constexpr int CPR = D / 16;  // 16-byte chunks (16 codes) of a row
         uint32_t ct = 0, rt = 0;
         bool ok = true;
-        for (; w.left > 0 && ok; w.step(w.part(), sp, seqs)) {
-            const Part P = part_of(w, sp);
+        Part P;
+        while (ok && next_part(P, kDevTimeoutProducer)) {
             for (int j = 0; j < P.tiles && ok; j++, ct++) {
                 const int nv = min(kKeys, P.end - (P.u0 + j) * kKeys);
-                const int st = ct % kStages;
-                if (!warp_wait(&ctl->kv_empty[st], ((ct / kStages) & 1) ^ 1, abort, p.err, kDevTimeoutProducer)) {
-                    ok = false;
-                    break;
-                }
+                const int st = ct % C::ST;
+                const uint32_t ph = (ct / C::ST) & 1;
                 for (int h = 0; h < 4; h++) {
                     const int k0 = (h & 1) * 64;
+                    if (k0 == 0 && !warp_wait(h ? &ctl->v_empty[st] : &ctl->k_empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) {
+                        ok = false;
+                        break;
+                    }
                     if (nv - k0 <= 0) continue;
                     const int rs = rt % kRaw;
                     if (!warp_wait(&ctl->raw_full[rs], (rt / kRaw) & 1, abort, p.err, kDevTimeoutProducer)) {
@@ -549,18 +627,30 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     }
                     const uint8_t *raw = smem + C::RAW_OFF + rs * C::RAW;
                     uint8_t *dst = smem + (h < 2 ? C::K_OFF : C::V_OFF) + st * C::TILE;
+                    // all of the thread's codes and scales first: the stores below may not be reordered with loads
+                    constexpr int IT = 64 * CPR / 128;
+                    uint4 v[IT];
+                    uint32_t sc[IT];
 #pragma unroll
-                    for (int i = 0; i < 64 * CPR / 128; i++) {
+                    for (int i = 0; i < IT; i++) {
+                        v[i] = *reinterpret_cast<const uint4 *>(raw + (i * 128 + tid) * 16);
+                        sc[i] = raw[64 * D + (i * 128 + tid) / CPR];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->raw_empty[rs]);
+                    rt++;
+#pragma unroll
+                    for (int i = 0; i < IT; i++) {
                         const int id = i * 128 + tid, r = id / CPR, ch = id % CPR;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(raw + id * 16);
-                        const uint32_t b = raw[64 * D + r];
+                        const uint32_t b = sc[i];
                         // 2^120 times the scale; 2^(b - 7) is beyond bf16 for the largest scales: the rest goes into a
                         // second product
-                        const uint32_t b1 = min(b, 134u), m1 = b == 255u ? 0x7fff7fffu : (b1 + 120u) * 0x00800080u;
+                        uint32_t m1 = (min(b, 134u) + 120u) * 0x00800080u;
+                        if (b == 255u) m1 = 0x7fff7fffu;
                         uint32_t o[8];
 #pragma unroll
                         for (int q = 0; q < 4; q++) {
-                            const uint32_t wd = reinterpret_cast<const uint32_t *>(&v)[q];
+                            const uint32_t wd = reinterpret_cast<const uint32_t *>(&v[i])[q];
                             o[2 * q] = mul_bf16x2(as_bf16(__byte_perm(wd, 0, 0x1404)), m1);
                             o[2 * q + 1] = mul_bf16x2(as_bf16(__byte_perm(wd, 0, 0x3424)), m1);
                         }
@@ -581,14 +671,12 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         *reinterpret_cast<uint4 *>(rowp + (((a + flip) ^ s) << 4)) = flip ? hi4 : lo;
                         *reinterpret_cast<uint4 *>(rowp + (((a + 1 - flip) ^ s) << 4)) = flip ? lo : hi4;
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->raw_empty[rs]);
-                    rt++;
+                    if (k0 == 64 || nv <= 64) {
+                        fence_proxy_async();  // the operand tiles are read by the tensor cores (async proxy)
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(h < 2 ? &ctl->k_full[st] : &ctl->v_full[st]);
+                    }
                 }
-                if (!ok) break;
-                fence_proxy_async();  // the operand tiles are read by the tensor cores (async proxy)
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->kv_full[st]);
             }
         }
     }

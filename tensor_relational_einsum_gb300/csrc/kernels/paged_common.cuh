@@ -21,10 +21,9 @@ __device__ __forceinline__ PgSeq load_seq(const PgTable &t, int i, int page_log2
     return s;
 }
 
-// Page number x of sequence i.  Out of range: raises the error word and
-// names page 0, so that what follows stays inside the pool.
-__device__ __forceinline__ int32_t load_page(const PgTable &t, int64_t n_pages, int i, int x, int *err) {
-    const int32_t g = __ldg(t.pages + (int64_t)i * t.page_stride + x);
+// A page number; out of range: raises the error word and names page 0, so
+// that what follows stays inside the pool.
+__device__ __forceinline__ int32_t check_page(int32_t g, int64_t n_pages, int *err) {
     if (g >= 0 && g < n_pages) return g;
     batch_fail(err);
     return 0;

@@ -4,9 +4,10 @@
 // and A = SUM e^(scale (s - m)) V.  The parts of an item are merged in the
 // order of its positions with
 //   M = max m_i,  w_i = e^(scale (m_i - M)),  O = (SUM w_i A_i) / (SUM w_i l_i),
-// so the result does not depend on which CTA was done first.  A warp takes a
-// row; lanes take D / 32 neighbouring columns.  Bound by the latency of one
-// read of the partial results, which are in L2.
+// so the result does not depend on which CTA was done first.  Bound by the
+// latency of reading the partial results, which are in L2, so all that a row
+// needs is asked for together: with few parts a warp takes two rows, with many
+// one row and eight parts at a time.
 #include "paged_common.cuh"
 
 namespace ea {
@@ -14,57 +15,127 @@ namespace {
 
 using namespace pg;
 
-constexpr int kRowsPerCta = 4;
+constexpr int kWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kRowsPerCta)
+__device__ __forceinline__ void load_acc(const float *src, int lane, float *v) {
+    if constexpr (D == 128) {
+        const float4 q = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        const float2 q = __ldcg(reinterpret_cast<const float2 *>(src) + lane);
+        v[0] = q.x; v[1] = q.y;
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void finish(const PgAttn &p, const PgSplit &sp, const PgSeq &s, const PgCut &c, int row, int lane,
+                                       float m, float l, const float *a) {
+    constexpr int C = D / 32;
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays NaN
+    const int64_t at = (int64_t)(s.first + c.item * sp.tok + row / sp.group) * p.qheads + c.head * sp.group + row % sp.group;
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int k = 0; k < C / 2; k++) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a[2 * k] * inv, a[2 * k + 1] * inv);
+        w[k] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    char *out = p.o + (at * D + lane * C) * 2;
+    if constexpr (C == 4) *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(out) = w[0];
+    if (p.m_out && lane == 0) {
+        p.m_out[at] = m * p.scale;
+        p.l_out[at] = l;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kWarps)
 cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgSplit sp, const __grid_constant__ PgWork w,
-                   int rows) {
+                   int rows, int per_cta) {
     constexpr int C = D / 32;
     const int x = blockIdx.x + 1;
     const PgCut c = w.cut[x];
     if (c.we == 0 || pg_first(c.total, c.parts, x - 1) > c.wi) return;  // not cut here, or merged by an earlier cut
     const PgSeq s = load_seq(p.t, c.seq, p.c.page_log2, p.err);
-    const int first = c.item * sp.tok;  // the item's tokens and rows
-    const int n = min(sp.tok, s.n - first) * sp.group;
-    const int row = blockIdx.y * kRowsPerCta + threadIdx.x / 32, lane = threadIdx.x & 31;
-    if (row >= n) return;
+    const int n = min(sp.tok, s.n - c.item * sp.tok) * sp.group;  // the item's rows
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int r0 = blockIdx.y * per_cta, r1 = min(n, r0 + per_cta);
+    if (r0 >= r1) return;
     // parts: the last of CTA x - 1 (its only one if the item begins with it), then the first of x, x + 1, ...
     const int slot0 = 2 * (x - 1) + (pg_first(c.total, c.parts, x - 1) < c.wi ? 1 : 0);
     int count = 1;
     while (x - 1 + count < c.parts && pg_first(c.total, c.parts, x - 1 + count) < c.we) count++;
-    auto slot = [&](int i) { return i == 0 ? slot0 : 2 * (x - 1 + i); };
-    float m = -INFINITY;
-    for (int i = lane; i < count; i += 32) m = fmaxf(m, __ldcg(&w.ml[(int64_t)slot(i) * rows + row]).x);
+    auto at = [&](int i, int row) { return (int64_t)(i == 0 ? slot0 : 2 * (x - 1 + i)) * rows + row; };
+
+    if (count <= 4) {
+        // a warp a row, two rows at a time, all parts at once
+        for (int row = r0 + 2 * warp; row < r1; row += 2 * kWarps) {
+            float2 ml[2][4];
+            float v[2][4][C];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, a[C] = {};
-#pragma unroll 4
-    for (int i = 0; i < count; i++) {
-        const int64_t at = (int64_t)slot(i) * rows + row;
-        const float2 ml = __ldcg(&w.ml[at]);
-        const float f = exp2f((ml.x - base) * p.scale_log2);
-        float v[C];
-        if constexpr (C == 4) {
-            const float4 q = __ldcg(reinterpret_cast<const float4 *>(w.acc + at * D) + lane);
-            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-        } else {
-            const float2 q = __ldcg(reinterpret_cast<const float2 *>(w.acc + at * D) + lane);
-            v[0] = q.x; v[1] = q.y;
+            for (int y = 0; y < 2; y++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    ml[y][i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (int k = 0; k < C; k++) v[y][i][k] = 0.f;
+                    if (i < count && row + y < r1) {
+                        const int64_t a = at(i, row + y);
+                        ml[y][i] = __ldcg(&w.ml[a]);
+                        load_acc<D>(w.acc + a * D, lane, v[y][i]);
+                    }
+                }
+#pragma unroll
+            for (int y = 0; y < 2; y++) {
+                if (row + y >= r1) break;
+                const float m = fmaxf(fmaxf(ml[y][0].x, ml[y][1].x), fmaxf(ml[y][2].x, ml[y][3].x));
+                const float base = m == -INFINITY ? 0.f : m;
+                float l = 0.f, a[C] = {};
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (i >= count) break;
+                    const float f = exp2f((ml[y][i].x - base) * p.scale_log2);
+                    l = fmaf(f, ml[y][i].y, l);
+#pragma unroll
+                    for (int k = 0; k < C; k++) a[k] = fmaf(f, v[y][i][k], a[k]);
+                }
+                finish<D>(p, sp, s, c, row + y, lane, m, l, a);
+            }
         }
-        l = fmaf(f, ml.y, l);
-#pragma unroll
-        for (int k = 0; k < C; k++) a[k] = fmaf(f, v[k], a[k]);
+        return;
     }
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays NaN
-    const int64_t at = (int64_t)(s.first + first + row / sp.group) * p.qheads + c.head * sp.group + row % sp.group;
-    __nv_bfloat162 *out = reinterpret_cast<__nv_bfloat162 *>(p.o + (at * D + lane * C) * 2);
+    // a warp a row, eight parts at a time
+    for (int row = r0 + warp; row < r1; row += kWarps) {
+        float m = -INFINITY;
+        for (int i = lane; i < count; i += 32) m = fmaxf(m, __ldcg(&w.ml[at(i, row)]).x);
 #pragma unroll
-    for (int k = 0; k < C / 2; k++) out[k] = __floats2bfloat162_rn(a[2 * k] * inv, a[2 * k + 1] * inv);
-    if (p.m_out && lane == 0) {
-        p.m_out[at] = m * p.scale;
-        p.l_out[at] = l;
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f, a[C] = {};
+        for (int i0 = 0; i0 < count; i0 += 8) {
+            float2 ml[8];
+            float v[8][C];
+#pragma unroll
+            for (int y = 0; y < 8; y++) {
+                const int i = i0 + y;
+                ml[y] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int k = 0; k < C; k++) v[y][k] = 0.f;
+                if (i < count) {
+                    ml[y] = __ldcg(&w.ml[at(i, row)]);
+                    load_acc<D>(w.acc + at(i, row) * D, lane, v[y]);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < 8; y++) {
+                const float f = exp2f((ml[y].x - base) * p.scale_log2);
+                l = fmaf(f, ml[y].y, l);
+#pragma unroll
+                for (int k = 0; k < C; k++) a[k] = fmaf(f, v[y][k], a[k]);
+            }
+        }
+        finish<D>(p, sp, s, c, row, lane, m, l, a);
     }
 }
 
@@ -73,9 +144,10 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgS
 cudaError_t launch_cache_merge(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st) {
     if (pl.ctas < 2) return cudaSuccess;
     const PgWork w = pg_work(pl, p.c.dim, ws);
-    const dim3 grid(pl.ctas - 1, (pl.rows + kRowsPerCta - 1) / kRowsPerCta);
-    if (p.c.dim == 64) cache_merge_kernel<64><<<grid, 32 * kRowsPerCta, 0, st>>>(p, pl.split, w, pl.rows);
-    else cache_merge_kernel<128><<<grid, 32 * kRowsPerCta, 0, st>>>(p, pl.split, w, pl.rows);
+    const int per = pl.rows <= kPgTokenRows ? kWarps : 4 * kWarps;  // CTAs without a cut cost too: not many of them
+    const dim3 grid(pl.ctas - 1, (pl.rows + per - 1) / per);
+    if (p.c.dim == 64) cache_merge_kernel<64><<<grid, 32 * kWarps, 0, st>>>(p, pl.split, w, pl.rows, per);
+    else cache_merge_kernel<128><<<grid, 32 * kWarps, 0, st>>>(p, pl.split, w, pl.rows, per);
     return cudaGetLastError();
 }
 

@@ -78,8 +78,10 @@ struct Seqs {
     __device__ __forceinline__ int count() const { return t.n_seqs; }
 };
 
-// Say where this CTA's share begins, if that is inside an item.
+// Say where this CTA's share begins, if that is inside an item (no workspace:
+// the plan cuts no item).
 __device__ __forceinline__ void note_cut(const PgWork &w, const PgShare &sh, const PgWalk &k) {
+    if (!w.cut) return;
     PgCut c{};
     c.total = sh.total;
     c.parts = sh.parts;

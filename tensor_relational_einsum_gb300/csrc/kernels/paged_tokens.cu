@@ -108,7 +108,7 @@ struct Loader {
     PgWalk w;
     int block, last;  // next block of the part, and its first one beyond
     int end;          // keys of the item
-    int page;         // page of this warp's keys of the next block
+    int page;         // page of this warp's keys of the next block, not checked yet: nothing waits for it here
     bool more;
 
     __device__ __forceinline__ void enter(const PgAttn &p, const PgSplit &sp, int warp) {
@@ -125,14 +125,14 @@ struct Loader {
     }
     __device__ __forceinline__ void look(const PgAttn &p, int warp) {
         const int key0 = block * kBlock + warp * 16;
-        page = more && key0 < end ? load_page(p.t, p.c.n_pages, w.seq, key0 >> p.c.page_log2, p.err) : 0;
+        page = more && key0 < end ? __ldg(p.t.pages + (int64_t)w.seq * p.t.page_stride + (key0 >> p.c.page_log2)) : 0;
     }
     __device__ __forceinline__ void issue(const PgAttn &p, const PgSplit &sp, uint32_t stage, uint32_t scales, int warp,
                                           int lane) {
         if (!more) return;
         const int key0 = block * kBlock + warp * 16, nv = end - key0;  // valid keys: the rest becomes zero
         if (nv > 0) {
-            const int64_t vec = pg_vec(p.c, page, w.head, key0 & ((1 << p.c.page_log2) - 1));
+            const int64_t vec = pg_vec(p.c, check_page(page, p.c.n_pages, p.err), w.head, key0 & ((1 << p.c.page_log2) - 1));
             const uint32_t ks = stage + warp * 2 * C::TILE, vs = ks + C::TILE;
             const char *kp = p.c.k + vec * C::ROWB, *vp = p.c.v + vec * C::ROWB;
             constexpr int CPR = C::ROWB / 16;  // chunks of a row
@@ -513,16 +513,16 @@ PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causa
     sp.kt = longest <= 512 ? 512 : kBlock;
     const int64_t units = (longest + sp.kt - 1) / sp.kt * t.n_seqs * c.heads;
     pl.ctas = (int)std::min<int64_t>(units, (int64_t)num_sms * 2);
-    pl.bytes = pg_work_bytes(pl.ctas, pl.rows, c.dim);
+    pl.bytes = units > t.n_seqs * (int64_t)c.heads ? pg_work_bytes(pl.ctas, pl.rows, c.dim) : 0;  // 0: a unit is an item
     return pl;
 }
 
 cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st) {
-    const PgWork w = pg_work(pl, p.c.dim, ws);
+    const PgWork w = pl.bytes ? pg_work(pl, p.c.dim, ws) : PgWork{};
     cudaError_t e;
     if (p.c.fmt == EA_CACHE_E4M3) e = p.c.dim == 64 ? launch_m<64, true>(p, pl, w, st) : launch_m<128, true>(p, pl, w, st);
     else e = p.c.dim == 64 ? launch_m<64, false>(p, pl, w, st) : launch_m<128, false>(p, pl, w, st);
-    if (e != cudaSuccess || pl.split.kt > kBlock) return e;
+    if (e != cudaSuccess || !pl.bytes) return e;
     return launch_cache_merge(p, pl, ws, st);
 }
 
