@@ -245,7 +245,7 @@ AttnPlans plans_of(const ea_cache_s *cache, const ea_page_batch *batch, int64_t 
     a.tokens = plan_cache_tokens(t, pool_of(cache), group, causal, cache->num_sms);
     a.chunks = plan_cache_chunks(t, pool_of(cache), group, causal, cache->num_sms,
                                  a.tokens.ctas ? a.tokens.split.max_rows + 1 : 1);
-    a.bytes = std::max(a.tokens.bytes, a.chunks.bytes);  // one after the other on the stream
+    a.bytes = a.tokens.bytes + a.chunks.bytes;
     return a;
 }
 
@@ -346,22 +346,34 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
         const AttnPlans a = plans_of(cache, batch, rows, heads, p.causal);
         if (a.bytes > 0 && (!o.workspace || o.workspace_bytes < a.bytes || ((uintptr_t)o.workspace & 15) != 0))
             return set_error(EA_ERR_ARG, "ea_cache_attention: workspace of %zu bytes, 16-byte aligned, needed", a.bytes);
+        // chunks, tokens, merge: the tokens' CTAs fill the SMs that the chunks' leave
+        char *ws = (char *)o.workspace;
+        const PgWork wc = pg_work(a.chunks, ws), wt = pg_work(a.tokens, ws + a.chunks.bytes);
         int64_t ctas = 0;
         int launches = 0;
-        if (a.tokens.ctas > 0) {
-            cudaError_t e = launch_cache_tokens(p, a.tokens, o.workspace, (cudaStream_t)stream);
-            if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
-            ctas += a.tokens.ctas;
-            launches += 1;
-        }
+        cudaError_t e = cudaSuccess;
         if (a.chunks.ctas > 0) {
             PgMaps maps;
             s = chunk_maps(c, cache, q, heads, rows, a.chunks.split, &maps);
             if (s) return s;
-            cudaError_t e = launch_cache_chunks(p, a.chunks, maps, o.workspace, (cudaStream_t)stream);
+            e = launch_cache_chunks(p, a.chunks, maps, wc, (cudaStream_t)stream);
             if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
             ctas += a.chunks.ctas;
-            launches += 1;
+            launches++;
+        }
+        if (a.tokens.ctas > 0) {
+            e = launch_cache_tokens(p, a.tokens, wt, launches > 0, (cudaStream_t)stream);
+            if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
+            ctas += a.tokens.ctas;
+            launches++;
+        }
+        PgMerge m{{wc, wt}, {a.chunks.split, a.tokens.split}, {wc.cut ? a.chunks.ctas - 1 : 0, wt.cut ? a.tokens.ctas - 1 : 0},
+                  {a.chunks.rows, a.tokens.rows}};
+        if (m.cuts[0] + m.cuts[1] > 0) {
+            e = launch_cache_merge(p, m, (cudaStream_t)stream);
+            if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
+            ctas += m.cuts[0] + m.cuts[1];
+            launches++;
         }
         note_launch(kCacheAttention, launches, ctas);
         return EA_OK;

@@ -201,6 +201,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     }
     if (warp == 9) tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
     tc_fence_before();
+    let_next_start();
     take_share<R::THREADS>(p.t, sp, p.c.page_log2, p.err, ctl->scan, &ctl->share);
     __syncthreads();
     tc_fence_after();
@@ -734,13 +735,9 @@ PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causa
     return pl;
 }
 
-cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, void *ws, cudaStream_t st) {
-    const PgWork w = pg_work(pl, p.c.dim, ws);
-    cudaError_t e;
-    if (p.c.fmt == EA_CACHE_E4M3) e = p.c.dim == 64 ? launch<64, true>(p, pl, w, maps, st) : launch<128, true>(p, pl, w, maps, st);
-    else e = p.c.dim == 64 ? launch<64, false>(p, pl, w, maps, st) : launch<128, false>(p, pl, w, maps, st);
-    if (e != cudaSuccess) return e;
-    return launch_cache_merge(p, pl, ws, st);
+cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, const PgWork &w, cudaStream_t st) {
+    if (p.c.fmt == EA_CACHE_E4M3) return p.c.dim == 64 ? launch<64, true>(p, pl, w, maps, st) : launch<128, true>(p, pl, w, maps, st);
+    return p.c.dim == 64 ? launch<64, false>(p, pl, w, maps, st) : launch<128, false>(p, pl, w, maps, st);
 }
 
 }  // namespace ea

@@ -21,6 +21,30 @@ __device__ __forceinline__ PgSeq load_seq(const PgTable &t, int i, int page_log2
     return s;
 }
 
+// The kernels of an attention call overlap at their ends (programmatic
+// dependent launch): each lets the next be placed as soon as it runs, and
+// waits for the one before it to be complete, at the latest before it ends
+// itself, so that the last one's end is the end of all.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch behind the stream's last kernel; `early`: it may be placed before
+// that one has ended (the kernel calls wait_for_previous).
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool early, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // A page number; out of range: raises the error word and names page 0, so
 // that what follows stays inside the pool.
 __device__ __forceinline__ int32_t check_page(int32_t g, int64_t n_pages, int *err) {

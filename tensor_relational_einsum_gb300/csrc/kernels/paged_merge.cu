@@ -8,6 +8,8 @@
 // latency of reading the partial results, which are in L2, so all that a row
 // needs is asked for together: with few parts a warp takes two rows, with many
 // one row and eight parts at a time.
+#include <algorithm>
+
 #include "paged_common.cuh"
 
 namespace ea {
@@ -16,6 +18,7 @@ namespace {
 using namespace pg;
 
 constexpr int kWarps = 8;
+constexpr int kRowsPerCta = 32;  // a CTA without a cut costs too: not too many of them
 
 template <int D>
 __device__ __forceinline__ void load_acc(const float *src, int lane, float *v) {
@@ -51,16 +54,22 @@ __device__ __forceinline__ void finish(const PgAttn &p, const PgSplit &sp, const
 
 template <int D>
 __global__ void __launch_bounds__(32 * kWarps)
-cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgSplit sp, const __grid_constant__ PgWork w,
-                   int rows, int per_cta) {
+cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgMerge mg) {
     constexpr int C = D / 32;
-    const int x = blockIdx.x + 1;
+    // the cuts of the first kernel, then those of the second
+    const int k = (int)blockIdx.x < mg.cuts[0] ? 0 : 1;
+    const int x = blockIdx.x - (k ? mg.cuts[0] : 0) + 1;
+    const PgWork &w = mg.w[k];
+    const PgSplit &sp = mg.split[k];
+    const int rows = mg.rows[k];
+    if ((int)blockIdx.y * kRowsPerCta >= rows) return;
+    wait_for_previous();
     const PgCut c = w.cut[x];
     if (c.we == 0 || pg_first(c.total, c.parts, x - 1) > c.wi) return;  // not cut here, or merged by an earlier cut
     const PgSeq s = load_seq(p.t, c.seq, p.c.page_log2, p.err);
     const int n = min(sp.tok, s.n - c.item * sp.tok) * sp.group;  // the item's rows
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int r0 = blockIdx.y * per_cta, r1 = min(n, r0 + per_cta);
+    const int r0 = blockIdx.y * kRowsPerCta, r1 = min(n, r0 + kRowsPerCta);
     if (r0 >= r1) return;
     // parts: the last of CTA x - 1 (its only one if the item begins with it), then the first of x, x + 1, ...
     const int slot0 = 2 * (x - 1) + (pg_first(c.total, c.parts, x - 1) < c.wi ? 1 : 0);
@@ -141,14 +150,10 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgS
 
 }  // namespace
 
-cudaError_t launch_cache_merge(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st) {
-    if (pl.ctas < 2) return cudaSuccess;
-    const PgWork w = pg_work(pl, p.c.dim, ws);
-    const int per = pl.rows <= kPgTokenRows ? kWarps : 4 * kWarps;  // CTAs without a cut cost too: not many of them
-    const dim3 grid(pl.ctas - 1, (pl.rows + per - 1) / per);
-    if (p.c.dim == 64) cache_merge_kernel<64><<<grid, 32 * kWarps, 0, st>>>(p, pl.split, w, pl.rows, per);
-    else cache_merge_kernel<128><<<grid, 32 * kWarps, 0, st>>>(p, pl.split, w, pl.rows, per);
-    return cudaGetLastError();
+cudaError_t launch_cache_merge(const PgAttn &p, const PgMerge &m, cudaStream_t st) {
+    const dim3 grid(m.cuts[0] + m.cuts[1], (std::max(m.rows[0], m.rows[1]) + kRowsPerCta - 1) / kRowsPerCta);
+    if (p.c.dim == 64) return launch_after(cache_merge_kernel<64>, grid, 32 * kWarps, 0, st, true, p, m);
+    return launch_after(cache_merge_kernel<128>, grid, 32 * kWarps, 0, st, true, p, m);
 }
 
 }  // namespace ea

@@ -169,12 +169,16 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     __shared__ float4 s_ml[4][16 * MT];  // a warp's reference maximum, sum, maximum of its rows
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+    let_next_start();
     take_share<kThreads>(p.t, sp, p.c.page_log2, p.err, scan, &share);
     Loader<D, E4M3, MT> ld;
     ld.w.begin(share, sp, Seqs{p.t, p.c.page_log2, p.err});
     PgWalk w = ld.w;
     if (threadIdx.x == 0) note_cut(ws, share, w);
-    if (share.count == 0) return;
+    if (share.count == 0) {
+        wait_for_previous();
+        return;
+    }
     ld.enter(p, sp, warp);
 #pragma unroll
     for (int s = 0; s < C::S - 1; s++) {
@@ -472,10 +476,11 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         w.step(np, sp, Seqs{p.t, p.c.page_log2, p.err});
     }
     cp_wait<0>();
+    wait_for_previous();
 }
 
 template <int D, bool E4M3, int MT>
-cudaError_t launch(const PgAttn &p, const PgPlan &pl, const PgWork &w, cudaStream_t st) {
+cudaError_t launch(const PgAttn &p, const PgPlan &pl, const PgWork &w, cudaStream_t st, bool early) {
     using C = Cfg<D, E4M3, MT>;
     static bool configured[64] = {};
     int dev = 0;
@@ -486,13 +491,12 @@ cudaError_t launch(const PgAttn &p, const PgPlan &pl, const PgWork &w, cudaStrea
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    cache_tokens_kernel<D, E4M3, MT><<<pl.ctas, kThreads, C::SMEM, st>>>(p, pl.split, w);
-    return cudaGetLastError();
+    return launch_after(cache_tokens_kernel<D, E4M3, MT>, dim3(pl.ctas), kThreads, C::SMEM, st, early, p, pl.split, w);
 }
 
 template <int D, bool E4M3>
-cudaError_t launch_m(const PgAttn &p, const PgPlan &pl, const PgWork &w, cudaStream_t st) {
-    return pl.rows == 16 ? launch<D, E4M3, 1>(p, pl, w, st) : launch<D, E4M3, 2>(p, pl, w, st);
+cudaError_t launch_m(const PgAttn &p, const PgPlan &pl, const PgWork &w, cudaStream_t st, bool early) {
+    return pl.rows == 16 ? launch<D, E4M3, 1>(p, pl, w, st, early) : launch<D, E4M3, 2>(p, pl, w, st, early);
 }
 
 }  // namespace
@@ -517,13 +521,10 @@ PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causa
     return pl;
 }
 
-cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st) {
-    const PgWork w = pl.bytes ? pg_work(pl, p.c.dim, ws) : PgWork{};
-    cudaError_t e;
-    if (p.c.fmt == EA_CACHE_E4M3) e = p.c.dim == 64 ? launch_m<64, true>(p, pl, w, st) : launch_m<128, true>(p, pl, w, st);
-    else e = p.c.dim == 64 ? launch_m<64, false>(p, pl, w, st) : launch_m<128, false>(p, pl, w, st);
-    if (e != cudaSuccess || !pl.bytes) return e;
-    return launch_cache_merge(p, pl, ws, st);
+cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, const PgWork &w, bool early, cudaStream_t st) {
+    if (p.c.fmt == EA_CACHE_E4M3)
+        return p.c.dim == 64 ? launch_m<64, true>(p, pl, w, st, early) : launch_m<128, true>(p, pl, w, st, early);
+    return p.c.dim == 64 ? launch_m<64, false>(p, pl, w, st, early) : launch_m<128, false>(p, pl, w, st, early);
 }
 
 }  // namespace ea

@@ -98,17 +98,17 @@ struct PgPlan {                  // a kernel of the call and its grid
     PgSplit split;
     int32_t ctas;                // 0: not launched
     int32_t rows;                // rows of an item
-    int32_t variant;
-    size_t bytes;                // workspace
+    size_t bytes;                // workspace; 0: no item is cut
 };
 
 // Workspace of a plan, and its parts in it.
 inline size_t pg_work_bytes(int ctas, int rows, int dim) {
     const size_t n = (size_t)2 * ctas * rows;
-    return ((size_t)ctas * sizeof(PgCut) + 255) / 256 * 256 + (n * sizeof(float2) + 255) / 256 * 256 + n * dim * sizeof(float);
+    return ((size_t)ctas * sizeof(PgCut) + 255) / 256 * 256 + (n * sizeof(float2) + 255) / 256 * 256 +
+           (n * dim * sizeof(float) + 255) / 256 * 256;
 }
-inline PgWork pg_work(const PgPlan &pl, int dim, void *ws) {
-    char *b = (char *)ws;
+inline PgWork pg_work(const PgPlan &pl, char *b) {
+    if (pl.bytes == 0) return PgWork{};
     const size_t cut = ((size_t)pl.ctas * sizeof(PgCut) + 255) / 256 * 256;
     const size_t ml = ((size_t)2 * pl.ctas * pl.rows * sizeof(float2) + 255) / 256 * 256;
     return PgWork{(PgCut *)b, (float2 *)(b + cut), (float *)(b + cut + ml)};
@@ -117,14 +117,22 @@ inline PgWork pg_work(const PgPlan &pl, int dim, void *ws) {
 // Token kernel: few rows a sequence, bound by reading the pages.
 constexpr int kPgTokenRows = 32;     // the most rows of a sequence (tokens x group) that it takes
 PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causal, int num_sms);
-cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st);
-cudaError_t launch_cache_merge(const PgAttn &p, const PgPlan &pl, void *ws, cudaStream_t st);
+cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, const PgWork &w, bool early, cudaStream_t st);
 // Chunk kernel: tiles of 128 rows on the tensor cores.
 struct PgMaps {                  // tensor maps: Q's rows; the pools as [vectors][dim] (bf16)
     CUtensorMap q, k, v;
 };
 PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causal, int num_sms, int min_rows);
-cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, void *ws, cudaStream_t st);
+cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, const PgWork &w, cudaStream_t st);
+
+// The merge of both kernels' cut items.
+struct PgMerge {
+    PgWork w[2];
+    PgSplit split[2];
+    int32_t cuts[2];             // CTAs - 1; 0: none
+    int32_t rows[2];
+};
+cudaError_t launch_cache_merge(const PgAttn &p, const PgMerge &m, cudaStream_t st);
 
 // ------------------------------------------------------------- sequences
 
