@@ -20,14 +20,18 @@
 // and output over its keys (the merge of (m, l, A) triples is associative),
 // and the four are merged through shared memory at the end of a part.
 //
-// 8-bit cells become bf16 in registers: sign and the 7 other bits moved to
-// bf16's places give value * 2^-120 (exponent biases 7 and 127; subnormals
-// too), one exact product with 2^120 puts that right.  The bytes of a 32-bit
-// word go to the fragments as pairs (0, 2) and (1, 3), the pairs that masks
-// and shifts give without a byte permutation: for the scores that is a fixed
-// order of the contracted dimension, applied to Q once; for the output it
-// only says which column an accumulator holds.  K's scales multiply the
-// scores' columns, V's the probabilities, both exact powers of two.
+// 8-bit cells become f16 in registers, two with one conversion (a code is an
+// f16 value exactly), and that is all that is done to them: 4 integer
+// instructions a pair, as the way to bf16 takes, bound this kernel at 3.5
+// TB/s.  The scales go where there is less to multiply: K's to the columns of
+// the scores, V's to the probabilities.  What f16 lacks is range, so
+//   - Q's rows are brought to [2^14, 2^15) by a power of two (a bf16 value is
+//     an f16 value down to 2^-28 of its row's largest, and 2^-39 of it is the
+//     step below);
+//   - a probability enters as p * 2^7 * 2^(v - vref), v its key's scale and
+//     vref the largest that the warp has met: 11 bits down to 2^-21 of the
+//     row's largest term, steps of 2^-31 of it below that.
+// Powers of two cost nothing in exactness: the f16 products are exact in fp32.
 #include "attn_common.cuh"
 #include "paged_sched.cuh"
 
@@ -54,10 +58,11 @@ struct Cfg {
     static constexpr int CTAS = 2;
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on) {
-    const int n = on ? 16 : 0;  // 0: the 16 bytes become zero, nothing is read
+// n bytes, and zeros up to 16.
+__device__ __forceinline__ void cp16n(uint32_t dst, const void *src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on) { cp16n(dst, src, on ? 16 : 0); }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -80,15 +85,28 @@ __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, ui
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Bytes 1 and 3 of w, e4m3, as two bf16 values.
-__device__ __forceinline__ uint32_t odd_bf16(uint32_t w) {
-    const uint32_t y = ((w & 0x7f007f00u) >> 4) | (w & 0x80008000u);
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));  // 2^120
-    return r;
+__device__ __forceinline__ void mma16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Bytes 0 and 2.
-__device__ __forceinline__ uint32_t even_bf16(uint32_t w) { return odd_bf16(w << 8); }
+
+// Four e4m3 bytes as f16: bytes 0 and 1, bytes 2 and 3.
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// 2^e for -126 <= e <= 127; 0 below.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)max(e + 127, 0) << 23); }
 
 // Byte offset of 16-byte chunk c of row r in a warp's tile.  bf16, and V's
 // 8-bit cells: ldmatrix reads one chunk of 8 rows, which must lie in 8
@@ -146,7 +164,7 @@ struct Loader {
                 const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
                 cp16(vs + chunk_at<C::ROWB, false>(r, c), vp + x * 16, r < nv);
             }
-            if (E4M3 && lane < 2) cp16(scales + warp * 32 + lane * 16, (lane ? p.c.vs : p.c.ks) + vec, true);
+            if (E4M3 && lane < 2) cp16n(scales + warp * 32 + lane * 16, (lane ? p.c.vs : p.c.ks) + vec, min(16, nv));
         }
         if (++block < last) {
             look(p, warp);
@@ -166,7 +184,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PgShare share;
     __shared__ int64_t scan[kThreads / 32];
-    __shared__ float4 s_ml[4][16 * MT];  // a warp's reference maximum, sum, maximum of its rows
+    __shared__ float4 s_ml[4][16 * MT];  // a warp's reference maximum, sum, maximum of its rows; unit of its output
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     let_next_start();
@@ -197,6 +215,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         const int tok0 = w.item * sp.tok, nrows = min(sp.tok, w.s.n - tok0) * sp.group;
         // Q's fragments, and the keys that each of the thread's rows keeps
         uint32_t q[MT][KS][4];
+        float qs[MT][2];  // e4m3: a score in units of the row's scaled Q, times this, is the score
         int lim[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; m++)
@@ -208,21 +227,35 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 const char *src = p.q + ((int64_t)(w.s.first + (in ? tok : 0)) * p.qheads + w.head * sp.group +
                                          (in ? r % sp.group : 0)) * D * 2;
                 if constexpr (E4M3) {
-                    // logical k = (2 t, 2 t + 1, 2 t + 8, 2 t + 9) of step 4 x + s: columns 64 x + 16 t + 4 s + (0, 2, 1, 3)
+                    // logical k = (2 t, 2 t + 1, 2 t + 8, 2 t + 9) of step 4 x + s: columns 64 x + 16 t + 4 s + (0, 1, 2, 3)
+                    uint32_t u[D / 64][8] = {};
+                    uint32_t big = 0;  // the row's largest magnitude: bf16 bits
 #pragma unroll
                     for (int x = 0; x < D / 64; x++) {
-                        uint4 v[2] = {};
                         if (in) {
-                            v[0] = __ldg(reinterpret_cast<const uint4 *>(src + (64 * x + 16 * tig) * 2));
-                            v[1] = __ldg(reinterpret_cast<const uint4 *>(src + (64 * x + 16 * tig) * 2) + 1);
+                            const uint4 *g = reinterpret_cast<const uint4 *>(src + (64 * x + 16 * tig) * 2);
+                            *reinterpret_cast<uint4 *>(u[x]) = __ldg(g);
+                            *reinterpret_cast<uint4 *>(u[x] + 4) = __ldg(g + 1);
                         }
-                        const uint32_t *u = reinterpret_cast<const uint32_t *>(v);
 #pragma unroll
-                        for (int s = 0; s < 4; s++) {
-                            q[m][4 * x + s][h] = __byte_perm(u[2 * s], u[2 * s + 1], 0x5410);
-                            q[m][4 * x + s][h + 2] = __byte_perm(u[2 * s], u[2 * s + 1], 0x7632);
-                        }
+                        for (int i = 0; i < 8; i++) big = __vmaxu2(big, u[x][i] & 0x7fff7fffu);
                     }
+                    big = max(big >> 16, big & 0xffffu);
+                    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                    big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    const int e = big == 0 || big >= 0x7f80u ? 0 : min(126, 14 - ((int)(big >> 7) - 127));
+                    const float up = pow2(e);
+                    qs[m][h] = pow2(-e);
+#pragma unroll
+                    for (int x = 0; x < D / 64; x++)
+#pragma unroll
+                        for (int s = 0; s < 4; s++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++) {
+                                const uint32_t w = u[x][2 * s + i];
+                                q[m][4 * x + s][h + 2 * i] =
+                                    pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+                            }
                 } else {
 #pragma unroll
                     for (int s = 0; s < KS; s++)
@@ -239,7 +272,9 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             for (int h = 0; h < 2; h++) {
                 mref[m][h] = mmax[m][h] = -INFINITY;
                 l[m][h] = 0.f;
+                if constexpr (!E4M3) qs[m][h] = 1.f;
             }
+        int vref = 0;  // e4m3: the accumulators are in units of 2^(vref - 127 - 7)
 
         for (int b = b0; b < b1; b++) {
             __syncwarp();  // every lane has read the slot that is filled next
@@ -263,9 +298,10 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                                          : "r"(kt + chunk_at<C::ROWB, true>(n * 8 + gid, 4 * x + tig)));
 #pragma unroll
                             for (int y = 0; y < 4; y++) {
-                                const uint32_t e = even_bf16(u[y]), d = odd_bf16(u[y]);
+                                uint32_t lo, hi;
+                                to_f16(u[y], lo, hi);
 #pragma unroll
-                                for (int m = 0; m < MT; m++) mma(s[m][n], q[m][4 * x + y], e, d);
+                                for (int m = 0; m < MT; m++) mma16(s[m][n], q[m][4 * x + y], lo, hi);
                             }
                         }
                 } else {
@@ -280,16 +316,34 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         }
                     }
                 }
-                float vsc[2][2];
+                float vsc[2][2];    // what V's scales make of the probabilities
+                float shift = 1.f;  // what a new vref makes of the accumulators
                 if constexpr (E4M3) {
                     const uint8_t *sc = smem + C::S * C::STAGE + slot * 128 + warp * 32;
+                    // bytes of keys beyond the end are 0 here; NaN vectors (255) do not move vref
+                    const uint4 all = *reinterpret_cast<const uint4 *>(sc + 16);
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint32_t w = reinterpret_cast<const uint32_t *>(&all)[i];
+                        top = __vmaxu4(top, w & ~__vcmpeq4(w, 0xffffffffu));
+                    }
+                    top = __vmaxu4(top, top >> 16);
+                    const int vmax = (int)max(top & 255u, (top >> 8) & 255u);
+                    if (vmax > vref) {
+                        shift = pow2(vref - vmax);
+                        vref = vmax;
+                    }
 #pragma unroll
                     for (int n = 0; n < 2; n++) {
                         const uint32_t kb = *reinterpret_cast<const uint16_t *>(sc + n * 8 + 2 * tig);
                         const uint32_t vb = *reinterpret_cast<const uint16_t *>(sc + 16 + n * 8 + 2 * tig);
                         const float k0 = scale_value(kb & 255u), k1 = scale_value(kb >> 8);
-                        vsc[n][0] = scale_value(vb & 255u);
-                        vsc[n][1] = scale_value(vb >> 8);
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            const uint32_t v = (vb >> (8 * i)) & 255u;
+                            vsc[n][i] = v == 255u ? __uint_as_float(0x7fffffffu) : pow2((int)v - vref + 7);
+                        }
 #pragma unroll
                         for (int m = 0; m < MT; m++)
 #pragma unroll
@@ -319,15 +373,17 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     bool move = false;
 #pragma unroll
                     for (int h = 0; h < 2; h++)
-                        move |= mx[h] != -INFINITY && (mref[m][h] == -INFINITY || (mx[h] - mref[m][h]) * c > kLazy);
+                        move |= mx[h] != -INFINITY && (mref[m][h] == -INFINITY || (mx[h] - mref[m][h]) * (c * qs[m][h]) > kLazy);
+                    if constexpr (E4M3) move |= shift != 1.f;
                     if (__any_sync(0xffffffffu, move)) {
                         float f[2];
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
                             const float to = mmax[m][h];
-                            f[h] = mref[m][h] == -INFINITY ? 0.f : ex2((mref[m][h] - to) * c);
+                            f[h] = mref[m][h] == -INFINITY ? 0.f : ex2((mref[m][h] - to) * (c * qs[m][h]));
                             mref[m][h] = to;
                             l[m][h] *= f[h];
+                            if constexpr (E4M3) f[h] *= shift;
                         }
 #pragma unroll
                         for (int n = 0; n < NT; n++) {
@@ -339,12 +395,12 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     }
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const float nb = mref[m][h] == -INFINITY ? 0.f : -mref[m][h] * c;
+                        const float cq = c * qs[m][h], nb = mref[m][h] == -INFINITY ? 0.f : -mref[m][h] * cq;
                         float e[2][2];
 #pragma unroll
                         for (int n = 0; n < 2; n++)
 #pragma unroll
-                            for (int i = 0; i < 2; i++) e[n][i] = ex2(fmaf(s[m][n][2 * h + i], c, nb));
+                            for (int i = 0; i < 2; i++) e[n][i] = ex2(fmaf(s[m][n][2 * h + i], cq, nb));
                         l[m][h] += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
                         if constexpr (E4M3) {
 #pragma unroll
@@ -353,8 +409,8 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                                 for (int i = 0; i < 2; i++)  // a dropped key's scale byte may hold anything
                                     e[n][i] = e[n][i] == 0.f ? 0.f : e[n][i] * vsc[n][i];
                         }
-                        pf[m][h] = pack_bf16(e[0][0], e[0][1]);
-                        pf[m][h + 2] = pack_bf16(e[1][0], e[1][1]);
+                        pf[m][h] = E4M3 ? pack_f16(e[0][0], e[0][1]) : pack_bf16(e[0][0], e[0][1]);
+                        pf[m][h + 2] = E4M3 ? pack_f16(e[1][0], e[1][1]) : pack_bf16(e[1][0], e[1][1]);
                     }
                 }
                 if constexpr (E4M3) {
@@ -364,12 +420,14 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         ldsm4_t(vt + chunk_at<C::ROWB, false>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * x + (lane >> 4)), u);
 #pragma unroll
                         for (int y = 0; y < 2; y++) {
-                            const uint32_t e0 = even_bf16(u[2 * y]), e1 = even_bf16(u[2 * y + 1]);
-                            const uint32_t d0 = odd_bf16(u[2 * y]), d1 = odd_bf16(u[2 * y + 1]);
+                            // keys (2 t, 2 t + 1) of two neighbouring columns: by column, then to f16
+                            uint32_t e0, e1, d0, d1;
+                            to_f16(__byte_perm(u[2 * y], 0, 0x3120), e0, d0);
+                            to_f16(__byte_perm(u[2 * y + 1], 0, 0x3120), e1, d1);
 #pragma unroll
                             for (int m = 0; m < MT; m++) {
-                                mma(o[m][4 * x + 2 * y], pf[m], e0, e1);
-                                mma(o[m][4 * x + 2 * y + 1], pf[m], d0, d1);
+                                mma16(o[m][4 * x + 2 * y], pf[m], e0, e1);
+                                mma16(o[m][4 * x + 2 * y + 1], pf[m], d0, d1);
                             }
                         }
                     }
@@ -397,7 +455,8 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             for (int h = 0; h < 2; h++) {
                 l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 1);
                 l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 2);
-                if (tig == 0) s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h], l[m][h], mmax[m][h], 0.f);
+                if (tig == 0) s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h] * qs[m][h], l[m][h], mmax[m][h] * qs[m][h],
+                                                                         E4M3 ? ldexpf(1.f, vref - 127 - 7) : 1.f);
             }
         const bool whole = w.u0 == 0 && np == w.units;
         const int64_t part = 2 * (int64_t)blockIdx.x + (first_part ? 0 : 1);
@@ -437,6 +496,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     const float4 v = s_ml[i][r];
                     f[i] = v.x == -INFINITY ? 0.f : ex2((v.x - top) * c);
                     sum = fmaf(f[i], v.y, sum);
+                    if constexpr (E4M3) f[i] *= v.w;
                 }
                 if (r < nrows) {
                     const int64_t at = ((int64_t)(w.s.first + tok0 + r / sp.group) * p.qheads + w.head * sp.group + r % sp.group);
