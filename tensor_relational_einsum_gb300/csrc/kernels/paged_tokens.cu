@@ -6,13 +6,14 @@
 // the kernel: 2 bytes (1 byte) of a cell against 64 flops, an eighth of what
 // the tensor cores could do meanwhile.  What it needs is bytes in flight on
 // every SM all the time, so
-//   - the units of all items (64 keys of one key-value head) are shared out
-//     evenly over the CTAs, whatever the lengths are (paged.h);
-//   - a warp owns 16 keys of each 64-key block and loads them itself with
-//     16-byte cp.async into its part of a ring of blocks: no barrier between
-//     warps inside an item, the next blocks' loads run across items;
+//   - the units of all items (a block of 64 or 128 keys of one key-value head)
+//     are shared out evenly over the CTAs, whatever the lengths are (paged.h);
+//   - a warp owns one or two runs of 16 keys of each block and loads them
+//     itself with 16-byte cp.async into its part of a ring of blocks: no
+//     barrier between warps inside an item, the next blocks' loads run across
+//     items;
 //   - 16 keys lie in one page (pages hold a multiple of 16 positions), so a
-//     warp needs one page number a block, read one block ahead.
+//     run needs one page number, read one block ahead.
 // The products run on mma.sync m16n8k16: its 16-row tile is what a group of
 // heads fills (a tcgen05 tile has 128 rows), and the accumulators stay in the
 // warp's registers, next to the softmax.  The rows of an item are its tokens
@@ -43,18 +44,22 @@ using attn::ex2;
 using attn::pack_bf16;
 
 constexpr int kThreads = 128;
-constexpr int kBlock = 64;     // keys of a block: 16 a warp
 constexpr float kLazy = 8.f;   // a running maximum moves when it is exceeded by this much (log2): P stays below 2^8
 
 template <int D, bool E4M3, int MT>
 struct Cfg {
     static constexpr int CELL = E4M3 ? 1 : 2;
     static constexpr int ROWB = D * CELL;               // bytes of a key's vector
-    static constexpr int TILE = 16 * ROWB;              // a warp's K (or V) of a block
+    // A warp takes G runs of 16 keys of a block: two where a run is 4 KB at most, because the waits, votes and
+    // shuffles of a block cost the same for both and the products of one run fill the latencies of the other's.
+    // (Two tiles of rows at D = 128 leave no registers for it.)
+    static constexpr int G = ROWB == 256 || (D == 128 && MT == 2) ? 1 : 2;
+    static constexpr int BLOCK = 64 * G;                // keys of a block
+    static constexpr int TILE = 16 * G * ROWB;          // a warp's K (or V) of a block
     static constexpr int STAGE = 4 * 2 * TILE;          // a block
-    static constexpr int S = E4M3 ? 4 : D == 64 ? 5 : 3;
-    static constexpr int SCALES = E4M3 ? S * 4 * 32 : 0;  // 16 bytes of K and of V a warp and stage
-    static constexpr int SMEM = S * STAGE + SCALES;
+    static constexpr int S = STAGE == 16384 ? 5 : 3;
+    static constexpr int SCALES = E4M3 ? 4 * 2 * 16 * G : 0;  // a stage's scale bytes
+    static constexpr int SMEM = S * (STAGE + SCALES);
     static constexpr int CTAS = 2;
 };
 
@@ -79,14 +84,14 @@ __device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t *r) {
                  : "r"(a));
 }
 __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void mma16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -126,15 +131,15 @@ struct Loader {
     PgWalk w;
     int block, last;  // next block of the part, and its first one beyond
     int end;          // keys of the item
-    int page;         // page of this warp's keys of the next block, not checked yet: nothing waits for it here
+    int page[C::G];   // pages of this warp's runs of the next block, not checked yet: nothing waits for them here
     bool more;
 
     __device__ __forceinline__ void enter(const PgAttn &p, const PgSplit &sp, int warp) {
-        const int per = sp.kt / kBlock;
+        const int per = sp.kt / C::BLOCK;
         while (w.left > 0) {
             end = pg_item_end(w.s, sp, w.item);
             block = w.u0 * per;
-            last = min((w.u0 + w.part()) * per, (end + kBlock - 1) / kBlock);
+            last = min((w.u0 + w.part()) * per, (end + C::BLOCK - 1) / C::BLOCK);
             if (block < last) break;
             w.step(w.part(), sp, Seqs{p.t, p.c.page_log2, p.err});
         }
@@ -142,29 +147,36 @@ struct Loader {
         look(p, warp);
     }
     __device__ __forceinline__ void look(const PgAttn &p, int warp) {
-        const int key0 = block * kBlock + warp * 16;
-        page = more && key0 < end ? __ldg(p.t.pages + (int64_t)w.seq * p.t.page_stride + (key0 >> p.c.page_log2)) : 0;
+#pragma unroll
+        for (int g = 0; g < C::G; g++) {
+            const int key0 = block * C::BLOCK + (warp * C::G + g) * 16;
+            page[g] = more && key0 < end ? __ldg(p.t.pages + (int64_t)w.seq * p.t.page_stride + (key0 >> p.c.page_log2)) : 0;
+        }
     }
     __device__ __forceinline__ void issue(const PgAttn &p, const PgSplit &sp, uint32_t stage, uint32_t scales, int warp,
                                           int lane) {
         if (!more) return;
-        const int key0 = block * kBlock + warp * 16, nv = end - key0;  // valid keys: the rest becomes zero
-        if (nv > 0) {
-            const int64_t vec = pg_vec(p.c, check_page(page, p.c.n_pages, p.err), w.head, key0 & ((1 << p.c.page_log2) - 1));
-            const uint32_t ks = stage + warp * 2 * C::TILE, vs = ks + C::TILE;
+        constexpr int CPR = C::ROWB / 16, IT = 16 * C::ROWB / 512;  // chunks of a row; copies of a lane and run
+        const uint32_t ks = stage + warp * 2 * C::TILE, vs = ks + C::TILE;
+#pragma unroll
+        for (int g = 0; g < C::G; g++) {
+            const int key0 = block * C::BLOCK + (warp * C::G + g) * 16, nv = end - key0;  // valid keys: the rest becomes zero
+            if (C::G == 1 && nv <= 0) break;
+            const int64_t vec = pg_vec(p.c, check_page(page[g], p.c.n_pages, p.err), w.head, key0 & ((1 << p.c.page_log2) - 1));
             const char *kp = p.c.k + vec * C::ROWB, *vp = p.c.v + vec * C::ROWB;
-            constexpr int CPR = C::ROWB / 16;  // chunks of a row
 #pragma unroll
-            for (int i = 0; i < C::TILE / 512; i++) {
+            for (int i = 0; i < IT; i++) {
                 const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
-                cp16(ks + chunk_at<C::ROWB, E4M3>(r, c), kp + x * 16, r < nv);
+                cp16(ks + chunk_at<C::ROWB, E4M3>(g * 16 + r, c), kp + x * 16, r < nv);
             }
 #pragma unroll
-            for (int i = 0; i < C::TILE / 512; i++) {
+            for (int i = 0; i < IT; i++) {
                 const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
-                cp16(vs + chunk_at<C::ROWB, false>(r, c), vp + x * 16, r < nv);
+                cp16(vs + chunk_at<C::ROWB, false>(g * 16 + r, c), vp + x * 16, r < nv);
             }
-            if (E4M3 && lane < 2) cp16n(scales + warp * 32 + lane * 16, (lane ? p.c.vs : p.c.ks) + vec, min(16, nv));
+            // a warp's scale bytes: K's runs, then V's
+            if (E4M3 && lane < 2)
+                cp16n(scales + (warp * 2 + lane) * 16 * C::G + g * 16, (lane ? p.c.vs : p.c.ks) + vec, max(0, min(16, nv)));
         }
         if (++block < last) {
             look(p, warp);
@@ -200,18 +212,18 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     ld.enter(p, sp, warp);
 #pragma unroll
     for (int s = 0; s < C::S - 1; s++) {
-        ld.issue(p, sp, base + s * C::STAGE, base + C::S * C::STAGE + s * 128, warp, lane);
+        ld.issue(p, sp, base + s * C::STAGE, base + C::S * C::STAGE + s * C::SCALES, warp, lane);
         cp_commit();
     }
     int slot = 0;  // ring slot of the next block to compute
     bool first_part = true;
     const float c = p.scale_log2;
-    const int per = sp.kt / kBlock;
+    const int per = sp.kt / C::BLOCK;
 
     while (w.left > 0) {
         const int np = w.part();
         const int end = pg_item_end(w.s, sp, w.item);
-        const int b0 = w.u0 * per, b1 = min((w.u0 + np) * per, (end + kBlock - 1) / kBlock);
+        const int b0 = w.u0 * per, b1 = min((w.u0 + np) * per, (end + C::BLOCK - 1) / C::BLOCK);
         const int tok0 = w.item * sp.tok, nrows = min(sp.tok, w.s.n - tok0) * sp.group;
         // Q's fragments, and the keys that each of the thread's rows keeps
         uint32_t q[MT][KS][4];
@@ -279,23 +291,23 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         for (int b = b0; b < b1; b++) {
             __syncwarp();  // every lane has read the slot that is filled next
             const int fill = slot == 0 ? C::S - 1 : slot - 1;
-            ld.issue(p, sp, base + fill * C::STAGE, base + C::S * C::STAGE + fill * 128, warp, lane);
+            ld.issue(p, sp, base + fill * C::STAGE, base + C::S * C::STAGE + fill * C::SCALES, warp, lane);
             cp_commit();
             cp_wait<C::S - 1>();
             __syncwarp();
-            const int key0 = b * kBlock + warp * 16;
+            const int key0 = b * C::BLOCK + warp * 16 * C::G;
             if (key0 < end) {
+                constexpr int N = 2 * C::G;  // runs of 8 keys
                 const uint32_t kt = base + slot * C::STAGE + warp * 2 * C::TILE, vt = kt + C::TILE;
-                float s[MT][2][4] = {};
+                float s[MT][N][4] = {};
                 if constexpr (E4M3) {
+                    const uint8_t *ksm = smem + slot * C::STAGE + warp * 2 * C::TILE;
 #pragma unroll
                     for (int x = 0; x < D / 64; x++)
 #pragma unroll
-                        for (int n = 0; n < 2; n++) {
-                            uint32_t u[4];
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                                         : "r"(kt + chunk_at<C::ROWB, true>(n * 8 + gid, 4 * x + tig)));
+                        for (int n = 0; n < N; n++) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(ksm + chunk_at<C::ROWB, true>(n * 8 + gid, 4 * x + tig));
+                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                             for (int y = 0; y < 4; y++) {
                                 uint32_t lo, hi;
@@ -306,27 +318,30 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         }
                 } else {
 #pragma unroll
-                    for (int x = 0; x < KS; x++) {
-                        uint32_t u[4];
-                        ldsm4(kt + chunk_at<C::ROWB, false>((lane >> 4) * 8 + (lane & 7), 2 * x + ((lane >> 3) & 1)), u);
+                    for (int x = 0; x < KS; x++)
 #pragma unroll
-                        for (int m = 0; m < MT; m++) {
-                            mma(s[m][0], q[m][x], u[0], u[1]);
-                            mma(s[m][1], q[m][x], u[2], u[3]);
+                        for (int g = 0; g < C::G; g++) {
+                            uint32_t u[4];
+                            ldsm4(kt + chunk_at<C::ROWB, false>(g * 16 + (lane >> 4) * 8 + (lane & 7), 2 * x + ((lane >> 3) & 1)), u);
+#pragma unroll
+                            for (int m = 0; m < MT; m++) {
+                                mma(s[m][2 * g], q[m][x], u[0], u[1]);
+                                mma(s[m][2 * g + 1], q[m][x], u[2], u[3]);
+                            }
                         }
-                    }
                 }
-                float vsc[2][2];    // what V's scales make of the probabilities
+                float vsc[N][2];    // what V's scales make of the probabilities
                 float shift = 1.f;  // what a new vref makes of the accumulators
                 if constexpr (E4M3) {
-                    const uint8_t *sc = smem + C::S * C::STAGE + slot * 128 + warp * 32;
+                    const uint8_t *sc = smem + C::S * C::STAGE + slot * C::SCALES + warp * 32 * C::G, *scv = sc + 16 * C::G;
                     // bytes of keys beyond the end are 0 here; NaN vectors (255) do not move vref
-                    const uint4 all = *reinterpret_cast<const uint4 *>(sc + 16);
                     uint32_t top = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint32_t w = reinterpret_cast<const uint32_t *>(&all)[i];
-                        top = __vmaxu4(top, w & ~__vcmpeq4(w, 0xffffffffu));
+                    for (int g = 0; g < C::G; g++) {
+                        const uint4 all = *reinterpret_cast<const uint4 *>(scv + 16 * g);
+                        const uint32_t w4[4] = {all.x, all.y, all.z, all.w};
+#pragma unroll
+                        for (int i = 0; i < 4; i++) top = __vmaxu4(top, w4[i] & ~__vcmpeq4(w4[i], 0xffffffffu));
                     }
                     top = __vmaxu4(top, top >> 16);
                     const int vmax = (int)max(top & 255u, (top >> 8) & 255u);
@@ -335,9 +350,9 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         vref = vmax;
                     }
 #pragma unroll
-                    for (int n = 0; n < 2; n++) {
+                    for (int n = 0; n < N; n++) {
                         const uint32_t kb = *reinterpret_cast<const uint16_t *>(sc + n * 8 + 2 * tig);
-                        const uint32_t vb = *reinterpret_cast<const uint16_t *>(sc + 16 + n * 8 + 2 * tig);
+                        const uint32_t vb = *reinterpret_cast<const uint16_t *>(scv + n * 8 + 2 * tig);
                         const float k0 = scale_value(kb & 255u), k1 = scale_value(kb >> 8);
 #pragma unroll
                         for (int i = 0; i < 2; i++) {
@@ -353,19 +368,21 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                             }
                     }
                 }
-                uint32_t pf[MT][4];
+                uint32_t pf[MT][C::G][4];
 #pragma unroll
                 for (int m = 0; m < MT; m++) {
                     float mx[2];
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const int keep = lim[m][h] - key0 - 2 * tig;  // of the thread's keys 0, 1, 8, 9
+                        const int keep = lim[m][h] - key0 - 2 * tig;  // of the thread's keys 0, 1, 8, 9, ..
+                        mx[h] = -INFINITY;
 #pragma unroll
-                        for (int n = 0; n < 2; n++)
+                        for (int n = 0; n < N; n++) {
 #pragma unroll
                             for (int e = 0; e < 2; e++)
                                 if (n * 8 + e >= keep) s[m][n][2 * h + e] = -INFINITY;
-                        mx[h] = fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]), fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1]));
+                            mx[h] = fmaxf(mx[h], fmaxf(s[m][n][2 * h], s[m][n][2 * h + 1]));
+                        }
                         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
                         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
                         mmax[m][h] = fmaxf(mmax[m][h], mx[h]);
@@ -396,52 +413,51 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
                         const float cq = c * qs[m][h], nb = mref[m][h] == -INFINITY ? 0.f : -mref[m][h] * cq;
-                        float e[2][2];
 #pragma unroll
-                        for (int n = 0; n < 2; n++)
-#pragma unroll
-                            for (int i = 0; i < 2; i++) e[n][i] = ex2(fmaf(s[m][n][2 * h + i], cq, nb));
-                        l[m][h] += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
-                        if constexpr (E4M3) {
-#pragma unroll
-                            for (int n = 0; n < 2; n++)
-#pragma unroll
-                                for (int i = 0; i < 2; i++)  // a dropped key's scale byte may hold anything
-                                    e[n][i] = e[n][i] == 0.f ? 0.f : e[n][i] * vsc[n][i];
+                        for (int n = 0; n < N; n++) {
+                            float e0 = ex2(fmaf(s[m][n][2 * h], cq, nb)), e1 = ex2(fmaf(s[m][n][2 * h + 1], cq, nb));
+                            l[m][h] += e0 + e1;
+                            if constexpr (E4M3) {  // a dropped key's scale byte may hold anything
+                                e0 = e0 == 0.f ? 0.f : e0 * vsc[n][0];
+                                e1 = e1 == 0.f ? 0.f : e1 * vsc[n][1];
+                            }
+                            pf[m][n >> 1][h + 2 * (n & 1)] = E4M3 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
                         }
-                        pf[m][h] = E4M3 ? pack_f16(e[0][0], e[0][1]) : pack_bf16(e[0][0], e[0][1]);
-                        pf[m][h + 2] = E4M3 ? pack_f16(e[1][0], e[1][1]) : pack_bf16(e[1][0], e[1][1]);
                     }
                 }
                 if constexpr (E4M3) {
 #pragma unroll
-                    for (int x = 0; x < D / 32; x++) {
-                        uint32_t u[4];
-                        ldsm4_t(vt + chunk_at<C::ROWB, false>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * x + (lane >> 4)), u);
+                    for (int x = 0; x < D / 32; x++)
 #pragma unroll
-                        for (int y = 0; y < 2; y++) {
-                            // keys (2 t, 2 t + 1) of two neighbouring columns: by column, then to f16
-                            uint32_t e0, e1, d0, d1;
-                            to_f16(__byte_perm(u[2 * y], 0, 0x3120), e0, d0);
-                            to_f16(__byte_perm(u[2 * y + 1], 0, 0x3120), e1, d1);
+                        for (int g = 0; g < C::G; g++) {
+                            uint32_t u[4];
+                            ldsm4_t(vt + chunk_at<C::ROWB, false>(g * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * x + (lane >> 4)), u);
 #pragma unroll
-                            for (int m = 0; m < MT; m++) {
-                                mma16(o[m][4 * x + 2 * y], pf[m], e0, e1);
-                                mma16(o[m][4 * x + 2 * y + 1], pf[m], d0, d1);
+                            for (int y = 0; y < 2; y++) {
+                                // keys (2 t, 2 t + 1) of two neighbouring columns: by column, then to f16
+                                uint32_t e0, e1, d0, d1;
+                                to_f16(__byte_perm(u[2 * y], 0, 0x3120), e0, d0);
+                                to_f16(__byte_perm(u[2 * y + 1], 0, 0x3120), e1, d1);
+#pragma unroll
+                                for (int m = 0; m < MT; m++) {
+                                    mma16(o[m][4 * x + 2 * y], pf[m][g], e0, e1);
+                                    mma16(o[m][4 * x + 2 * y + 1], pf[m][g], d0, d1);
+                                }
                             }
                         }
-                    }
                 } else {
 #pragma unroll
-                    for (int x = 0; x < D / 16; x++) {
-                        uint32_t u[4];
-                        ldsm4_t(vt + chunk_at<C::ROWB, false>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * x + (lane >> 4)), u);
+                    for (int x = 0; x < D / 16; x++)
 #pragma unroll
-                        for (int m = 0; m < MT; m++) {
-                            mma(o[m][2 * x], pf[m], u[0], u[1]);
-                            mma(o[m][2 * x + 1], pf[m], u[2], u[3]);
+                        for (int g = 0; g < C::G; g++) {
+                            uint32_t u[4];
+                            ldsm4_t(vt + chunk_at<C::ROWB, false>(g * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * x + (lane >> 4)), u);
+#pragma unroll
+                            for (int m = 0; m < MT; m++) {
+                                mma(o[m][2 * x], pf[m][g], u[0], u[1]);
+                                mma(o[m][2 * x + 1], pf[m][g], u[2], u[3]);
+                            }
                         }
-                    }
                 }
             }
             slot = slot + 1 == C::S ? 0 : slot + 1;
@@ -460,7 +476,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             }
         const bool whole = w.u0 == 0 && np == w.units;
         const int64_t part = 2 * (int64_t)blockIdx.x + (first_part ? 0 : 1);
-        constexpr int H = E4M3 ? 2 : 1, DH = D / H;  // an 8-bit slot holds half of the columns at a time
+        constexpr int H = 256 * D > C::STAGE ? 2 : 1, DH = D / H;  // a smaller slot holds half of the columns at a time
         float *scratch = reinterpret_cast<float *>(smem + (slot == 0 ? C::S - 1 : slot - 1) * C::STAGE);
         const int row = threadIdx.x / 8, col = (threadIdx.x % 8) * 4;
 #pragma unroll
@@ -574,7 +590,7 @@ PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causa
     sp.max_rows = pl.rows;
     // Short sequences are not cut: another block adds less than the merge's launch.
     const int64_t longest = (int64_t)t.max_pages << c.page_log2;
-    sp.kt = longest <= 512 ? 512 : kBlock;
+    sp.kt = longest <= 512 ? 512 : c.fmt == EA_CACHE_E4M3 || c.dim == 64 ? 128 : 64;  // a block
     const int64_t units = (longest + sp.kt - 1) / sp.kt * t.n_seqs * c.heads;
     pl.ctas = (int)std::min<int64_t>(units, (int64_t)num_sms * 2);
     pl.bytes = units > t.n_seqs * (int64_t)c.heads ? pg_work_bytes(pl.ctas, pl.rows, c.dim) : 0;  // 0: a unit is an item
