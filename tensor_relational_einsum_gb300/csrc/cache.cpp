@@ -387,7 +387,7 @@ extern "C" ea_status ea_cache_attention_split(const ea_page_batch *batch, int32_
         ea_status s = batch_args(batch, page, rows);
         if (s) return s;
         const PgTable t = table_of(batch, rows);
-        const PgSplit sp{split[0], split[1], split[2], split[3], split[4], split[5], split[6]};
+        const PgSplit sp{split[0], split[1], split[2], split[3], split[4], split[5], split[6], 0};
         if (sp.heads < 1 || sp.group < 1 || sp.tok < 1 || sp.kt < 1) return set_error(EA_ERR_ARG, "ea_cache_attention_split: split");
         std::vector<PgSeq> seqs(t.n_seqs);
         std::vector<int64_t> first(t.n_seqs + 1, 0);

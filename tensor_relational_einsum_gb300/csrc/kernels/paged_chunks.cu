@@ -202,7 +202,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     if (warp == 9) tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
     tc_fence_before();
     let_next_start();
-    take_share<R::THREADS>(p.t, sp, p.c.page_log2, p.err, ctl->scan, &ctl->share);
+    take_shares<R::THREADS>(p.t, sp, p.c.page_log2, p.err, ctl->scan, 1, &ctl->share);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;

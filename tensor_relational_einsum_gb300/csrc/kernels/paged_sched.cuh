@@ -32,39 +32,46 @@ __device__ __forceinline__ int64_t block_scan(int64_t u, int64_t *incl, int64_t 
     return all;
 }
 
+// Shares blockIdx.x * each .. + each - 1 of gridDim.x * each, into out[].
 template <int NT>
-__device__ __forceinline__ void take_share(const PgTable &t, const PgSplit &sp, int page_log2, int *err, int64_t *scratch,
-                                           PgShare *out) {
-    int64_t u = 0, incl, total = 0;
+__device__ __forceinline__ void take_shares(const PgTable &t, const PgSplit &sp, int page_log2, int *err, int64_t *scratch,
+                                            int each, PgShare *out) {
+    int64_t u = 0, incl, total = 0, last = 0;
     for (int base = 0; base < t.n_seqs; base += NT) {
         const int i = base + threadIdx.x;
         u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, page_log2, err), sp) : 0;
-        total += block_scan<NT>(u, &incl, scratch);
+        last = block_scan<NT>(u, &incl, scratch);
+        total += last;
     }
-    const int parts = pg_parts(total, gridDim.x), x = blockIdx.x;
-    const bool any = x < parts;
-    const int64_t w0 = any ? pg_first(total, parts, x) : 0;
-    if (threadIdx.x == 0) {
-        out->w0 = w0;
-        out->total = total;
-        out->parts = parts;
-        out->count = any ? pg_first(total, parts, x + 1) - w0 : 0;
-        out->seq = 0;
-        out->off = 0;
+    const int parts = pg_parts(total, gridDim.x * each), x0 = blockIdx.x * each;
+    if ((int)threadIdx.x < each) {
+        const int x = x0 + threadIdx.x;
+        const bool any = x < parts;
+        PgShare s;
+        s.w0 = any ? pg_first(total, parts, x) : 0;
+        s.off = 0;
+        s.total = total;
+        s.count = any ? pg_first(total, parts, x + 1) - s.w0 : 0;
+        s.seq = 0;
+        s.parts = parts;
+        out[threadIdx.x] = s;
     }
     __syncthreads();
     int64_t run = 0;
-    for (int base = 0; any && base < t.n_seqs; base += NT) {
+    for (int base = 0; x0 < parts && base < t.n_seqs; base += NT) {
         if (t.n_seqs > NT) {
             const int i = base + threadIdx.x;
             u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, page_log2, err), sp) : 0;
-            total = block_scan<NT>(u, &incl, scratch);
+            last = block_scan<NT>(u, &incl, scratch);
         }
-        if (u > 0 && run + incl - u <= w0 && w0 < run + incl) {
-            out->seq = base + threadIdx.x;
-            out->off = w0 - (run + incl - u);
+        for (int e = 0; u > 0 && e < each && x0 + e < parts; e++) {
+            const int64_t w0 = pg_first(total, parts, x0 + e);
+            if (run + incl - u <= w0 && w0 < run + incl) {
+                out[e].seq = base + threadIdx.x;
+                out[e].off = w0 - (run + incl - u);
+            }
         }
-        run += total;
+        run += last;
     }
     __syncthreads();
 }

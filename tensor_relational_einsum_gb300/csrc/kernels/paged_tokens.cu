@@ -129,27 +129,28 @@ template <int D, bool E4M3, int MT>
 struct Loader {
     using C = Cfg<D, E4M3, MT>;
     PgWalk w;
+    int keys, off;    // keys of a block; this warp's first one
     int block, last;  // next block of the part, and its first one beyond
     int end;          // keys of the item
     int page[C::G];   // pages of this warp's runs of the next block, not checked yet: nothing waits for them here
     bool more;
 
-    __device__ __forceinline__ void enter(const PgAttn &p, const PgSplit &sp, int warp) {
-        const int per = sp.kt / C::BLOCK;
+    __device__ __forceinline__ void enter(const PgAttn &p, const PgSplit &sp) {
+        const int per = sp.kt / keys;
         while (w.left > 0) {
             end = pg_item_end(w.s, sp, w.item);
             block = w.u0 * per;
-            last = min((w.u0 + w.part()) * per, (end + C::BLOCK - 1) / C::BLOCK);
+            last = min((w.u0 + w.part()) * per, (end + keys - 1) / keys);
             if (block < last) break;
             w.step(w.part(), sp, Seqs{p.t, p.c.page_log2, p.err});
         }
         more = w.left > 0;
-        look(p, warp);
+        look(p);
     }
-    __device__ __forceinline__ void look(const PgAttn &p, int warp) {
+    __device__ __forceinline__ void look(const PgAttn &p) {
 #pragma unroll
         for (int g = 0; g < C::G; g++) {
-            const int key0 = block * C::BLOCK + (warp * C::G + g) * 16;
+            const int key0 = block * keys + off + g * 16;
             page[g] = more && key0 < end ? __ldg(p.t.pages + (int64_t)w.seq * p.t.page_stride + (key0 >> p.c.page_log2)) : 0;
         }
     }
@@ -160,7 +161,7 @@ struct Loader {
         const uint32_t ks = stage + warp * 2 * C::TILE, vs = ks + C::TILE;
 #pragma unroll
         for (int g = 0; g < C::G; g++) {
-            const int key0 = block * C::BLOCK + (warp * C::G + g) * 16, nv = end - key0;  // valid keys: the rest becomes zero
+            const int key0 = block * keys + off + g * 16, nv = end - key0;  // valid keys: the rest becomes zero
             if (C::G == 1 && nv <= 0) break;
             const int64_t vec = pg_vec(p.c, check_page(page[g], p.c.n_pages, p.err), w.head, key0 & ((1 << p.c.page_log2) - 1));
             const char *kp = p.c.k + vec * C::ROWB, *vp = p.c.v + vec * C::ROWB;
@@ -179,10 +180,10 @@ struct Loader {
                 cp16n(scales + (warp * 2 + lane) * 16 * C::G + g * 16, (lane ? p.c.vs : p.c.ks) + vec, max(0, min(16, nv)));
         }
         if (++block < last) {
-            look(p, warp);
+            look(p);
         } else {
             w.step(w.part(), sp, Seqs{p.t, p.c.page_log2, p.err});
-            enter(p, sp, warp);
+            enter(p, sp);
         }
     }
 };
@@ -194,13 +195,15 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     using C = Cfg<D, E4M3, MT>;
     constexpr int KS = D / 16, NT = D / 8;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ PgShare share;
+    __shared__ PgShare shares[4];
     __shared__ int64_t scan[kThreads / 32];
     __shared__ float4 s_ml[4][16 * MT];  // a warp's reference maximum, sum, maximum of its rows; unit of its output
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     let_next_start();
-    take_share<kThreads>(p.t, sp, p.c.page_log2, p.err, scan, &share);
+    const bool solo = sp.solo != 0;
+    take_shares<kThreads>(p.t, sp, p.c.page_log2, p.err, scan, solo ? 4 : 1, shares);
+    const PgShare &share = shares[solo ? warp : 0];
     Loader<D, E4M3, MT> ld;
     ld.w.begin(share, sp, Seqs{p.t, p.c.page_log2, p.err});
     PgWalk w = ld.w;
@@ -209,7 +212,11 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         wait_for_previous();
         return;
     }
-    ld.enter(p, sp, warp);
+    const int keys = solo ? C::BLOCK / 4 : C::BLOCK;  // of a block, and this warp's first one
+    const int off = solo ? 0 : warp * 16 * C::G;
+    ld.keys = keys;
+    ld.off = off;
+    ld.enter(p, sp);
 #pragma unroll
     for (int s = 0; s < C::S - 1; s++) {
         ld.issue(p, sp, base + s * C::STAGE, base + C::S * C::STAGE + s * C::SCALES, warp, lane);
@@ -218,12 +225,12 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     int slot = 0;  // ring slot of the next block to compute
     bool first_part = true;
     const float c = p.scale_log2;
-    const int per = sp.kt / C::BLOCK;
+    const int per = sp.kt / keys;
 
     while (w.left > 0) {
         const int np = w.part();
         const int end = pg_item_end(w.s, sp, w.item);
-        const int b0 = w.u0 * per, b1 = min((w.u0 + np) * per, (end + C::BLOCK - 1) / C::BLOCK);
+        const int b0 = w.u0 * per, b1 = min((w.u0 + np) * per, (end + keys - 1) / keys);
         const int tok0 = w.item * sp.tok, nrows = min(sp.tok, w.s.n - tok0) * sp.group;
         // Q's fragments, and the keys that each of the thread's rows keeps
         uint32_t q[MT][KS][4];
@@ -295,7 +302,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             cp_commit();
             cp_wait<C::S - 1>();
             __syncwarp();
-            const int key0 = b * C::BLOCK + warp * 16 * C::G;
+            const int key0 = b * keys + off;
             if (key0 < end) {
                 constexpr int N = 2 * C::G;  // runs of 8 keys
                 const uint32_t kt = base + slot * C::STAGE + warp * 2 * C::TILE, vt = kt + C::TILE;
@@ -463,17 +470,55 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             slot = slot + 1 == C::S ? 0 : slot + 1;
         }
 
-        // ---- the four warps' results: scaled to the item's maximum and summed through shared memory.  The scratch is
-        // the ring slot that was computed last: it is refilled after this part's barriers.
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 1);
                 l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 2);
-                if (tig == 0) s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h] * qs[m][h], l[m][h], mmax[m][h] * qs[m][h],
-                                                                         E4M3 ? ldexpf(1.f, vref - 127 - 7) : 1.f);
             }
+        const float unit = E4M3 ? ldexpf(1.f, vref - 127 - 7) : 1.f;
+        if (solo) {
+            // ---- the warp has the item to itself
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int r = m * 16 + h * 8 + gid;
+                    if (r >= nrows) continue;
+                    const int64_t at = (int64_t)(w.s.first + tok0 + r / sp.group) * p.qheads + w.head * sp.group + r % sp.group;
+                    const float sum = l[m][h], inv = (sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum) * unit;
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int x = 0; x < D / 16; x++) {
+                            const float *a = o[m][2 * x], *d = o[m][2 * x + 1];
+                            *reinterpret_cast<uint2 *>(p.o + (at * D + 16 * x + 4 * tig) * 2) = make_uint2(
+                                pack_bf16(a[2 * h] * inv, d[2 * h] * inv), pack_bf16(a[2 * h + 1] * inv, d[2 * h + 1] * inv));
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NT; n++)
+                            *reinterpret_cast<uint32_t *>(p.o + (at * D + 8 * n + 2 * tig) * 2) =
+                                pack_bf16(o[m][n][2 * h] * inv, o[m][n][2 * h + 1] * inv);
+                    }
+                    if (p.m_out && tig == 0) {
+                        const float f = mref[m][h] == -INFINITY ? 0.f : ex2((mref[m][h] - mmax[m][h]) * (c * qs[m][h]));
+                        p.m_out[at] = mmax[m][h] * qs[m][h] * p.scale;
+                        p.l_out[at] = sum * f;
+                    }
+                }
+            w.step(np, sp, Seqs{p.t, p.c.page_log2, p.err});
+            continue;
+        }
+
+        // ---- the four warps' results: scaled to the item's maximum and summed through shared memory.  The scratch is
+        // the ring slot that was computed last: it is refilled after this part's barriers.
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                if (tig == 0)
+                    s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h] * qs[m][h], l[m][h], mmax[m][h] * qs[m][h], unit);
         const bool whole = w.u0 == 0 && np == w.units;
         const int64_t part = 2 * (int64_t)blockIdx.x + (first_part ? 0 : 1);
         constexpr int H = 256 * D > C::STAGE ? 2 : 1, DH = D / H;  // a smaller slot holds half of the columns at a time
@@ -592,7 +637,9 @@ PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causa
     const int64_t longest = (int64_t)t.max_pages << c.page_log2;
     sp.kt = longest <= 512 ? 512 : c.fmt == EA_CACHE_E4M3 || c.dim == 64 ? 128 : 64;  // a block
     const int64_t units = (longest + sp.kt - 1) / sp.kt * t.n_seqs * c.heads;
-    pl.ctas = (int)std::min<int64_t>(units, (int64_t)num_sms * 2);
+    // Many short sequences: a warp an item, without barriers or a merge between warps.
+    sp.solo = sp.kt == 512 && (int64_t)t.n_seqs * c.heads >= 4 * (int64_t)num_sms;
+    pl.ctas = (int)std::min<int64_t>(sp.solo ? (units + 3) / 4 : units, (int64_t)num_sms * 2);
     pl.bytes = units > t.n_seqs * (int64_t)c.heads ? pg_work_bytes(pl.ctas, pl.rows, c.dim) : 0;  // 0: a unit is an item
     return pl;
 }

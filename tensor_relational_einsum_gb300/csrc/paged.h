@@ -78,6 +78,7 @@ struct PgSplit {
     int32_t kt;                  // keys of a unit
     int32_t causal;
     int32_t min_rows, max_rows;  // the sequences served: min_rows <= n * group <= max_rows
+    int32_t solo;                // token kernel: a warp, not a CTA, takes a share
 };
 
 // What a CTA whose range begins inside an item says to the merge.
