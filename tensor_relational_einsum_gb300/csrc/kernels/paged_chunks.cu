@@ -14,10 +14,14 @@
 // the swizzled operand tiles (a box of up to 128 positions x 64 columns: a
 // page is contiguous for a head, so a page is one box per 64 columns).
 // 8-bit pages are copied with bulk copies into a ring of 64-key half tiles
-// and rewritten as bf16 operands by a warpgroup of their own: sign and the
-// other 7 bits moved to bf16's places give value * 2^-120, one product with
-// 2^120 times the scale (exact) puts that right, so that nothing behind the
-// tiles knows of the format.
+// and rewritten as f16 operands by a warpgroup of their own: a conversion and
+// a product for two codes (twice as many integer instructions lead to bf16).
+// f16's range is kept by powers of two, so that the operands are exact: K's
+// vectors are brought to the largest scale of their tile, V's to the largest
+// of the part so far (exact down to 2^-21 of it), Q's rows to [2^14, 2^15),
+// the probabilities to 2^7.  All of these are one number a tile or a row to
+// the softmax.  (Scales left to the softmax, a number a key, cost it 64
+// broadcast reads of shared memory a row and tile: 6200 cycles a tile.)
 //
 // Keys at and beyond the sequence's end lie in the last tile only.  Their
 // scores are dropped by position whatever they are; the second product stops
@@ -27,18 +31,19 @@
 // Roles (one CTA per SM; bf16: 384 threads, e4m3: 512):
 //   warps 0-3, 4-7  softmax of tile X = 0, 1: a query row per thread (TMEM
 //              lane = row), its 128 scores in registers: mask by position,
-//              row maximum, p = 2^(c s - c m), row sum, P as bf16 over the
+//              row maximum, p = 2^(c s - c m), row sum, P as 16 bits over the
 //              scores; A is rescaled in TMEM when the reference maximum moves
 //              by more than 2^64 (fp32 and bf16 have the same 8 exponent
 //              bits, so P, l and A stay in range and their relative rounding
-//              is the same at any magnitude); at the part's end A / l to the
+//              is the same at any magnitude; 2^8 with f16); at the part's end A / l to the
 //              output, or (m, l, A) to the workspace.
 //   warp 8     copies: Q tiles; K and V pages (or the raw half tiles).
 //   warp 9     TMEM and MMA issue: per key tile and X, A_X (+)= P_X V, then
 //              S_X = Q_X K^T of the next key tile, so that one tile's products
 //              run while the other's softmax does.
 //   warp 10    hands the CTA's parts of items to the others through a ring.
-//   warps 12-15 (e4m3) rewrite the half tiles as bf16.
+//   warps 12-15 (e4m3) rewrite the half tiles and Q as f16 and lay out the
+//              scales.
 // Every mbarrier wait is bounded (2 s); on time-out the kernel raises the
 // device error word, all roles leave their loops, the copies and MMAs in
 // flight are waited for and TMEM is freed before the CTA exits.
@@ -57,8 +62,9 @@ constexpr int kRows = 128;        // rows of a tile (TMEM lanes)
 constexpr int kKeys = 128;        // keys of a key tile
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;   // S_0 [0, 128), S_1 [128, 256), A_0 [256, 256 + D), A_1 [256 + D, ..)
-constexpr float kLazy = 64.0f;
-constexpr int kRaw = 4;           // e4m3: ring of raw half tiles
+template <bool E4M3>
+constexpr float kLazy = E4M3 ? 8.0f : 64.0f;
+constexpr int kRaw = 3;           // e4m3: ring of raw half tiles
 constexpr int kParts = 4;         // ring of parts
 constexpr int kMaxStages = 4;
 
@@ -68,9 +74,9 @@ template <bool E4M3>
 struct Regs {
     static constexpr int THREADS = E4M3 ? 512 : 384;
     static constexpr int LAUNCH = E4M3 ? 128 : 168;
-    static constexpr int SOFTMAX = E4M3 ? 192 : 208;
-    static constexpr int CTL = E4M3 ? 64 : 88;
-    static constexpr int CONV = 64;
+    static constexpr int SOFTMAX = E4M3 ? 184 : 208;
+    static constexpr int CTL = E4M3 ? 72 : 88;
+    static constexpr int CONV = 72;
     static_assert(128 * (2 * SOFTMAX + CTL + (E4M3 ? CONV : 0)) <= THREADS * LAUNCH, "register split");
 };
 
@@ -111,7 +117,7 @@ __device__ __forceinline__ Part part_of(const PgWalk &w, const PgSplit &sp) {
 }
 
 struct Ctl {
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full[2], q_empty[2], q_ready[2];
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t s_full[2], p_full[2], o_fin[2];
@@ -121,7 +127,15 @@ struct Ctl {
     int abort;
     PgShare share;
     int64_t scan[16];
+    int2 top[2][4];          // e4m3: the largest scale bytes of a tile's K and V, by warp (two tiles' worth)
+    uint32_t mul[2][2][kKeys];  // e4m3: factors of a tile's K and V vectors, two halves each
     Part part[kParts];
+};
+
+// e4m3: what a tile's operands were brought to.  K = f16 value * 2^(k - 133),
+// V = f16 value * 2^(v - 133).
+struct Refs {
+    int k, v;
 };
 
 template <int D, bool E4M3>
@@ -136,8 +150,12 @@ struct Cfg {
     static constexpr int K_OFF = 2 * TILE;                  // Q_0, Q_1, then K of each stage, V of each stage
     static constexpr int V_OFF = K_OFF + ST * TILE;
     static constexpr int RAW_OFF = V_OFF + ST * TILE;
-    static constexpr int RAW = E4M3 ? 64 * D + 64 : 0;      // 64 keys' codes, then their scale bytes
-    static constexpr int CTL_OFF = RAW_OFF + kRaw * RAW;
+    static constexpr int RAW = E4M3 ? 64 * D + 256 : 0;     // 64 keys' codes; K's first half: the tile's scale bytes
+    // A tile's references are read until its P is written.  K of tile t + 2 ST waits for S(t + ST), which is behind P
+    // of tile t + ST - 1, so a ring of 2 ST is safe; Q's scales by part and by the part before.
+    static constexpr int SC_OFF = RAW_OFF + kRaw * RAW;
+    static constexpr int QS_OFF = SC_OFF + (E4M3 ? 2 * ST * (int)sizeof(Refs) : 0);
+    static constexpr int CTL_OFF = QS_OFF + (E4M3 ? 2 * 2 * kRows * 4 : 0);
     static constexpr int SMEM = 1024 + CTL_OFF + (int)sizeof(Ctl);
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -148,13 +166,26 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// Two e4m3 bytes at bits 8..15 and 24..31 of x as bf16 times 2^-120.
-__device__ __forceinline__ uint32_t as_bf16(uint32_t x) { return ((x & 0x7f007f00u) >> 4) | (x & 0x80008000u); }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+// Four e4m3 bytes as f16: bytes 0 and 1, bytes 2 and 3.
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// 2^e for -126 <= e <= 127; 0 below.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)max(e + 127, 0) << 23); }
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(Regs<E4M3>::THREADS, 1)
@@ -176,6 +207,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         for (int b = 0; b < 2; b++) {
             mbar_init(&ctl->q_full[b], 1);
             mbar_init(&ctl->q_empty[b], 1);
+            mbar_init(&ctl->q_ready[b], 4);
             mbar_init(&ctl->s_full[b], 1);
             mbar_init(&ctl->p_full[b], 4);
             mbar_init(&ctl->o_fin[b], 1);
@@ -235,26 +267,29 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                            ? __ldg(p.t.pages + (int64_t)P.seq * p.t.page_stride + (key >> lg)) : 0;
             };
             int32_t next = look(0);
-            for (int x = 0; x < 2 && ok; x++) {
-                if (P.n[x] == 0) continue;
-                const uint32_t qn = x == 0 ? qx0 : qx1;
-                if (!warp_wait(&ctl->q_empty[x], (qn & 1) ^ 1, abort, p.err, kDevTimeoutProducer)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    const uint32_t qs = smem_u32(smem + x * C::TILE);
-                    mbar_expect_tx(&ctl->q_full[x], half_rows * D * 2);
+            // Q, behind the first K and V: its buffers are free only when the part before has done its last scores
+            auto load_q = [&]() {
+                for (int x = 0; x < 2; x++) {
+                    if (P.n[x] == 0) continue;
+                    const uint32_t qn = x == 0 ? qx0 : qx1;
+                    if (!warp_wait(&ctl->q_empty[x], (qn & 1) ^ 1, abort, p.err, kDevTimeoutProducer)) {
+                        return false;
+                    }
+                    if (lane == 0) {
+                        const uint32_t qs = smem_u32(smem + x * C::TILE);
+                        mbar_expect_tx(&ctl->q_full[x], half_rows * D * 2);
 #pragma unroll
-                    for (int c = 0; c < C::CH; c++)
-                        tma_load_3d(qs + c * (kRows * 128), &q_map, &ctl->q_full[x], 64 * c, P.head * sp.group,
-                                    P.row0 + x * half_tok);
+                        for (int c = 0; c < C::CH; c++)
+                            tma_load_3d(qs + c * (kRows * 128), &q_map, &ctl->q_full[x], 64 * c, P.head * sp.group,
+                                        P.row0 + x * half_tok);
+                    }
+                    q_armed |= 1u << x;
+                    q_par = (q_par & ~(1u << x)) | ((qn & 1) << x);
+                    if (x == 0) qx0++;
+                    else qx1++;
                 }
-                q_armed |= 1u << x;
-                q_par = (q_par & ~(1u << x)) | ((qn & 1) << x);
-                if (x == 0) qx0++;
-                else qx1++;
-            }
+                return true;
+            };
             for (int j = 0; j < P.tiles && ok; j++, ct++) {
                 const int key0 = (P.u0 + j) * kKeys, nv = min(kKeys, P.end - key0);
                 const int32_t g = check_page(next, p.c.n_pages, p.err);
@@ -300,19 +335,25 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         // a run: a page, or the half of one of 128 positions
                         const int run = min(page, 64), np = (nh + run - 1) / run;
                         const int32_t gi = __shfl_sync(0xffffffffu, g, (k0 + lane * run) >> lg);
-                        if (lane == 0) mbar_expect_tx(&ctl->raw_full[st], np * run * (D + 1));
+                        const int np_all = (nv + page - 1) >> lg;
+                        if (lane == 0) mbar_expect_tx(&ctl->raw_full[st], np * run * D + (h == 0 ? 2 * np_all * page : 0));
                         __syncwarp();
+                        const uint32_t dst = smem_u32(smem + C::RAW_OFF + st * C::RAW);
                         if (lane < np) {
-                            const uint32_t dst = smem_u32(smem + C::RAW_OFF + st * C::RAW);
                             const int64_t vec = pg_vec(p.c, gi, P.head, (k0 + lane * run) & (page - 1));
                             bulk_load(dst + lane * run * D, (h < 2 ? p.c.k : p.c.v) + vec * D, run * D, &ctl->raw_full[st]);
-                            bulk_load(dst + 64 * D + lane * run, (h < 2 ? p.c.ks : p.c.vs) + vec, run, &ctl->raw_full[st]);
+                        }
+                        if (h == 0 && lane < np_all) {
+                            const int64_t vec = pg_vec(p.c, g, P.head, 0);
+                            bulk_load(dst + 64 * D + (lane << lg), p.c.ks + vec, page, &ctl->raw_full[st]);
+                            bulk_load(dst + 64 * D + 128 + (lane << lg), p.c.vs + vec, page, &ctl->raw_full[st]);
                         }
                         raw_armed |= 1u << st;
                         raw_par = (raw_par & ~(1u << st)) | (ph << st);
                         rt++;
                     }
                 }
+                if (ok && j == 0) ok = load_q();
             }
         }
         if (*abort && lane == 0) {
@@ -328,8 +369,9 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         }
     } else if (warp == 9) {
         // ------------------------------------------------ MMA issue (the whole warp; one elected lane issues)
-        const uint32_t idesc_s = make_idesc(kRows, kKeys, 0, 0);  // Q (K-major) x K (K-major)
-        const uint32_t idesc_o = make_idesc(kRows, D, 0, 1);      // P (TMEM) x V (MN-major)
+        constexpr uint32_t kBf16 = E4M3 ? (1u << 7) | (1u << 10) : 0u;  // bits that say bf16; f16 is 0
+        const uint32_t idesc_s = make_idesc(kRows, kKeys, 0, 0) & ~kBf16;  // Q (K-major) x K (K-major)
+        const uint32_t idesc_o = make_idesc(kRows, D, 0, 1) & ~kBf16;      // P (TMEM) x V (MN-major)
         uint32_t ct = 0, qx0 = 0, qx1 = 0, tx0 = 0, tx1 = 0;
         bool ok = true;
         auto mma_s = [&](int x, uint32_t t) {
@@ -387,7 +429,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             for (int x = 0; x < 2 && ok; x++) {
                 const int ntx = x == 0 ? nt0 : nt1;
                 if (ntx == 0) continue;
-                if (!warp_wait(&ctl->q_full[x], (x == 0 ? qx0 : qx1) & 1, abort, p.err, kDevTimeoutMma)) {
+                if (!warp_wait(E4M3 ? &ctl->q_ready[x] : &ctl->q_full[x], (x == 0 ? qx0 : qx1) & 1, abort, p.err, kDevTimeoutMma)) {
                     ok = false;
                     break;
                 }
@@ -470,15 +512,18 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         const float c = p.scale_log2;
         const int rtok = row / sp.group, rhead = row - rtok * sp.group;  // the row's token and head of the tile
         uint32_t ci = 0, ct = 0;  // parts and key tiles of this X
+        uint32_t gt = 0;          // key tiles of both: the ring of scales
         bool ok = true;
         while (ok) {
             int n, u0, slot, whole;  // what the loop over key tiles needs of the part
             int hi;                  // last key the row keeps
             int64_t at;              // the row's place in O; -1: no token of the sequence
+            const uint32_t gt0 = gt;
             {
                 Part P;
                 const bool first_part = pi == 0;
                 if (!next_part(P, kDevTimeoutSoftmax)) break;
+                gt += P.tiles;
                 const int ntok = min(half_tok, P.ntok - x * half_tok);
                 if (ntok <= 0) continue;
                 n = x == 0 ? P.n[0] : P.n[1];
@@ -493,6 +538,8 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             }
             const bool mine = at >= 0;
             float m_ref = -INFINITY, m_max = -INFINITY, l = 0.f;
+            float qs = 1.f;  // e4m3: Q is qs times its f16 values
+            int vref = 0;    // e4m3: A is in units of 2^(vref - 133 - 7), l in units of 2^-7
             for (int j = 0; j < n; j++) {
                 if (!warp_wait(&ctl->s_full[x], (ct + j) & 1, abort, p.err, kDevTimeoutSoftmax)) {
                     ok = false;
@@ -500,37 +547,51 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 }
                 tc_fence_after();
                 uint32_t u[kKeys];
+                const int jhi = hi - (u0 + j) * kKeys;
                 float hm0, hm1, hm2, hm3;
                 tmem_ld32_max(srow, u, hm0);
                 tmem_ld32_max(srow + 32, u + 32, hm1);
                 tmem_ld32_max(srow + 64, u + 64, hm2);
                 tmem_ld32_max(srow + 96, u + 96, hm3);
+                float ft = 1.f, cr = c, shift = 1.f;  // a score is ft times what the product gives
+                if constexpr (E4M3) {
+                    const Refs rf = reinterpret_cast<const Refs *>(smem + C::SC_OFF)[(gt0 + j) % (2 * C::ST)];
+                    if (j == 0) {
+                        qs = reinterpret_cast<const float *>(smem + C::QS_OFF)[((ci & 1) * 2 + x) * kRows + row];
+                        vref = rf.v;
+                    }
+                    shift = pow2(vref - rf.v);
+                    vref = rf.v;
+                    ft = pow2(max(rf.k - 133, -126)) * qs;
+                    cr = fmaxf(c * ft, 1.2e-38f);  // not 0: a dropped score is -inf
+                }
                 tmem_wait_ld();
-                const int jhi = hi - (u0 + j) * kKeys;
                 float mx = fmaxf(max3(hm0, hm1, hm2), hm3);
                 if (jhi < kKeys - 1) {
                     mx = -INFINITY;
 #pragma unroll
                     for (int q = 0; q < kKeys; q += 32) mx = fmaxf(mx, mask_chunk(u + q, q, 0, jhi));
                 }
+                if constexpr (E4M3) mx *= ft;
                 m_max = fmaxf(m_max, mx);
                 float alpha = 1.f;
-                if (mx != -INFINITY && (m_ref == -INFINITY || (mx - m_ref) * c > kLazy)) {
+                if (mx != -INFINITY && (m_ref == -INFINITY || (mx - m_ref) * c > kLazy<E4M3>)) {
                     alpha = m_ref == -INFINITY ? 0.f : ex2((m_ref - mx) * c);
                     m_ref = mx;
                 }
-                const float base = m_ref == -INFINITY ? 0.f : m_ref * c;
-                const uint64_t c2 = pack_f32x2(c, c), nb2 = pack_f32x2(-base, -base);
+                const float base = (m_ref == -INFINITY ? 0.f : m_ref * c) - (E4M3 ? 7.f : 0.f);
+                const uint64_t c2 = pack_f32x2(cr, cr), nb2 = pack_f32x2(-base, -base);
                 uint64_t ls[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int q = 0; q < kKeys / 2; q++) {
                     const uint64_t y = fma_f32x2(pack_u32x2(u[2 * q], u[2 * q + 1]), c2, nb2);
                     const float e0 = ex2(lo_f32(y)), e1 = ex2(hi_f32(y));
                     ls[q & 3] = add_f32x2(ls[q & 3], pack_f32x2(e0, e1));
-                    u[q] = pack_bf16(e0, e1);
+                    u[q] = E4M3 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
                 }
                 const uint64_t s01 = add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3]));
                 l = fmaf(l, alpha, lo_f32(s01) + hi_f32(s01));
+                if constexpr (E4M3) alpha *= shift;
                 tmem_st32(srow, u);
                 tmem_st32(srow + 32, u + 32);
                 // The previous A += P V of this tile has completed: these scores were computed after it, in order.
@@ -562,7 +623,9 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             tc_fence_after();
             // whole item: A / l as bf16; a part of one: (m, l, A) with the true maximum as reference
             const float to_max = m_max == -INFINITY ? 0.f : ex2((m_ref - m_max) * c);
-            const float f = !whole ? to_max : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+            const float unit = E4M3 ? ldexpf(1.f, vref - 133 - 7) : 1.f;
+            if constexpr (E4M3) l *= 0.0078125f;
+            const float f = (!whole ? to_max : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l) * unit;
             const int64_t prow = (int64_t)slot * (2 * half_rows) + x * half_rows + row;
 #pragma unroll
             for (int cc = 0; cc < D / 32; cc++) {
@@ -606,8 +669,45 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         // ------------------------------------------------ raw half tiles to bf16 operands
         const int tid = threadIdx.x - 384;
         constexpr int CPR = D / 16;  // 16-byte chunks (16 codes) of a row
-        uint32_t ct = 0, rt = 0;
+        uint32_t ct = 0, rt = 0, qx0 = 0, qx1 = 0;
+        int vref = 0;
         bool ok = true;
+        // Q of both tiles, a row a thread, in place: bf16 to f16, brought to [2^14, 2^15) by a power of two
+        auto rewrite_q = [&](const Part &P) {
+            for (int x = 0; x < 2; x++) {
+                if (P.n[x] == 0) continue;
+                const uint32_t qn = x == 0 ? qx0 : qx1;
+                if (!warp_wait(&ctl->q_full[x], qn & 1, abort, p.err, kDevTimeoutProducer)) return false;
+                if (tid < half_rows) {
+                    uint8_t *rowp = smem + x * C::TILE + tid * 128;
+                    const int s = tid & 7;
+                    uint32_t big = 0;
+#pragma unroll
+                    for (int i = 0; i < D / 8; i++) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(rowp + (i / 8) * (kRows * 128) + (((i & 7) ^ s) << 4));
+                        big = __vmaxu2(big, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
+                        big = __vmaxu2(big, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                    }
+                    big = max(big >> 16, big & 0xffffu);
+                    const int e = big == 0 || big >= 0x7f80u ? 0 : min(126, 14 - ((int)(big >> 7) - 127));
+                    const float up = pow2(e);
+                    auto cvt = [&](uint32_t w) { return pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up); };
+#pragma unroll
+                    for (int i = 0; i < D / 8; i++) {
+                        uint4 *at = reinterpret_cast<uint4 *>(rowp + (i / 8) * (kRows * 128) + (((i & 7) ^ s) << 4));
+                        const uint4 v = *at;
+                        *at = make_uint4(cvt(v.x), cvt(v.y), cvt(v.z), cvt(v.w));
+                    }
+                    reinterpret_cast<float *>(smem + C::QS_OFF)[((qn & 1) * 2 + x) * kRows + tid] = pow2(-e);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->q_ready[x]);
+                if (x == 0) qx0++;
+                else qx1++;
+            }
+            return true;
+        };
         Part P;
         while (ok && next_part(P, kDevTimeoutProducer)) {
             for (int j = 0; j < P.tiles && ok; j++, ct++) {
@@ -628,47 +728,65 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     }
                     const uint8_t *raw = smem + C::RAW_OFF + rs * C::RAW;
                     uint8_t *dst = smem + (h < 2 ? C::K_OFF : C::V_OFF) + st * C::TILE;
-                    // all of the thread's codes and scales first: the stores below may not be reordered with loads
+                    // all of the thread's codes first: the stores below may not be reordered with loads
                     constexpr int IT = 64 * CPR / 128;
                     uint4 v[IT];
-                    uint32_t sc[IT];
 #pragma unroll
-                    for (int i = 0; i < IT; i++) {
-                        v[i] = *reinterpret_cast<const uint4 *>(raw + (i * 128 + tid) * 16);
-                        sc[i] = raw[64 * D + (i * 128 + tid) / CPR];
-                    }
+                    for (int i = 0; i < IT; i++) v[i] = *reinterpret_cast<const uint4 *>(raw + (i * 128 + tid) * 16);
+                    const uint32_t kb = h == 0 ? raw[64 * D + tid] : 0u, vb = h == 0 ? raw[64 * D + 128 + tid] : 0u;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->raw_empty[rs]);
                     rt++;
+                    if (h == 0) {
+                        // the tile's scales, a key a thread; NaN vectors (255) and what lies beyond the last key do not
+                        // move the references
+                        const uint32_t tk = __reduce_max_sync(0xffffffffu, tid < nv && kb != 255u ? kb : 0u);
+                        const uint32_t tv = __reduce_max_sync(0xffffffffu, tid < nv && vb != 255u ? vb : 0u);
+                        if (lane == 0) ctl->top[ct & 1][warp - 12] = make_int2((int)tk, (int)tv);
+                        named_bar(1, 128);
+                        int kref = 0;
+                        if (j == 0) vref = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int2 t = ctl->top[ct & 1][i];
+                            kref = max(kref, t.x);
+                            vref = max(vref, t.y);
+                        }
+                        // 2^(byte - reference + 6) in f16
+                        auto factor = [](uint32_t b, int ref) {
+                            const float f = b == 255u ? __uint_as_float(0x7fffffffu) : pow2((int)b - ref + 6);
+                            return pack_f16(f, f);
+                        };
+                        ctl->mul[ct & 1][0][tid] = factor(kb, kref);
+                        ctl->mul[ct & 1][1][tid] = factor(vb, vref);
+                        if (tid == 0) reinterpret_cast<Refs *>(smem + C::SC_OFF)[ct % (2 * C::ST)] = Refs{kref, vref};
+                        named_bar(1, 128);
+                    }
+                    const uint32_t *mul = ctl->mul[ct & 1][h >> 1] + k0;
+                    uint32_t mr[IT];
+#pragma unroll
+                    for (int i = 0; i < IT; i++) {
+                        const int r = (i * 128 + tid) / CPR;
+                        mr[i] = mul[r];
+                        if (k0 + r >= nv) {  // whatever is there: zeros
+                            v[i] = make_uint4(0, 0, 0, 0);
+                            mr[i] = 0u;
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < IT; i++) {
                         const int id = i * 128 + tid, r = id / CPR, ch = id % CPR;
-                        const uint32_t b = sc[i];
-                        // 2^120 times the scale; 2^(b - 7) is beyond bf16 for the largest scales: the rest goes into a
-                        // second product
-                        uint32_t m1 = (min(b, 134u) + 120u) * 0x00800080u;
-                        if (b == 255u) m1 = 0x7fff7fffu;
-                        uint32_t o[8];
-#pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            const uint32_t wd = reinterpret_cast<const uint32_t *>(&v[i])[q];
-                            o[2 * q] = mul_bf16x2(as_bf16(__byte_perm(wd, 0, 0x1404)), m1);
-                            o[2 * q + 1] = mul_bf16x2(as_bf16(__byte_perm(wd, 0, 0x3424)), m1);
-                        }
-                        if (b > 134u && b != 255u) {
-                            const uint32_t m2 = (b - 134u + 127u) * 0x00800080u;
-#pragma unroll
-                            for (int q = 0; q < 8; q++) o[q] = mul_bf16x2(o[q], m2);
-                        }
-                        if (k0 + r >= nv) {
-#pragma unroll
-                            for (int q = 0; q < 8; q++) o[q] = 0u;
-                        }
+                        uint4 lo, hi4;
+                        to_f16(v[i].x, lo.x, lo.y);
+                        to_f16(v[i].y, lo.z, lo.w);
+                        to_f16(v[i].z, hi4.x, hi4.y);
+                        to_f16(v[i].w, hi4.z, hi4.w);
+                        lo = make_uint4(mul_f16x2(lo.x, mr[i]), mul_f16x2(lo.y, mr[i]), mul_f16x2(lo.z, mr[i]), mul_f16x2(lo.w, mr[i]));
+                        hi4 = make_uint4(mul_f16x2(hi4.x, mr[i]), mul_f16x2(hi4.y, mr[i]), mul_f16x2(hi4.z, mr[i]), mul_f16x2(hi4.w, mr[i]));
                         // columns 16 ch .. + 15 of row k0 + r: two 16-byte chunks of the 128-byte swizzled row; the lanes
                         // of the second 64 columns store theirs in the other order (their banks are the same)
                         uint8_t *rowp = dst + (ch / 4) * (kKeys * 128) + (k0 + r) * 128;
                         const int s = (k0 + r) & 7, a = 2 * (ch & 3), flip = D == 128 ? ch >> 2 : r & 1;
-                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
                         *reinterpret_cast<uint4 *>(rowp + (((a + flip) ^ s) << 4)) = flip ? hi4 : lo;
                         *reinterpret_cast<uint4 *>(rowp + (((a + 1 - flip) ^ s) << 4)) = flip ? lo : hi4;
                     }
@@ -676,6 +794,11 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         fence_proxy_async();  // the operand tiles are read by the tensor cores (async proxy)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(h < 2 ? &ctl->k_full[st] : &ctl->v_full[st]);
+                        // the part's Q between its first K and V: it arrives when the part before has done its last scores
+                        if (j == 0 && h < 2 && !rewrite_q(P)) {
+                            ok = false;
+                            break;
+                        }
                     }
                 }
             }
