@@ -13,8 +13,7 @@
 // Key tiles come page by page.  bf16 pages are copied by TMA straight into
 // the swizzled operand tiles (a box of up to 128 positions x 64 columns: a
 // page is contiguous for a head, so a page is one box per 64 columns).
-// 8-bit pages are copied with bulk copies into a ring of 64-key half tiles
-// and rewritten as f16 operands by a warpgroup of their own: a conversion and
+// 8-bit pages are copied with bulk copies into raw tiles and rewritten as f16 operands by a warpgroup of their own: a conversion and
 // a product for two codes (twice as many integer instructions lead to bf16).
 // f16's range is kept by powers of two, so that the operands are exact: K's
 // vectors are brought to the largest scale of their tile, V's to the largest
@@ -37,13 +36,12 @@
 //              bits, so P, l and A stay in range and their relative rounding
 //              is the same at any magnitude; 2^8 with f16); at the part's end A / l to the
 //              output, or (m, l, A) to the workspace.
-//   warp 8     copies: Q tiles; K and V pages (or the raw half tiles).
+//   warp 8     copies: Q tiles; K and V pages (or the raw tiles).
 //   warp 9     TMEM and MMA issue: per key tile and X, A_X (+)= P_X V, then
 //              S_X = Q_X K^T of the next key tile, so that one tile's products
 //              run while the other's softmax does.
 //   warp 10    hands the CTA's parts of items to the others through a ring.
-//   warps 12-15 (e4m3) rewrite the half tiles and Q as f16 and lay out the
-//              scales.
+//   warps 12-15 (e4m3) rewrite the raw tiles and Q as f16, 32 rows a warp.
 // Every mbarrier wait is bounded (2 s); on time-out the kernel raises the
 // device error word, all roles leave their loops, the copies and MMAs in
 // flight are waited for and TMEM is freed before the CTA exits.
@@ -64,7 +62,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;   // S_0 [0, 128), S_1 [128, 256), A_0 [256, 256 + D), A_1 [256 + D, ..)
 template <bool E4M3>
 constexpr float kLazy = E4M3 ? 8.0f : 64.0f;
-constexpr int kRaw = 3;           // e4m3: ring of raw half tiles
 constexpr int kParts = 4;         // ring of parts
 constexpr int kMaxStages = 4;
 
@@ -119,7 +116,7 @@ __device__ __forceinline__ Part part_of(const PgWalk &w, const PgSplit &sp) {
 struct Ctl {
     uint64_t q_full[2], q_empty[2], q_ready[2];
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-    uint64_t raw_full[kRaw], raw_empty[kRaw];
+    uint64_t raw_full[2][2], raw_empty[2][2];  // of K, of V
     uint64_t s_full[2], p_full[2], o_fin[2];
     uint64_t part_full[kParts], part_empty[kParts];
     uint64_t mma_done;
@@ -128,7 +125,6 @@ struct Ctl {
     PgShare share;
     int64_t scan[16];
     int2 top[2][4];          // e4m3: the largest scale bytes of a tile's K and V, by warp (two tiles' worth)
-    uint32_t mul[2][2][kKeys];  // e4m3: factors of a tile's K and V vectors, two halves each
     Part part[kParts];
 };
 
@@ -150,12 +146,14 @@ struct Cfg {
     static constexpr int K_OFF = 2 * TILE;                  // Q_0, Q_1, then K of each stage, V of each stage
     static constexpr int V_OFF = K_OFF + ST * TILE;
     static constexpr int RAW_OFF = V_OFF + ST * TILE;
-    static constexpr int RAW = E4M3 ? 64 * D + 256 : 0;     // 64 keys' codes; K's first half: the tile's scale bytes
+    static constexpr int NR = D == 64 ? 2 : 1;              // e4m3: raw tiles of K, and of V
+    static constexpr int RAW = E4M3 ? kKeys * D : 0;
+    static constexpr int RSC_OFF = RAW_OFF + 2 * NR * RAW;  // the scale bytes of a raw K's tile: K's, V's
     // A tile's references are read until its P is written.  K of tile t + 2 ST waits for S(t + ST), which is behind P
     // of tile t + ST - 1, so a ring of 2 ST is safe; Q's scales by part and by the part before.
-    static constexpr int SC_OFF = RAW_OFF + kRaw * RAW;
+    static constexpr int SC_OFF = RSC_OFF + (E4M3 ? NR * 2 * kKeys : 0);
     static constexpr int QS_OFF = SC_OFF + (E4M3 ? 2 * ST * (int)sizeof(Refs) : 0);
-    static constexpr int CTL_OFF = QS_OFF + (E4M3 ? 2 * 2 * kRows * 4 : 0);
+    static constexpr int CTL_OFF = QS_OFF + (E4M3 ? 2 * 2 * kRows : 0);
     static constexpr int SMEM = 1024 + CTL_OFF + (int)sizeof(Ctl);
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -218,9 +216,9 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             mbar_init(&ctl->v_full[b], E4M3 ? 4 : 1);
             mbar_init(&ctl->v_empty[b], 1);
         }
-        for (int b = 0; b < kRaw; b++) {
-            mbar_init(&ctl->raw_full[b], 1);
-            mbar_init(&ctl->raw_empty[b], 4);
+        for (int b = 0; b < 4; b++) {
+            mbar_init(&ctl->raw_full[b >> 1][b & 1], 1);
+            mbar_init(&ctl->raw_empty[b >> 1][b & 1], 4);
         }
         for (int b = 0; b < kParts; b++) {
             mbar_init(&ctl->part_full[b], 1);
@@ -253,7 +251,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     if (warp >= 8 && warp < 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::CTL));
     if (warp == 8) {
         // ------------------------------------------------ copies (the whole warp; a lane looks up and copies a page)
-        uint32_t ct = 0, rt = 0, qx0 = 0, qx1 = 0;  // key tiles, raw half tiles, items per X
+        uint32_t ct = 0, qx0 = 0, qx1 = 0;  // key tiles, items per X
         uint32_t q_armed = 0, q_par = 0, k_armed = 0, k_par = 0, v_armed = 0, v_par = 0, raw_armed = 0, raw_par = 0;
         bool ok = true;
         const int lg = p.c.page_log2, page = 1 << lg;
@@ -323,34 +321,28 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     v_armed |= 1u << st;
                     v_par = (v_par & ~(1u << st)) | (ph << st);
                 } else {
-                    for (int h = 0; h < 4; h++) {  // K's halves, then V's
-                        const int k0 = (h & 1) * 64, nh = min(64, nv - k0);
-                        if (nh <= 0) continue;
-                        const int st = rt % kRaw;
-                        const uint32_t ph = (rt / kRaw) & 1;
-                        if (!warp_wait(&ctl->raw_empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) {
+                    const int rs = ct % C::NR, np = (nv + page - 1) >> lg;
+                    const uint32_t ph = (ct / C::NR) & 1;
+                    const int64_t vec = pg_vec(p.c, g, P.head, 0);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {  // K with the scales of both, then V
+                        if (!warp_wait(&ctl->raw_empty[h][rs], ph ^ 1, abort, p.err, kDevTimeoutProducer)) {
                             ok = false;
                             break;
                         }
-                        // a run: a page, or the half of one of 128 positions
-                        const int run = min(page, 64), np = (nh + run - 1) / run;
-                        const int32_t gi = __shfl_sync(0xffffffffu, g, (k0 + lane * run) >> lg);
-                        const int np_all = (nv + page - 1) >> lg;
-                        if (lane == 0) mbar_expect_tx(&ctl->raw_full[st], np * run * D + (h == 0 ? 2 * np_all * page : 0));
+                        if (lane == 0) mbar_expect_tx(&ctl->raw_full[h][rs], np * page * (h == 0 ? D + 2 : D));
                         __syncwarp();
-                        const uint32_t dst = smem_u32(smem + C::RAW_OFF + st * C::RAW);
                         if (lane < np) {
-                            const int64_t vec = pg_vec(p.c, gi, P.head, (k0 + lane * run) & (page - 1));
-                            bulk_load(dst + lane * run * D, (h < 2 ? p.c.k : p.c.v) + vec * D, run * D, &ctl->raw_full[st]);
+                            bulk_load(smem_u32(smem + C::RAW_OFF + (h * C::NR + rs) * C::RAW) + (lane << lg) * D,
+                                      (h ? p.c.v : p.c.k) + vec * D, page * D, &ctl->raw_full[h][rs]);
+                            if (h == 0) {
+                                const uint32_t sc = smem_u32(smem + C::RSC_OFF + rs * 2 * kKeys) + (lane << lg);
+                                bulk_load(sc, p.c.ks + vec, page, &ctl->raw_full[h][rs]);
+                                bulk_load(sc + kKeys, p.c.vs + vec, page, &ctl->raw_full[h][rs]);
+                            }
                         }
-                        if (h == 0 && lane < np_all) {
-                            const int64_t vec = pg_vec(p.c, g, P.head, 0);
-                            bulk_load(dst + 64 * D + (lane << lg), p.c.ks + vec, page, &ctl->raw_full[st]);
-                            bulk_load(dst + 64 * D + 128 + (lane << lg), p.c.vs + vec, page, &ctl->raw_full[st]);
-                        }
-                        raw_armed |= 1u << st;
-                        raw_par = (raw_par & ~(1u << st)) | (ph << st);
-                        rt++;
+                        raw_armed |= 1u << (2 * h + rs);
+                        raw_par = (raw_par & ~(1u << (2 * h + rs))) | (ph << (2 * h + rs));
                     }
                 }
                 if (ok && j == 0) ok = load_q();
@@ -364,8 +356,9 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 if (k_armed & (1u << s)) mbar_wait(&ctl->k_full[s], (k_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
                 if (v_armed & (1u << s)) mbar_wait(&ctl->v_full[s], (v_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
             }
-            for (int s = 0; s < kRaw; s++)
-                if (raw_armed & (1u << s)) mbar_wait(&ctl->raw_full[s], (raw_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
+            for (int s = 0; s < 4; s++)
+                if (raw_armed & (1u << s))
+                    mbar_wait(&ctl->raw_full[s >> 1][s & 1], (raw_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
         }
     } else if (warp == 9) {
         // ------------------------------------------------ MMA issue (the whole warp; one elected lane issues)
@@ -557,7 +550,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 if constexpr (E4M3) {
                     const Refs rf = reinterpret_cast<const Refs *>(smem + C::SC_OFF)[(gt0 + j) % (2 * C::ST)];
                     if (j == 0) {
-                        qs = reinterpret_cast<const float *>(smem + C::QS_OFF)[((ci & 1) * 2 + x) * kRows + row];
+                        qs = pow2(-(int)reinterpret_cast<const int8_t *>(smem + C::QS_OFF)[((ci & 1) * 2 + x) * kRows + row]);
                         vref = rf.v;
                     }
                     shift = pow2(vref - rf.v);
@@ -669,7 +662,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         // ------------------------------------------------ raw half tiles to bf16 operands
         const int tid = threadIdx.x - 384;
         constexpr int CPR = D / 16;  // 16-byte chunks (16 codes) of a row
-        uint32_t ct = 0, rt = 0, qx0 = 0, qx1 = 0;
+        uint32_t ct = 0, qx0 = 0, qx1 = 0;
         int vref = 0;
         bool ok = true;
         // Q of both tiles, a row a thread, in place: bf16 to f16, brought to [2^14, 2^15) by a power of two
@@ -698,7 +691,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         const uint4 v = *at;
                         *at = make_uint4(cvt(v.x), cvt(v.y), cvt(v.z), cvt(v.w));
                     }
-                    reinterpret_cast<float *>(smem + C::QS_OFF)[((qn & 1) * 2 + x) * kRows + tid] = pow2(-e);
+                    reinterpret_cast<int8_t *>(smem + C::QS_OFF)[((qn & 1) * 2 + x) * kRows + tid] = (int8_t)e;
                 }
                 fence_proxy_async();
                 __syncwarp();
@@ -712,36 +705,32 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         while (ok && next_part(P, kDevTimeoutProducer)) {
             for (int j = 0; j < P.tiles && ok; j++, ct++) {
                 const int nv = min(kKeys, P.end - (P.u0 + j) * kKeys);
-                const int st = ct % C::ST;
-                const uint32_t ph = (ct / C::ST) & 1;
-                for (int h = 0; h < 4; h++) {
-                    const int k0 = (h & 1) * 64;
-                    if (k0 == 0 && !warp_wait(h ? &ctl->v_empty[st] : &ctl->k_empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) {
-                        ok = false;
-                        break;
-                    }
-                    if (nv - k0 <= 0) continue;
-                    const int rs = rt % kRaw;
-                    if (!warp_wait(&ctl->raw_full[rs], (rt / kRaw) & 1, abort, p.err, kDevTimeoutProducer)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint8_t *raw = smem + C::RAW_OFF + rs * C::RAW;
-                    uint8_t *dst = smem + (h < 2 ? C::K_OFF : C::V_OFF) + st * C::TILE;
-                    // all of the thread's codes first: the stores below may not be reordered with loads
-                    constexpr int IT = 64 * CPR / 128;
-                    uint4 v[IT];
+                const int st = ct % C::ST, rs = ct % C::NR, row0 = (warp - 12) * 32;
+                uint32_t fv = 0, fk = 0;  // factors of row row0 + lane of K and V, f16 twice
 #pragma unroll
-                    for (int i = 0; i < IT; i++) v[i] = *reinterpret_cast<const uint4 *>(raw + (i * 128 + tid) * 16);
-                    const uint32_t kb = h == 0 ? raw[64 * D + tid] : 0u, vb = h == 0 ? raw[64 * D + 128 + tid] : 0u;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->raw_empty[rs]);
-                    rt++;
+                for (int h = 0; h < 2; h++) {  // K, V
+                    if (!warp_wait(h ? &ctl->v_empty[st] : &ctl->k_empty[st], ((ct / C::ST) & 1) ^ 1, abort, p.err, kDevTimeoutProducer) ||
+                        !warp_wait(&ctl->raw_full[h][rs], (ct / C::NR) & 1, abort, p.err, kDevTimeoutProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    // all of the lane's codes first: the raw tile is free, and no load waits behind a store
+                    const uint8_t *raw = smem + C::RAW_OFF + (h * C::NR + rs) * C::RAW + row0 * D;
+                    uint4 v[CPR];
+#pragma unroll
+                    for (int i = 0; i < CPR; i++) v[i] = *reinterpret_cast<const uint4 *>(raw + (i * 32 + lane) * 16);
+                    uint32_t kb = 0, vb = 0;
                     if (h == 0) {
-                        // the tile's scales, a key a thread; NaN vectors (255) and what lies beyond the last key do not
-                        // move the references
-                        const uint32_t tk = __reduce_max_sync(0xffffffffu, tid < nv && kb != 255u ? kb : 0u);
-                        const uint32_t tv = __reduce_max_sync(0xffffffffu, tid < nv && vb != 255u ? vb : 0u);
+                        kb = smem[C::RSC_OFF + rs * 2 * kKeys + row0 + lane];
+                        vb = smem[C::RSC_OFF + rs * 2 * kKeys + kKeys + row0 + lane];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->raw_empty[h][rs]);
+                    if (h == 0) {
+                        // NaN vectors (255) and what lies beyond the last key do not move the references
+                        const bool in = row0 + lane < nv;
+                        const uint32_t tk = __reduce_max_sync(0xffffffffu, in && kb != 255u ? kb : 0u);
+                        const uint32_t tv = __reduce_max_sync(0xffffffffu, in && vb != 255u ? vb : 0u);
                         if (lane == 0) ctl->top[ct & 1][warp - 12] = make_int2((int)tk, (int)tv);
                         named_bar(1, 128);
                         int kref = 0;
@@ -752,53 +741,46 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                             kref = max(kref, t.x);
                             vref = max(vref, t.y);
                         }
-                        // 2^(byte - reference + 6) in f16
-                        auto factor = [](uint32_t b, int ref) {
-                            const float f = b == 255u ? __uint_as_float(0x7fffffffu) : pow2((int)b - ref + 6);
+                        // 2^(byte - reference + 6)
+                        auto factor = [&](uint32_t b, int ref) {
+                            const float f = !in ? 0.f : b == 255u ? __uint_as_float(0x7fffffffu) : pow2((int)b - ref + 6);
                             return pack_f16(f, f);
                         };
-                        ctl->mul[ct & 1][0][tid] = factor(kb, kref);
-                        ctl->mul[ct & 1][1][tid] = factor(vb, vref);
+                        fk = factor(kb, kref);
+                        fv = factor(vb, vref);
                         if (tid == 0) reinterpret_cast<Refs *>(smem + C::SC_OFF)[ct % (2 * C::ST)] = Refs{kref, vref};
-                        named_bar(1, 128);
                     }
-                    const uint32_t *mul = ctl->mul[ct & 1][h >> 1] + k0;
-                    uint32_t mr[IT];
+                    if (nv - row0 < 32) {  // beyond the last key: zeros, whatever is there
 #pragma unroll
-                    for (int i = 0; i < IT; i++) {
-                        const int r = (i * 128 + tid) / CPR;
-                        mr[i] = mul[r];
-                        if (k0 + r >= nv) {  // whatever is there: zeros
-                            v[i] = make_uint4(0, 0, 0, 0);
-                            mr[i] = 0u;
-                        }
+                        for (int i = 0; i < CPR; i++)
+                            if (row0 + (i * 32 + lane) / CPR >= nv) v[i] = make_uint4(0, 0, 0, 0);
                     }
+                    uint8_t *dst = smem + (h ? C::V_OFF : C::K_OFF) + st * C::TILE + row0 * 128;
 #pragma unroll
-                    for (int i = 0; i < IT; i++) {
-                        const int id = i * 128 + tid, r = id / CPR, ch = id % CPR;
-                        uint4 lo, hi4;
+                    for (int i = 0; i < CPR; i++) {
+                        const int r = (i * 32 + lane) / CPR, ch = lane % CPR;
+                        const uint32_t f = __shfl_sync(0xffffffffu, h ? fv : fk, r);
+                        uint4 lo, hi;
                         to_f16(v[i].x, lo.x, lo.y);
                         to_f16(v[i].y, lo.z, lo.w);
-                        to_f16(v[i].z, hi4.x, hi4.y);
-                        to_f16(v[i].w, hi4.z, hi4.w);
-                        lo = make_uint4(mul_f16x2(lo.x, mr[i]), mul_f16x2(lo.y, mr[i]), mul_f16x2(lo.z, mr[i]), mul_f16x2(lo.w, mr[i]));
-                        hi4 = make_uint4(mul_f16x2(hi4.x, mr[i]), mul_f16x2(hi4.y, mr[i]), mul_f16x2(hi4.z, mr[i]), mul_f16x2(hi4.w, mr[i]));
-                        // columns 16 ch .. + 15 of row k0 + r: two 16-byte chunks of the 128-byte swizzled row; the lanes
-                        // of the second 64 columns store theirs in the other order (their banks are the same)
-                        uint8_t *rowp = dst + (ch / 4) * (kKeys * 128) + (k0 + r) * 128;
-                        const int s = (k0 + r) & 7, a = 2 * (ch & 3), flip = D == 128 ? ch >> 2 : r & 1;
-                        *reinterpret_cast<uint4 *>(rowp + (((a + flip) ^ s) << 4)) = flip ? hi4 : lo;
-                        *reinterpret_cast<uint4 *>(rowp + (((a + 1 - flip) ^ s) << 4)) = flip ? lo : hi4;
+                        to_f16(v[i].z, hi.x, hi.y);
+                        to_f16(v[i].w, hi.z, hi.w);
+                        lo = make_uint4(mul_f16x2(lo.x, f), mul_f16x2(lo.y, f), mul_f16x2(lo.z, f), mul_f16x2(lo.w, f));
+                        hi = make_uint4(mul_f16x2(hi.x, f), mul_f16x2(hi.y, f), mul_f16x2(hi.z, f), mul_f16x2(hi.w, f));
+                        // columns 16 ch .. + 15 of the row: two 16-byte chunks of its 128-byte swizzled piece; the lanes of
+                        // the second 64 columns store theirs in the other order (their banks are the same)
+                        uint8_t *rowp = dst + (ch / 4) * (kKeys * 128) + r * 128;
+                        const int s = r & 7, a = 2 * (ch & 3), flip = ch >> 2;
+                        *reinterpret_cast<uint4 *>(rowp + (((a + flip) ^ s) << 4)) = flip ? hi : lo;
+                        *reinterpret_cast<uint4 *>(rowp + (((a + 1 - flip) ^ s) << 4)) = flip ? lo : hi;
                     }
-                    if (k0 == 64 || nv <= 64) {
-                        fence_proxy_async();  // the operand tiles are read by the tensor cores (async proxy)
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(h < 2 ? &ctl->k_full[st] : &ctl->v_full[st]);
-                        // the part's Q between its first K and V: it arrives when the part before has done its last scores
-                        if (j == 0 && h < 2 && !rewrite_q(P)) {
-                            ok = false;
-                            break;
-                        }
+                    fence_proxy_async();  // the operand tiles are read by the tensor cores (async proxy)
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(h ? &ctl->v_full[st] : &ctl->k_full[st]);
+                    // the part's Q between its first K and V: it arrives when the part before has done its last scores
+                    if (j == 0 && h == 0 && !rewrite_q(P)) {
+                        ok = false;
+                        break;
                     }
                 }
             }
