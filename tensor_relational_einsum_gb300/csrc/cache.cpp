@@ -42,8 +42,9 @@ ea_status batch_args(const ea_page_batch *b, int32_t page, int64_t rows) {
     return EA_OK;
 }
 
-PgTable table_of(const ea_page_batch *b, int64_t rows) {
+PgTable table_of(const ea_page_batch *b, int32_t page, int64_t rows) {
     PgTable t{};
+    t.cap = (int64_t)b->max_pages * page;
     t.pages = b->pages;
     t.starts = b->starts;
     t.lens = b->lens;
@@ -115,7 +116,7 @@ ea_status rows_call(const char *what, bool read, ea_cache cache, const ea_page_b
     s = here(cache, &c);
     if (s) return s;
     PgRows p{};
-    p.t = table_of(batch, rows);
+    p.t = table_of(batch, cache->page, rows);
     p.c = pool_of(cache);
     p.k = k->arena;
     p.v = v->arena;
@@ -235,17 +236,19 @@ ea_status attn_shape(ea_cache cache, const ea_page_batch *batch, ea_relation q, 
 struct AttnPlans {
     PgPlan tokens;
     PgPlan chunks;
+    PgExpand expand;
     size_t bytes;
 };
 
 AttnPlans plans_of(const ea_cache_s *cache, const ea_page_batch *batch, int64_t rows, int64_t heads, int causal) {
     AttnPlans a{};
-    const PgTable t = table_of(batch, rows);
+    const PgTable t = table_of(batch, cache->page, rows);
     const int group = (int)(heads / cache->heads);
     a.tokens = plan_cache_tokens(t, pool_of(cache), group, causal, cache->num_sms);
     a.chunks = plan_cache_chunks(t, pool_of(cache), group, causal, cache->num_sms,
                                  a.tokens.ctas ? a.tokens.split.max_rows + 1 : 1);
-    a.bytes = a.tokens.bytes + a.chunks.bytes;
+    if (a.chunks.ctas > 0) a.expand = plan_cache_expand(t, pool_of(cache), group);
+    a.bytes = a.tokens.bytes + a.chunks.bytes + a.expand.bytes;
     return a;
 }
 
@@ -260,12 +263,19 @@ ea_status encode(DevCtx *c, const void *base, uint64_t d0, uint64_t d1, uint64_t
 }
 
 // Tensor maps of a chunk launch: a tile of Q is the group's heads of `tok / 2`
-// tokens; a page of K or V is `page` vectors.
+// tokens; a page of K or V is `page` vectors.  `wide`: the pages are the bf16
+// ones in the workspace (pages of 128), not the cache's.
 ea_status chunk_maps(DevCtx *c, ea_cache_s *cache, const ea_relation_s *q, int64_t heads, int64_t rows, const PgSplit &sp,
-                     PgMaps *m) {
+                     const PgPool *wide, PgMaps *m) {
     memset(m, 0, sizeof *m);
     ea_status s = encode(c, q->arena, cache->dim, heads, rows, sp.group, sp.tok / 2, &m->q);
-    if (s || cache->format != EA_CACHE_BF16) return s;
+    if (s) return s;
+    if (wide) {
+        const uint64_t vecs = (uint64_t)wide->n_pages * wide->heads << wide->page_log2;
+        s = encode(c, wide->k, wide->dim, vecs, 1, 1 << wide->page_log2, 1, &m->k);
+        return s ? s : encode(c, wide->v, wide->dim, vecs, 1, 1 << wide->page_log2, 1, &m->v);
+    }
+    if (cache->format != EA_CACHE_BF16) return EA_OK;
     if (!cache->mapped) {
         const uint64_t vecs = (uint64_t)cache->n_pages * cache->heads * cache->page;
         s = encode(c, cache->k, cache->dim, vecs, 1, cache->page, 1, &cache->k_map);
@@ -331,7 +341,7 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
         s = here(cache, &c);
         if (s) return s;
         PgAttn p{};
-        p.t = table_of(batch, rows);
+        p.t = table_of(batch, cache->page, rows);
         p.c = pool_of(cache);
         p.q = q->arena;
         p.o = out->arena;
@@ -346,7 +356,7 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
         const AttnPlans a = plans_of(cache, batch, rows, heads, p.causal);
         if (a.bytes > 0 && (!o.workspace || o.workspace_bytes < a.bytes || ((uintptr_t)o.workspace & 15) != 0))
             return set_error(EA_ERR_ARG, "ea_cache_attention: workspace of %zu bytes, 16-byte aligned, needed", a.bytes);
-        // chunks, tokens, merge: the tokens' CTAs fill the SMs that the chunks' leave
+        // (expansion,) chunks, tokens, merge: the tokens' CTAs fill the SMs that the chunks' leave
         char *ws = (char *)o.workspace;
         const PgWork wc = pg_work(a.chunks, ws), wt = pg_work(a.tokens, ws + a.chunks.bytes);
         int64_t ctas = 0;
@@ -354,9 +364,23 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
         cudaError_t e = cudaSuccess;
         if (a.chunks.ctas > 0) {
             PgMaps maps;
-            s = chunk_maps(c, cache, q, heads, rows, a.chunks.split, &maps);
+            PgAttn pc = p;
+            if (a.expand.blocks > 0) {
+                char *wide = ws + a.chunks.bytes + a.tokens.bytes;
+                pc.c = PgPool{wide, wide + a.expand.bytes / 2, nullptr, nullptr, (int64_t)p.t.n_seqs * a.expand.blocks, 7,
+                              p.c.heads, p.c.dim, EA_CACHE_BF16};
+                pc.t.pages = nullptr;
+                pc.t.page_stride = a.expand.blocks;
+            }
+            s = chunk_maps(c, cache, q, heads, rows, a.chunks.split, a.expand.blocks > 0 ? &pc.c : nullptr, &maps);
             if (s) return s;
-            e = launch_cache_chunks(p, a.chunks, maps, wc, (cudaStream_t)stream);
+            if (a.expand.blocks > 0) {
+                e = launch_cache_expand(p, a.chunks.split, a.expand, pc.c.k, (cudaStream_t)stream);
+                if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
+                ctas += (int64_t)p.t.n_seqs * a.expand.blocks * p.c.heads;
+                launches++;
+            }
+            e = launch_cache_chunks(pc, a.chunks, maps, wc, launches > 0, (cudaStream_t)stream);
             if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
             ctas += a.chunks.ctas;
             launches++;
@@ -386,7 +410,7 @@ extern "C" ea_status ea_cache_attention_split(const ea_page_batch *batch, int32_
         if (!split || !parts || !n_parts || ctas < 1 || page < 1) return set_error(EA_ERR_ARG, "ea_cache_attention_split: arguments");
         ea_status s = batch_args(batch, page, rows);
         if (s) return s;
-        const PgTable t = table_of(batch, rows);
+        const PgTable t = table_of(batch, page, rows);
         const PgSplit sp{split[0], split[1], split[2], split[3], split[4], split[5], split[6], 0};
         if (sp.heads < 1 || sp.group < 1 || sp.tok < 1 || sp.kt < 1) return set_error(EA_ERR_ARG, "ea_cache_attention_split: split");
         std::vector<PgSeq> seqs(t.n_seqs);
@@ -425,7 +449,7 @@ extern "C" ea_status ea_cache_check_batch(int64_t pages, int32_t page, const ea_
         if (page < 1 || pages < 1 || rows < 0) return set_error(EA_ERR_ARG, "ea_cache_check_batch: pages, page or rows");
         ea_status s = batch_args(batch, page, rows);
         if (s) return s;
-        const PgTable t = table_of(batch, rows);
+        const PgTable t = table_of(batch, page, rows);
         std::unordered_set<int64_t> slots;
         for (int i = 0; i < t.n_seqs; i++) {
             PgSeq q;

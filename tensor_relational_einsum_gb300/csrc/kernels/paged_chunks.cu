@@ -71,9 +71,9 @@ template <bool E4M3>
 struct Regs {
     static constexpr int THREADS = E4M3 ? 512 : 384;
     static constexpr int LAUNCH = E4M3 ? 128 : 168;
-    static constexpr int SOFTMAX = E4M3 ? 184 : 208;
+    static constexpr int SOFTMAX = E4M3 ? 176 : 208;
     static constexpr int CTL = E4M3 ? 72 : 88;
-    static constexpr int CONV = 72;
+    static constexpr int CONV = 88;
     static_assert(128 * (2 * SOFTMAX + CTL + (E4M3 ? CONV : 0)) <= THREADS * LAUNCH, "register split");
 };
 
@@ -197,7 +197,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::CTL_OFF);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     volatile int *abort = &ctl->abort;
-    const Seqs seqs{p.t, p.c.page_log2, p.err};
+    const Seqs seqs{p.t, p.err};
     const int half_tok = sp.tok / 2;      // tokens of a tile
     const int half_rows = half_tok * sp.group;
 
@@ -232,7 +232,8 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     if (warp == 9) tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
     tc_fence_before();
     let_next_start();
-    take_shares<R::THREADS>(p.t, sp, p.c.page_log2, p.err, ctl->scan, 1, &ctl->share);
+    take_shares<R::THREADS>(p.t, sp, p.err, ctl->scan, 1, &ctl->share);
+    wait_for_previous();  // expanded pages
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
@@ -259,10 +260,11 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         while (ok && next_part(P, kDevTimeoutProducer)) {
             // The number of this lane's page of tile j, read a tile ahead: the reads of a tile's pages do not wait for
             // one another, nor the copies for them.
-            auto look = [&](int j) {
+            auto look = [&](int j) -> int32_t {
                 const int key = (P.u0 + j) * kKeys + (lane << lg);
-                return j < P.tiles && (lane << lg) < kKeys && key < P.end
-                           ? __ldg(p.t.pages + (int64_t)P.seq * p.t.page_stride + (key >> lg)) : 0;
+                if (j >= P.tiles || (lane << lg) >= kKeys || key >= P.end) return 0;
+                const int64_t at = (int64_t)P.seq * p.t.page_stride + (key >> lg);
+                return p.t.pages ? __ldg(p.t.pages + at) : (int32_t)at;
             };
             int32_t next = look(0);
             // Q, behind the first K and V: its buffers are free only when the part before has done its last scores
@@ -796,7 +798,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
 }
 
 template <int D, bool E4M3>
-cudaError_t launch(const PgAttn &p, const PgPlan &pl, const PgWork &w, const PgMaps &maps, cudaStream_t st) {
+cudaError_t launch(const PgAttn &p, const PgPlan &pl, const PgWork &w, const PgMaps &maps, bool early, cudaStream_t st) {
     using C = Cfg<D, E4M3>;
     using R = Regs<E4M3>;
     static bool configured[64] = {};
@@ -814,8 +816,7 @@ cudaError_t launch(const PgAttn &p, const PgPlan &pl, const PgWork &w, const PgM
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    cache_chunks_kernel<D, E4M3><<<pl.ctas, R::THREADS, C::SMEM, st>>>(p, pl.split, w, maps.q, maps.k, maps.v);
-    return cudaGetLastError();
+    return launch_after(cache_chunks_kernel<D, E4M3>, dim3(pl.ctas), R::THREADS, C::SMEM, st, early, p, pl.split, w, maps.q, maps.k, maps.v);
 }
 
 }  // namespace
@@ -840,9 +841,22 @@ PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causa
     return pl;
 }
 
-cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, const PgWork &w, cudaStream_t st) {
-    if (p.c.fmt == EA_CACHE_E4M3) return p.c.dim == 64 ? launch<64, true>(p, pl, w, maps, st) : launch<128, true>(p, pl, w, maps, st);
-    return p.c.dim == 64 ? launch<64, false>(p, pl, w, maps, st) : launch<128, false>(p, pl, w, maps, st);
+PgExpand plan_cache_expand(const PgTable &t, const PgPool &c, int group) {
+    PgExpand x{};
+    if (c.fmt != EA_CACHE_E4M3 || (int64_t)t.max_new * group < 2 * kRows) return x;
+    const int64_t blocks = (t.cap + kKeys - 1) / kKeys, vectors = blocks * kKeys * t.n_seqs * c.heads;
+    // Up to 4 GB.  A batch that could need more has so many long sequences that few of them can have long chunks; it
+    // keeps to the 8-bit pages.
+    if (vectors * c.dim * 4 > (int64_t)1 << 32) return x;
+    x.blocks = (int32_t)blocks;
+    x.bytes = (size_t)vectors * c.dim * 4;
+    return x;
+}
+
+cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, const PgWork &w, bool early, cudaStream_t st) {
+    if (p.c.fmt == EA_CACHE_E4M3)
+        return p.c.dim == 64 ? launch<64, true>(p, pl, w, maps, early, st) : launch<128, true>(p, pl, w, maps, early, st);
+    return p.c.dim == 64 ? launch<64, false>(p, pl, w, maps, early, st) : launch<128, false>(p, pl, w, maps, early, st);
 }
 
 }  // namespace ea

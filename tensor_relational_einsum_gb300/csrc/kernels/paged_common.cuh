@@ -13,10 +13,9 @@ namespace pg {
 __device__ __forceinline__ void batch_fail(int *err) { atomicCAS(err, 0, (int)kDevBatch); }
 
 // Sequence i of the table; out of range: raises the error word, no rows.
-__device__ __forceinline__ PgSeq load_seq(const PgTable &t, int i, int page_log2, int *err) {
+__device__ __forceinline__ PgSeq load_seq(const PgTable &t, int i, int *err) {
     PgSeq s;
-    if (!pg_seq(__ldg(t.starts + i), __ldg(t.starts + i + 1), __ldg(t.lens + i), t.rows, t.max_new,
-                (int64_t)t.max_pages << page_log2, &s))
+    if (!pg_seq(__ldg(t.starts + i), __ldg(t.starts + i + 1), __ldg(t.lens + i), t.rows, t.max_new, t.cap, &s))
         batch_fail(err);
     return s;
 }

@@ -1,0 +1,69 @@
+// paged_expand.cu -- 8-bit pages of the sequences that the chunk kernel serves
+// as bf16 vectors [sequence][128 positions][head][position][dim] in the call's
+// workspace, for chunks whose keys are read by many row tiles.
+//
+// The chunk kernel can rewrite 8-bit tiles itself, but does so once for every
+// 256 rows, next to products that take all of shared memory's bandwidth: a
+// tile then takes 6000 cycles instead of 3800.  Writing 2 bytes and reading
+// them from L2 once for 256 rows is cheaper from about that many rows on
+// (2048 tokens after 14336, 32 heads over 8: 620 us there, 410 us here with
+// this kernel; 32 tokens after 8160 in 8 sequences: 120 us there, 160 here).
+// Every cell is a bf16 value, so nothing is lost.  Bound by HBM: one byte read
+// and two written a cell.
+#include "paged_common.cuh"
+
+namespace ea {
+namespace {
+
+using namespace pg;
+
+constexpr int kThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+cache_expand_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgSplit sp, char *wk, char *wv, int blocks) {
+    constexpr int CPR = D / 16, IT = 128 * CPR / kThreads;  // 16-code chunks of a vector; of a thread and tensor
+    let_next_start();
+    const int head = blockIdx.x % p.c.heads, at = blockIdx.x / p.c.heads, x = at % blocks, i = at / blocks;
+    const PgSeq s = load_seq(p.t, i, p.err);
+    const int key0 = x * 128, lg = p.c.page_log2;
+    if (!pg_served(s, sp) || key0 >= s.len) return;
+    const int64_t out0 = ((int64_t)at * p.c.heads + head) * 128;  // first vector of the block in the workspace
+#pragma unroll 4
+    for (int it = 0; it < IT; it++) {
+        const int id = it * kThreads + threadIdx.x, r = id / CPR, ch = id % CPR, key = key0 + r;
+        if (key >= s.len) break;
+        const int32_t g = check_page(__ldg(p.t.pages + (int64_t)i * p.t.page_stride + (key >> lg)), p.c.n_pages, p.err);
+        const int64_t vec = pg_vec(p.c, g, head, key & ((1 << lg) - 1));
+        const uint4 cells[2] = {__ldg(reinterpret_cast<const uint4 *>(p.c.k + vec * D) + ch),
+                                __ldg(reinterpret_cast<const uint4 *>(p.c.v + vec * D) + ch)};
+        const float scale[2] = {scale_value(__ldg(p.c.ks + vec)), scale_value(__ldg(p.c.vs + vec))};
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            const uint32_t u[4] = {cells[w].x, cells[w].y, cells[w].z, cells[w].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[q >> 1] >> (16 * (q & 1))), __NV_E4M3));
+                const float2 f = __half22float2(h);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * scale[w], f.y * scale[w]);
+                o[q] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            uint4 *dst = reinterpret_cast<uint4 *>((w ? wv : wk) + (out0 + r) * D * 2) + 2 * ch;
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_expand(const PgAttn &p, const PgSplit &sp, const PgExpand &x, char *ws, cudaStream_t st) {
+    const unsigned grid = (unsigned)((int64_t)p.t.n_seqs * x.blocks * p.c.heads);
+    char *wv = ws + x.bytes / 2;
+    if (p.c.dim == 64) cache_expand_kernel<64><<<grid, kThreads, 0, st>>>(p, sp, ws, wv, x.blocks);
+    else cache_expand_kernel<128><<<grid, kThreads, 0, st>>>(p, sp, ws, wv, x.blocks);
+    return cudaGetLastError();
+}
+
+}  // namespace ea

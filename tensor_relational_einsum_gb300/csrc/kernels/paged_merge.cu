@@ -66,7 +66,7 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
     wait_for_previous();
     const PgCut c = w.cut[x];
     if (c.we == 0 || pg_first(c.total, c.parts, x - 1) > c.wi) return;  // not cut here, or merged by an earlier cut
-    const PgSeq s = load_seq(p.t, c.seq, p.c.page_log2, p.err);
+    const PgSeq s = load_seq(p.t, c.seq, p.err);
     const int n = min(sp.tok, s.n - c.item * sp.tok) * sp.group;  // the item's rows
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int r0 = blockIdx.y * kRowsPerCta, r1 = min(n, r0 + kRowsPerCta);

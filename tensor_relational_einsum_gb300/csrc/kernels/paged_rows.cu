@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
         const uint32_t row = vec[u] / (uint32_t)p.c.heads, head = vec[u] - row * (uint32_t)p.c.heads;
         const int i = find_seq(starts, n_seqs, (int32_t)row);
         if (i < 0) continue;
-        const PgSeq s = load_seq(p.t, i, p.c.page_log2, p.err);
+        const PgSeq s = load_seq(p.t, i, p.err);
         if (s.n == 0) continue;
         const int pos = s.len - s.n + ((int)row - s.first);
         if (s.n > s.len || pos < 0) {

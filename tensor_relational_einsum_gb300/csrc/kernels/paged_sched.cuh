@@ -34,12 +34,12 @@ __device__ __forceinline__ int64_t block_scan(int64_t u, int64_t *incl, int64_t 
 
 // Shares blockIdx.x * each .. + each - 1 of gridDim.x * each, into out[].
 template <int NT>
-__device__ __forceinline__ void take_shares(const PgTable &t, const PgSplit &sp, int page_log2, int *err, int64_t *scratch,
+__device__ __forceinline__ void take_shares(const PgTable &t, const PgSplit &sp, int *err, int64_t *scratch,
                                             int each, PgShare *out) {
     int64_t u = 0, incl, total = 0, last = 0;
     for (int base = 0; base < t.n_seqs; base += NT) {
         const int i = base + threadIdx.x;
-        u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, page_log2, err), sp) : 0;
+        u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, err), sp) : 0;
         last = block_scan<NT>(u, &incl, scratch);
         total += last;
     }
@@ -61,7 +61,7 @@ __device__ __forceinline__ void take_shares(const PgTable &t, const PgSplit &sp,
     for (int base = 0; x0 < parts && base < t.n_seqs; base += NT) {
         if (t.n_seqs > NT) {
             const int i = base + threadIdx.x;
-            u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, page_log2, err), sp) : 0;
+            u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, err), sp) : 0;
             last = block_scan<NT>(u, &incl, scratch);
         }
         for (int e = 0; u > 0 && e < each && x0 + e < parts; e++) {
@@ -79,9 +79,8 @@ __device__ __forceinline__ void take_shares(const PgTable &t, const PgSplit &sp,
 // Sequences of the batch for a PgWalk.
 struct Seqs {
     const PgTable &t;
-    int page_log2;
     int *err;
-    __device__ __forceinline__ PgSeq operator()(int i) const { return load_seq(t, i, page_log2, err); }
+    __device__ __forceinline__ PgSeq operator()(int i) const { return load_seq(t, i, err); }
     __device__ __forceinline__ int count() const { return t.n_seqs; }
 };
 

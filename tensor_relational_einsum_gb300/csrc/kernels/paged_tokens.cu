@@ -142,7 +142,7 @@ struct Loader {
             block = w.u0 * per;
             last = min((w.u0 + w.part()) * per, (end + keys - 1) / keys);
             if (block < last) break;
-            w.step(w.part(), sp, Seqs{p.t, p.c.page_log2, p.err});
+            w.step(w.part(), sp, Seqs{p.t, p.err});
         }
         more = w.left > 0;
         look(p);
@@ -182,7 +182,7 @@ struct Loader {
         if (++block < last) {
             look(p);
         } else {
-            w.step(w.part(), sp, Seqs{p.t, p.c.page_log2, p.err});
+            w.step(w.part(), sp, Seqs{p.t, p.err});
             enter(p, sp);
         }
     }
@@ -202,10 +202,10 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     let_next_start();
     const bool solo = sp.solo != 0;
-    take_shares<kThreads>(p.t, sp, p.c.page_log2, p.err, scan, solo ? 4 : 1, shares);
+    take_shares<kThreads>(p.t, sp, p.err, scan, solo ? 4 : 1, shares);
     const PgShare &share = shares[solo ? warp : 0];
     Loader<D, E4M3, MT> ld;
-    ld.w.begin(share, sp, Seqs{p.t, p.c.page_log2, p.err});
+    ld.w.begin(share, sp, Seqs{p.t, p.err});
     PgWalk w = ld.w;
     if (threadIdx.x == 0) note_cut(ws, share, w);
     if (share.count == 0) {
@@ -507,7 +507,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         p.l_out[at] = sum * f;
                     }
                 }
-            w.step(np, sp, Seqs{p.t, p.c.page_log2, p.err});
+            w.step(np, sp, Seqs{p.t, p.err});
             continue;
         }
 
@@ -594,7 +594,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         }
         __syncthreads();  // the scratch and s_ml are free
         first_part = false;
-        w.step(np, sp, Seqs{p.t, p.c.page_log2, p.err});
+        w.step(np, sp, Seqs{p.t, p.err});
     }
     cp_wait<0>();
     wait_for_previous();

@@ -44,9 +44,10 @@ struct PgPool {
 };
 
 struct PgTable {
-    const int32_t *pages, *starts, *lens;
+    const int32_t *pages, *starts, *lens;  // pages NULL: page x of sequence i is number i * page_stride + x
     int64_t page_stride;
     int64_t rows;        // dense rows
+    int64_t cap;         // positions that a sequence can have
     int32_t n_seqs, max_pages, max_new;
 };
 
@@ -119,12 +120,21 @@ inline PgWork pg_work(const PgPlan &pl, char *b) {
 constexpr int kPgTokenRows = 32;     // the most rows of a sequence (tokens x group) that it takes
 PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causal, int num_sms);
 cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, const PgWork &w, bool early, cudaStream_t st);
+// 8-bit pages as bf16 vectors in the workspace, in blocks of 128 positions.
+struct PgExpand {
+    int32_t blocks;              // of a sequence; 0: the chunk kernel reads the 8-bit pages itself
+    size_t bytes;                // K's vectors and V's
+};
+PgExpand plan_cache_expand(const PgTable &t, const PgPool &c, int group);
+cudaError_t launch_cache_expand(const PgAttn &p, const PgSplit &sp, const PgExpand &x, char *ws, cudaStream_t st);
+
 // Chunk kernel: tiles of 128 rows on the tensor cores.
 struct PgMaps {                  // tensor maps: Q's rows; the pools as [vectors][dim] (bf16)
     CUtensorMap q, k, v;
 };
 PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causal, int num_sms, int min_rows);
-cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, const PgWork &w, cudaStream_t st);
+cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, const PgWork &w, bool early,
+                                cudaStream_t st);
 
 // The merge of both kernels' cut items.
 struct PgMerge {
