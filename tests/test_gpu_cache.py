@@ -588,3 +588,161 @@ def test_generation_as_a_run(fmt):
     check()
     a, w = dense.to_dense().double(), got.to_dense().double()
     assert (a - w).norm() <= 2 * 2.0 ** -8 * 2 * a.norm()
+
+
+# ------------------------------------------ the rules that choose a variant
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kv,group,dim,page,seqs", ATTEND)
+def test_attention_with_a_promised_bound(kv, group, dim, page, seqs, fmt):
+    """max_new says how long chunks can be: it rules kernels out, and with fewer than 256 rows to a sequence the chunk
+    kernel reads 8-bit pages itself."""
+    b = cu.Batch(seqs, page, seed=17)
+    c = nan_cache(b, kv, dim, fmt)
+    rng = np.random.default_rng(18)
+    held = fill(c, b, rng)
+    attend(b, c, held, group, rng, max_new=max(n for n, _ in seqs))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [(1, 4), (3, 4), (2, 9), (16, 1)])
+def test_many_short_sequences(rows, dim, fmt):
+    """At least 608 items of up to 512 positions: a warp an item."""
+    n, group = rows
+    rng = np.random.default_rng(19)
+    seqs = [(int(rng.integers(0, n + 1)), int(t)) for t in rng.integers(0, 80, size=200)] + [(n, 512), (n, 511), (n, 0), (n, 17)] * 2
+    b = cu.Batch(seqs, 16, behind=1)
+    c = nan_cache(b, 3, dim, fmt)
+    held = fill(c, b, rng)
+    attend(b, c, held, group, rng, max_new=n)
+
+
+@pytest.mark.parametrize("n", [1, 5, 30, 100])
+def test_scales_far_apart(n):
+    """8-bit vectors whose scales spread over 2^16 within a tile and move along the positions: f16 operands brought to a
+    common reference must keep every one of them."""
+    from tensor_relational_einsum_gb300.relation import check
+    b = cu.Batch([(n, 400), (n, 1111)], 16)
+    c = nan_cache(b, 2, 128, "e4m3")
+    rng = np.random.default_rng(20)
+    held = []
+    kc, vc = c.k.view(torch.uint8).cpu(), c.v.view(torch.uint8).cpu()
+    ks, vs = c.k_scale.cpu(), c.v_scale.cpu()
+    for i in range(2):
+        pg, sl = b.places(i)
+        pair = []
+        for cells, scale in ((kc, ks), (vc, vs)):
+            t = int(b.lens[i])
+            grow = np.exp2(rng.integers(-8, 9, size=(t, 2, 1)) + 4.0 * np.arange(t)[:, None, None] / t)
+            x = rng.normal(size=(t, 2, 128)) * (grow if cells is vc else np.exp2(rng.integers(-10, 1, size=(t, 2, 1))))
+            e = cu.e4m3_scale(x)
+            y = cu.e4m3_round(x / np.exp2(e)[..., None])
+            cells[pg, :, sl] = torch.from_numpy(y).to(torch.float8_e4m3fn).view(torch.uint8)
+            scale[pg, :, sl] = torch.from_numpy((e + 127).astype(np.uint8))
+            pair.append(y * np.exp2(e)[..., None])
+        held.append(pair)
+    c.k.copy_(kc.view(torch.float8_e4m3fn))
+    c.v.copy_(vc.view(torch.float8_e4m3fn))
+    c.k_scale.copy_(ks)
+    c.v_scale.copy_(vs)
+    check()
+    for max_new in (n, 0):
+        attend(b, c, held, 2, rng, max_new=max_new)
+
+
+@pytest.mark.parametrize("spread", [1e-30, 1e-6, 1e6, 1e15])
+def test_queries_and_keys_of_any_size(spread):
+    """Q far from 1 and K as far the other way: the scores are ordinary."""
+    for n in (1, 50):
+        b = cu.Batch([(n, 333)], 16)
+        c = nan_cache(b, 1, 64, "e4m3")
+        rng = np.random.default_rng(21)
+        held = fill(c, b, rng)
+        pg, sl = b.places(0)
+        shift = int(np.round(np.log2(spread)))
+        s = c.k_scale.cpu()
+        s[pg, :, sl] = (s[pg, :, sl].int() - shift).to(torch.uint8)
+        c.k_scale.copy_(s)
+        held[0][0] = held[0][0] * 2.0 ** -shift
+        attend(b, c, held, 2, rng, spread=2.0 ** shift, max_new=n)
+
+
+@pytest.mark.parametrize("n,max_new", [(1, 1), (40, 40), (200, 200)])
+def test_a_stored_nan_reaches_the_rows_that_keep_it(n, max_new):
+    """A NaN vector of an 8-bit cache: rows before it in another tile, and other sequences, stay right."""
+    from tensor_relational_einsum_gb300 import cache_attention
+    from tensor_relational_einsum_gb300.relation import check
+    b = cu.Batch([(n, 400), (n, 450)], 16)
+    c = nan_cache(b, 1, 64, "e4m3")
+    rng = np.random.default_rng(22)
+    held = fill(c, b, rng)
+    c.v_scale[int(b.pages[0, 3]), 0, 5] = 255            # position 53 of sequence 0: all its rows keep it
+    q = torch.from_numpy(values(rng, (b.rows, 2, 64))).to(torch.bfloat16).cuda()
+    out = torch.zeros_like(q)
+    cache_attention(relation(q), c, on_gpu(b, max_new=max_new), out=relation(out))
+    check()
+    out = out.double().cpu().numpy()
+    keeps = 400 - n + np.arange(n) >= 53
+    assert np.isnan(out[:n][keeps]).all()
+    qd = q.double().cpu().numpy()
+    for h in range(2):
+        k, v = (x[:, 0] for x in held[1])
+        wo, _, _, big, slack = cu.softmax_attention(qd[n:, h], k, v, 450 - n + np.arange(n), 0.125, True)
+        assert (np.abs(out[n:, h] - wo) <= cu.out_bound(wo, big, slack, 450)).all()
+
+
+def test_workspace_is_checked_and_means_nothing():
+    """Too small a workspace is refused; whatever it holds, the result is the same."""
+    import ctypes
+    from tensor_relational_einsum_gb300 import _abi
+    from tensor_relational_einsum_gb300.relation import check
+    L = _abi.lib()
+    b = cu.Batch([(1, 3000), (70, 2000)], 16)
+    c = nan_cache(b, 1, 128, "e4m3")
+    rng = np.random.default_rng(23)
+    fill(c, b, rng)
+    q = torch.from_numpy(values(rng, (b.rows, 4, 128))).to(torch.bfloat16).cuda()
+    batch, r = on_gpu(b), relation(q)
+    need = ctypes.c_size_t()
+    assert L.ea_cache_attention_workspace(c.handle, batch.ref, r.handle, ctypes.byref(need)) == 0 and need.value > 0
+    got = []
+    for fill_byte in (0, 255, 127):
+        ws = torch.full((need.value,), fill_byte, dtype=torch.uint8, device="cuda")
+        out = torch.zeros_like(q)
+        o = relation(out)
+        for size, ptr, want in ((need.value - 1, ws.data_ptr(), 7), (need.value, None, 7), (need.value, ws.data_ptr() + 8, 7),
+                                (need.value, ws.data_ptr(), 0)):
+            opts = _abi.CacheAttnOpts(0.0, 1, None, None, ptr, size)
+            stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+            assert L.ea_cache_attention(c.handle, batch.ref, r.handle, ctypes.byref(opts), stream, o.handle) == want
+        check()
+        got.append(out)
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2]) and torch.isfinite(got[0]).all()
+
+
+def test_large_pool_offsets():
+    """A pool of more than 2^31 bytes and 2^32 elements' worth of offsets: pages at its far end."""
+    from tensor_relational_einsum_gb300 import PageBatch, PagedCache, cache_append, cache_attention, cache_read
+    from tensor_relational_einsum_gb300.relation import check
+    pages, page, heads, dim = 70000, 128, 4, 128          # 4.6e9 cells a tensor
+    k, v = (torch.empty(pages, heads, page, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    c = PagedCache(pages, page, heads, dim, k=k, v=v)
+    rng = np.random.default_rng(24)
+    n = 300
+    table = torch.tensor([[pages - 1, 5, pages - 2], [pages - 3, pages // 2, 0]], dtype=torch.int32, device="cuda")
+    batch = PageBatch(table, torch.tensor([0, n, n + 1], dtype=torch.int32, device="cuda"),
+                      torch.tensor([n, 1], dtype=torch.int32, device="cuda"))
+    x = [values(rng, (n + 1, heads, dim)) for _ in range(2)]
+    kr, vr = (relation(torch.from_numpy(t).to(torch.bfloat16).cuda()) for t in x)
+    cache_append(c, batch, kr, vr)
+    got = cache_read(c, batch, rows=n + 1)
+    assert all(torch.equal(g.to_dense(), w.to_dense()) for g, w in zip(got, (kr, vr)))
+    q = values(rng, (n + 1, heads, dim))
+    out = cache_attention(relation(torch.from_numpy(q).to(torch.bfloat16).cuda()), c, batch).to_dense().double().cpu().numpy()
+    check()
+    sc = float(np.float32(1 / np.sqrt(dim)))
+    for h in range(heads):
+        for rows, pos in ((slice(0, n), np.arange(n)), (slice(n, n + 1), np.arange(1))):
+            wo, _, _, big, slack = cu.softmax_attention(q[rows, h], x[0][rows, h], x[1][rows, h], pos, sc, True)
+            assert (np.abs(out[rows, h] - wo) <= cu.out_bound(wo, big, slack, n)).all()
