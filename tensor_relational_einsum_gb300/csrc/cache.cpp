@@ -412,7 +412,7 @@ extern "C" ea_status ea_cache_attention_split(const ea_page_batch *batch, int32_
         if (s) return s;
         const PgTable t = table_of(batch, page, rows);
         const PgSplit sp{split[0], split[1], split[2], split[3], split[4], split[5], split[6], 0};
-        if (sp.heads < 1 || sp.group < 1 || sp.tok < 1 || sp.kt < 1) return set_error(EA_ERR_ARG, "ea_cache_attention_split: split");
+        if (sp.heads < 1 || sp.group < 1 || sp.tok < 1 || sp.kt < 1 || ctas > 65535) return set_error(EA_ERR_ARG, "ea_cache_attention_split: split");
         std::vector<PgSeq> seqs(t.n_seqs);
         std::vector<int64_t> first(t.n_seqs + 1, 0);
         for (int i = 0; i < t.n_seqs; i++) {
@@ -433,8 +433,9 @@ extern "C" ea_status ea_cache_attention_split(const ea_page_batch *batch, int32_
             sh.count = pg_first(sh.total, sh.parts, x + 1) - sh.w0;
             sh.seq = (int32_t)(std::upper_bound(first.begin(), first.end(), sh.w0) - first.begin()) - 1;
             sh.off = sh.w0 - first[sh.seq];
+            sh.s = seqs[sh.seq];
             PgWalk w;
-            for (w.begin(sh, sp, get); w.left > 0; w.step(w.part(), sp, get)) {
+            for (w.begin(sh, sp); w.left > 0; w.step(w.part(), sp, get)) {
                 if (*n_parts == capacity) return set_error(EA_ERR_ARG, "ea_cache_attention_split: capacity");
                 const int64_t row[7] = {x, w.seq, w.head, w.item, w.u0, w.u0 + w.part(), w.units};
                 std::copy(row, row + 7, parts + 7 * (*n_parts)++);

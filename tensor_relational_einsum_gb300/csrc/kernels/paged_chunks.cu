@@ -480,7 +480,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         if (lane == 0) {
             // ------------------------------------------------ parts
             PgWalk w;
-            w.begin(ctl->share, sp, seqs);
+            w.begin(ctl->share, sp);
             note_cut(ws, ctl->share, w);
             for (uint32_t i = 0;; i++) {
                 const int b = i % kParts;

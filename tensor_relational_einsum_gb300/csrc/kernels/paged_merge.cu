@@ -7,7 +7,7 @@
 // so the result does not depend on which CTA was done first.  Bound by the
 // latency of reading the partial results, which are in L2, so all that a row
 // needs is asked for together: with few parts a warp takes two rows, with many
-// one row and eight parts at a time.
+// one row and eight parts at a time, and rows that leave warps idle are shared.
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -56,6 +56,7 @@ template <int D>
 __global__ void __launch_bounds__(32 * kWarps)
 cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgMerge mg) {
     constexpr int C = D / 32;
+    __shared__ float s_l[kWarps], s_a[kWarps][D];
     // the cuts of the first kernel, then those of the second
     const int k = (int)blockIdx.x < mg.cuts[0] ? 0 : 1;
     const int x = blockIdx.x - (k ? mg.cuts[0] : 0) + 1;
@@ -114,20 +115,23 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
         }
         return;
     }
-    // a warp a row, eight parts at a time
-    for (int row = r0 + warp; row < r1; row += kWarps) {
+    // many parts, eight at a time; with few rows several warps share a row's parts
+    const int left = r1 - r0, share = left <= 1 ? 8 : left <= 2 ? 4 : left <= 4 ? 2 : 1, sub = warp % share;
+    for (int row0 = r0; row0 < r1; row0 += kWarps / share) {
+        const int row = row0 + warp / share;
+        const bool in = row < r1;
         float m = -INFINITY;
-        for (int i = lane; i < count; i += 32) m = fmaxf(m, __ldcg(&w.ml[at(i, row)]).x);
+        for (int i = lane; in && i < count; i += 32) m = fmaxf(m, __ldcg(&w.ml[at(i, row)]).x);
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float base = m == -INFINITY ? 0.f : m;
         float l = 0.f, a[C] = {};
-        for (int i0 = 0; i0 < count; i0 += 8) {
+        for (int i0 = sub; in && i0 < count; i0 += 8 * share) {
             float2 ml[8];
             float v[8][C];
 #pragma unroll
             for (int y = 0; y < 8; y++) {
-                const int i = i0 + y;
+                const int i = i0 + y * share;
                 ml[y] = make_float2(-INFINITY, 0.f);
 #pragma unroll
                 for (int k = 0; k < C; k++) v[y][k] = 0.f;
@@ -144,7 +148,19 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
                 for (int k = 0; k < C; k++) a[k] = fmaf(f, v[y][k], a[k]);
             }
         }
-        finish<D>(p, sp, s, c, row, lane, m, l, a);
+        if (share > 1) {  // the same order every time: sub 0, 1, ..
+            s_l[warp] = l;
+#pragma unroll
+            for (int k = 0; k < C; k++) s_a[warp][lane * C + k] = a[k];
+            __syncthreads();
+            for (int i = 1; sub == 0 && i < share; i++) {
+                l += s_l[warp + i];
+#pragma unroll
+                for (int k = 0; k < C; k++) a[k] += s_a[warp + i][lane * C + k];
+            }
+        }
+        if (in && sub == 0) finish<D>(p, sp, s, c, row, lane, m, l, a);
+        if (share > 1) __syncthreads();
     }
 }
 

@@ -7,9 +7,11 @@
 // bounds, page number) before a vector's address is known.  So
 //   - a thread takes the vectors of K and of V at the same place and asks
 //     for everything that does not depend on the table first;
-//   - the sequence bounds are staged in shared memory (one round trip for
-//     all of them) and searched there, not in global memory, where each of
-//     the log2(sequences) steps would wait for the last.
+//   - the sequences' bounds and lengths are staged in shared memory (one round
+//     trip for all of them) and searched there, not in global memory, where
+//     each of the log2(sequences) steps would wait for the last;
+//   - large calls take four vectors a thread, small ones one or two, so that
+//     they fill the SMs.
 // Quantising: the vector's largest magnitude over its lanes by shuffles on
 // the integer bits (an integer maximum orders fp32 magnitudes and puts
 // infinities and NaN on top), one power-of-two scale, codes rounded once by
@@ -58,13 +60,12 @@ __device__ __forceinline__ uint4 to_bf16(const float *x) {
     return u;
 }
 
-template <int D, bool F32, bool E4M3, bool READ>
+template <int D, bool F32, bool E4M3, bool READ, int U>
 __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_constant__ PgRows p) {
     constexpr int LPV = D / 8;                // lanes of a vector
     constexpr int VPB = kThreads / LPV;       // vectors of a pass
-    constexpr int U = 2;                      // passes of a CTA
     constexpr int RAW = F32 ? 2 : 1;          // 16-byte words of a lane's dense values
-    __shared__ int32_t s_starts[kStaged + 1];
+    __shared__ int32_t s_starts[kStaged + 1], s_lens[kStaged];  // U: passes of a CTA
     const int n_seqs = p.t.n_seqs;
     const uint32_t total = (uint32_t)(p.t.rows * p.c.heads);
     const int lane_v = threadIdx.x % LPV;
@@ -84,7 +85,10 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
     }
     const bool staged = n_seqs <= kStaged;
     if (staged) {
-        for (int i = threadIdx.x; i <= n_seqs; i += kThreads) s_starts[i] = __ldg(p.t.starts + i);
+        for (int i = threadIdx.x; i <= n_seqs; i += kThreads) {
+            s_starts[i] = __ldg(p.t.starts + i);
+            if (i < n_seqs) s_lens[i] = __ldg(p.t.lens + i);
+        }
         __syncthreads();
     }
     const int32_t *starts = staged ? s_starts : p.t.starts;
@@ -97,8 +101,11 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
         const uint32_t row = vec[u] / (uint32_t)p.c.heads, head = vec[u] - row * (uint32_t)p.c.heads;
         const int i = find_seq(starts, n_seqs, (int32_t)row);
         if (i < 0) continue;
-        const PgSeq s = load_seq(p.t, i, p.err);
-        if (s.n == 0) continue;
+        PgSeq s;
+        if (!pg_seq(starts[i], starts[i + 1], staged ? s_lens[i] : __ldg(p.t.lens + i), p.t.rows, p.t.max_new, p.t.cap, &s)) {
+            batch_fail(p.err);
+            continue;
+        }
         const int pos = s.len - s.n + ((int)row - s.first);
         if (s.n > s.len || pos < 0) {
             batch_fail(p.err);
@@ -204,13 +211,20 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
     }
 }
 
+template <int D, bool F32, bool E4M3, int U>
+cudaError_t launch_u(const PgRows &p, int64_t *ctas, cudaStream_t st) {
+    constexpr int per = U * kThreads / (D / 8);  // vectors of a CTA
+    *ctas = (p.t.rows * p.c.heads + per - 1) / per;
+    if (p.read) cache_rows_kernel<D, F32, E4M3, true, U><<<(unsigned)*ctas, kThreads, 0, st>>>(p);
+    else cache_rows_kernel<D, F32, E4M3, false, U><<<(unsigned)*ctas, kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
 template <int D, bool F32, bool E4M3>
 cudaError_t launch(const PgRows &p, int64_t *ctas, cudaStream_t st) {
-    constexpr int per = 2 * kThreads / (D / 8);  // vectors of a CTA
-    *ctas = (p.t.rows * p.c.heads + per - 1) / per;
-    if (p.read) cache_rows_kernel<D, F32, E4M3, true><<<(unsigned)*ctas, kThreads, 0, st>>>(p);
-    else cache_rows_kernel<D, F32, E4M3, false><<<(unsigned)*ctas, kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    // 4 vectors a thread once they make 8 CTAs for each of some 150 SMs
+    const int64_t threads = p.t.rows * p.c.heads * (D / 8);
+    return threads >= (int64_t)4 * 8 * 150 * kThreads ? launch_u<D, F32, E4M3, 4>(p, ctas, st) : launch_u<D, F32, E4M3, 1>(p, ctas, st);
 }
 
 }  // namespace

@@ -37,9 +37,11 @@ template <int NT>
 __device__ __forceinline__ void take_shares(const PgTable &t, const PgSplit &sp, int *err, int64_t *scratch,
                                             int each, PgShare *out) {
     int64_t u = 0, incl, total = 0, last = 0;
+    PgSeq q{};
     for (int base = 0; base < t.n_seqs; base += NT) {
         const int i = base + threadIdx.x;
-        u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, err), sp) : 0;
+        if (i < t.n_seqs) q = load_seq(t, i, err);
+        u = i < t.n_seqs ? pg_seq_units(q, sp) : 0;
         last = block_scan<NT>(u, &incl, scratch);
         total += last;
     }
@@ -54,6 +56,7 @@ __device__ __forceinline__ void take_shares(const PgTable &t, const PgSplit &sp,
         s.count = any ? pg_first(total, parts, x + 1) - s.w0 : 0;
         s.seq = 0;
         s.parts = parts;
+        s.s = PgSeq{0, 0, 0};
         out[threadIdx.x] = s;
     }
     __syncthreads();
@@ -61,7 +64,8 @@ __device__ __forceinline__ void take_shares(const PgTable &t, const PgSplit &sp,
     for (int base = 0; x0 < parts && base < t.n_seqs; base += NT) {
         if (t.n_seqs > NT) {
             const int i = base + threadIdx.x;
-            u = i < t.n_seqs ? pg_seq_units(load_seq(t, i, err), sp) : 0;
+            if (i < t.n_seqs) q = load_seq(t, i, err);
+            u = i < t.n_seqs ? pg_seq_units(q, sp) : 0;
             last = block_scan<NT>(u, &incl, scratch);
         }
         for (int e = 0; u > 0 && e < each && x0 + e < parts; e++) {
@@ -69,6 +73,7 @@ __device__ __forceinline__ void take_shares(const PgTable &t, const PgSplit &sp,
             if (run + incl - u <= w0 && w0 < run + incl) {
                 out[e].seq = base + threadIdx.x;
                 out[e].off = w0 - (run + incl - u);
+                out[e].s = q;
             }
         }
         run += last;

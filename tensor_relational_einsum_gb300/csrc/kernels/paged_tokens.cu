@@ -52,14 +52,14 @@ struct Cfg {
     static constexpr int ROWB = D * CELL;               // bytes of a key's vector
     // A warp takes G runs of 16 keys of a block: two where a run is 4 KB at most, because the waits, votes and
     // shuffles of a block cost the same for both and the products of one run fill the latencies of the other's.
-    // (Two tiles of rows at D = 128 leave no registers for it.)
-    static constexpr int G = ROWB == 256 || (D == 128 && MT == 2) ? 1 : 2;
+    static constexpr int G = ROWB == 256 ? 1 : 2;
     static constexpr int BLOCK = 64 * G;                // keys of a block
     static constexpr int TILE = 16 * G * ROWB;          // a warp's K (or V) of a block
     static constexpr int STAGE = 4 * 2 * TILE;          // a block
     static constexpr int S = STAGE == 16384 ? 5 : 3;
     static constexpr int SCALES = E4M3 ? 4 * 2 * 16 * G : 0;  // a stage's scale bytes
-    static constexpr int SMEM = S * (STAGE + SCALES);
+    static constexpr int Q_OFF = S * (STAGE + SCALES);  // two row tiles: Q's fragments, which registers cannot hold as well
+    static constexpr int SMEM = Q_OFF + (MT == 2 ? MT * (D / 16) * 512 : 0);
     static constexpr int CTAS = 2;
 };
 
@@ -201,11 +201,11 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     let_next_start();
-    const bool solo = sp.solo != 0;
+    const bool solo = MT == 1 && sp.solo != 0;
     take_shares<kThreads>(p.t, sp, p.err, scan, solo ? 4 : 1, shares);
     const PgShare &share = shares[solo ? warp : 0];
     Loader<D, E4M3, MT> ld;
-    ld.w.begin(share, sp, Seqs{p.t, p.err});
+    ld.w.begin(share, sp);
     PgWalk w = ld.w;
     if (threadIdx.x == 0) note_cut(ws, share, w);
     if (share.count == 0) {
@@ -233,7 +233,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         const int b0 = w.u0 * per, b1 = min((w.u0 + np) * per, (end + keys - 1) / keys);
         const int tok0 = w.item * sp.tok, nrows = min(sp.tok, w.s.n - tok0) * sp.group;
         // Q's fragments, and the keys that each of the thread's rows keeps
-        uint32_t q[MT][KS][4];
+        uint32_t q[MT][KS][4];  // (a row tile alone; else written to shared memory at once)
         float qs[MT][2];  // e4m3: a score in units of the row's scaled Q, times this, is the score
         int lim[MT][2];
 #pragma unroll
@@ -283,6 +283,28 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                             q[m][s][h + 2 * x] = in ? __ldg(reinterpret_cast<const uint32_t *>(src + (16 * s + 8 * x + 2 * tig) * 2)) : 0u;
                 }
             }
+        uint4 *q_sm = reinterpret_cast<uint4 *>(smem + C::Q_OFF) + lane;
+        if constexpr (MT == 2) {  // every warp has made all fragments; each stores a quarter
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int x = 0; x < KS; x++)
+                    if ((x & 3) == warp) q_sm[(m * KS + x) * 32] = make_uint4(q[m][x][0], q[m][x][1], q[m][x][2], q[m][x][3]);
+            __syncthreads();
+        }
+        // A fragment of step x of row tile m
+        auto qf = [&](int m, int x, uint32_t *f) {
+            if constexpr (MT == 2) {
+                const uint4 v = q_sm[(m * KS + x) * 32];
+                f[0] = v.x;
+                f[1] = v.y;
+                f[2] = v.z;
+                f[3] = v.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++) f[i] = q[m][x][i];
+            }
+        };
         float o[MT][NT][4] = {};
         float mref[MT][2], mmax[MT][2], l[MT][2];
 #pragma unroll
@@ -310,32 +332,42 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 if constexpr (E4M3) {
                     const uint8_t *ksm = smem + slot * C::STAGE + warp * 2 * C::TILE;
 #pragma unroll
-                    for (int x = 0; x < D / 64; x++)
+                    for (int x = 0; x < D / 64; x++) {
+                        uint4 v[N];
 #pragma unroll
-                        for (int n = 0; n < N; n++) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(ksm + chunk_at<C::ROWB, true>(n * 8 + gid, 4 * x + tig));
-                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                        for (int n = 0; n < N; n++)
+                            v[n] = *reinterpret_cast<const uint4 *>(ksm + chunk_at<C::ROWB, true>(n * 8 + gid, 4 * x + tig));
 #pragma unroll
-                            for (int y = 0; y < 4; y++) {
+                        for (int y = 0; y < 4; y++) {
+                            uint32_t f[MT][4];
+#pragma unroll
+                            for (int m = 0; m < MT; m++) qf(m, 4 * x + y, f[m]);
+#pragma unroll
+                            for (int n = 0; n < N; n++) {
                                 uint32_t lo, hi;
-                                to_f16(u[y], lo, hi);
+                                to_f16(y == 0 ? v[n].x : y == 1 ? v[n].y : y == 2 ? v[n].z : v[n].w, lo, hi);
 #pragma unroll
-                                for (int m = 0; m < MT; m++) mma16(s[m][n], q[m][4 * x + y], lo, hi);
+                                for (int m = 0; m < MT; m++) mma16(s[m][n], f[m], lo, hi);
                             }
                         }
+                    }
                 } else {
 #pragma unroll
-                    for (int x = 0; x < KS; x++)
+                    for (int x = 0; x < KS; x++) {
+                        uint32_t f[MT][4];
+#pragma unroll
+                        for (int m = 0; m < MT; m++) qf(m, x, f[m]);
 #pragma unroll
                         for (int g = 0; g < C::G; g++) {
                             uint32_t u[4];
                             ldsm4(kt + chunk_at<C::ROWB, false>(g * 16 + (lane >> 4) * 8 + (lane & 7), 2 * x + ((lane >> 3) & 1)), u);
 #pragma unroll
                             for (int m = 0; m < MT; m++) {
-                                mma(s[m][2 * g], q[m][x], u[0], u[1]);
-                                mma(s[m][2 * g + 1], q[m][x], u[2], u[3]);
+                                mma(s[m][2 * g], f[m], u[0], u[1]);
+                                mma(s[m][2 * g + 1], f[m], u[2], u[3]);
                             }
                         }
+                    }
                 }
                 float vsc[N][2];    // what V's scales make of the probabilities
                 float shift = 1.f;  // what a new vref makes of the accumulators
@@ -638,7 +670,7 @@ PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causa
     sp.kt = longest <= 512 ? 512 : c.fmt == EA_CACHE_E4M3 || c.dim == 64 ? 128 : 64;  // a block
     const int64_t units = (longest + sp.kt - 1) / sp.kt * t.n_seqs * c.heads;
     // Many short sequences: a warp an item, without barriers or a merge between warps.
-    sp.solo = sp.kt == 512 && (int64_t)t.n_seqs * c.heads >= 4 * (int64_t)num_sms;
+    sp.solo = sp.kt == 512 && pl.rows == 16 && (int64_t)t.n_seqs * c.heads >= 4 * (int64_t)num_sms;
     pl.ctas = (int)std::min<int64_t>(sp.solo ? (units + 3) / 4 : units, (int64_t)num_sms * 2);
     pl.bytes = units > t.n_seqs * (int64_t)c.heads ? pg_work_bytes(pl.ctas, pl.rows, c.dim) : 0;  // 0: a unit is an item
     return pl;

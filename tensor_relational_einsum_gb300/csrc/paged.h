@@ -194,7 +194,11 @@ EA_HD bool pg_served(const PgSeq &s, const PgSplit &sp) {
     return s.n > 0 && r >= sp.min_rows && r <= sp.max_rows;
 }
 
-EA_HD int pg_items(const PgSeq &s, const PgSplit &sp) { return (int)(((int64_t)s.n + sp.tok - 1) / sp.tok); }
+// ceil(a / b) for 0 <= a < 2^31, 0 < b < 2^31 (32 bits: a 64-bit division takes
+// a GPU thread a hundred cycles, and these are on the way to the first load).
+EA_HD int pg_ceil(int a, int b) { return (int)(((uint32_t)a + (uint32_t)b - 1u) / (uint32_t)b); }
+
+EA_HD int pg_items(const PgSeq &s, const PgSplit &sp) { return pg_ceil(s.n, sp.tok); }
 
 // Keys [0, e) that item j's last token keeps.
 EA_HD int pg_item_end(const PgSeq &s, const PgSplit &sp, int j) {
@@ -205,7 +209,7 @@ EA_HD int pg_item_end(const PgSeq &s, const PgSplit &sp, int j) {
 }
 
 EA_HD int pg_item_units(const PgSeq &s, const PgSplit &sp, int j) {
-    const int u = (int)(((int64_t)pg_item_end(s, sp, j) + sp.kt - 1) / sp.kt);
+    const int u = pg_ceil(pg_item_end(s, sp, j), sp.kt);
     return u > 0 ? u : 1;
 }
 
@@ -240,7 +244,14 @@ EA_HD int pg_item_of(const PgSeq &s, const PgSplit &sp, int64_t u) {
 }
 
 // Units [pg_first(x), pg_first(x + 1)) of CTA x, of `parts` with work.
-EA_HD int64_t pg_first(int64_t total, int parts, int x) { return total / parts * x + total % parts * x / parts; }
+EA_HD int64_t pg_first(int64_t total, int parts, int x) {
+    if (total <= INT32_MAX) {  // parts * parts < 2^32
+        const uint32_t t = (uint32_t)total, q = t / (uint32_t)parts, r = t - q * (uint32_t)parts;
+        return (int64_t)q * x + r * (uint32_t)x / (uint32_t)parts;
+    }
+    return total / parts * x + total % parts * x / parts;
+}
+EA_HD int64_t pg_div(int64_t a, int b) { return a <= INT32_MAX ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b; }
 EA_HD int pg_parts(int64_t total, int ctas) { return (int)(total < ctas ? total : ctas); }
 
 // A CTA's share of the units.
@@ -249,6 +260,7 @@ struct PgShare {
     int64_t total;     // units of the batch
     int64_t count;     // units of this CTA
     int32_t seq, parts;
+    PgSeq s;           // sequence `seq`
 };
 
 // The parts of items in a CTA's share, in order (Seqs: seqs(i) is sequence i,
@@ -260,16 +272,15 @@ struct PgWalk {
     int32_t u0;              // first unit of the current item not taken yet
     int32_t units;           // units of the current item
 
-    template <class Seqs>
-    EA_HD void begin(const PgShare &sh, const PgSplit &sp, const Seqs &seqs) {
+    EA_HD void begin(const PgShare &sh, const PgSplit &sp) {
         left = sh.count;
         seq = sh.seq;
         head = item = u0 = units = 0;
         if (left <= 0) return;
-        s = seqs(seq);
+        s = sh.s;
         if (pg_items(s, sp) == 1) {  // one item a head: no search
             units = pg_item_units(s, sp, 0);
-            head = (int)(sh.off / units);
+            head = (int)pg_div(sh.off, units);
             u0 = (int)(sh.off - (int64_t)head * units);
             return;
         }
