@@ -5,17 +5,19 @@
 // bytes for e4m3 codes.  Both operators move bytes and nothing else: the
 // bound is HBM, and for small calls the chain of dependent reads (sequence
 // bounds, page number) before a vector's address is known.  So
+//   - a CTA takes 16 rows of a few heads, and 16 of its threads look up where
+//     the rows live: the sequences' bounds and lengths are staged in shared
+//     memory (one round trip for all of them) and searched there, not in
+//     global memory, where each of the log2(sequences) steps would wait for
+//     the last;
 //   - a thread takes the vectors of K and of V at the same place and asks
 //     for everything that does not depend on the table first;
-//   - the sequences' bounds and lengths are staged in shared memory (one round
-//     trip for all of them) and searched there, not in global memory, where
-//     each of the log2(sequences) steps would wait for the last;
-//   - large calls take four vectors a thread, small ones one or two, so that
-//     they fill the SMs.
+//   - the scale bytes of neighbouring positions, which lie next to each other,
+//     are stored together (a byte at a time they were a fourth of all writes).
 // Quantising: the vector's largest magnitude over its lanes by shuffles on
-// the integer bits (an integer maximum orders fp32 magnitudes and puts
-// infinities and NaN on top), one power-of-two scale, codes rounded once by
-// the hardware conversion; the scaling itself is exact.
+// the integer bits (an integer maximum orders magnitudes and puts infinities
+// and NaN on top), one power-of-two scale, codes rounded once by the hardware
+// conversion; the scaling itself is exact.
 #include "paged_common.cuh"
 
 namespace ea {
@@ -24,6 +26,7 @@ namespace {
 using namespace pg;
 
 constexpr int kThreads = 256;
+constexpr int kRowsCta = 16;   // rows of a CTA
 constexpr int kStaged = 1024;  // sequence bounds staged in shared memory; longer batches are searched in global memory
 
 // The sequence that holds dense row r (starts[i] <= r < starts[i + 1]), or -1.
@@ -64,22 +67,27 @@ template <int D, bool F32, bool E4M3, bool READ, int U>
 __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_constant__ PgRows p) {
     constexpr int LPV = D / 8;                // lanes of a vector
     constexpr int VPB = kThreads / LPV;       // vectors of a pass
+    constexpr int HEADS = U * VPB / kRowsCta; // heads of a CTA
     constexpr int RAW = F32 ? 2 : 1;          // 16-byte words of a lane's dense values
-    __shared__ int32_t s_starts[kStaged + 1], s_lens[kStaged];  // U: passes of a CTA
-    const int n_seqs = p.t.n_seqs;
-    const uint32_t total = (uint32_t)(p.t.rows * p.c.heads);
+    __shared__ int32_t s_starts[kStaged + 1], s_lens[kStaged];
+    __shared__ int64_t s_base[kRowsCta];      // slot of the row's vector of head 0; -1: none
+    __shared__ uint8_t s_scale[2][HEADS][kRowsCta];
+    const int n_seqs = p.t.n_seqs, heads = p.c.heads, lg = p.c.page_log2;
+    const int row0 = blockIdx.x * kRowsCta, head0 = blockIdx.y * HEADS;
     const int lane_v = threadIdx.x % LPV;
-    uint32_t vec[U];
+    bool on[U];
+    int64_t dense[U];                         // the lane's dense element
     uint4 kx[U][RAW], vx[U][RAW];
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        vec[u] = (blockIdx.x * U + u) * VPB + threadIdx.x / LPV;
-        if (!READ && vec[u] < total) {
-            const int64_t at = ((int64_t)vec[u] * D + lane_v * 8) * (F32 ? 4 : 2);
+        const int v = u * VPB + threadIdx.x / LPV, row = row0 + v % kRowsCta, head = head0 + v / kRowsCta;
+        on[u] = row < p.t.rows && head < heads;
+        dense[u] = ((int64_t)row * heads + head) * D + lane_v * 8;
+        if (!READ && on[u]) {
 #pragma unroll
             for (int i = 0; i < RAW; i++) {
-                kx[u][i] = __ldg(reinterpret_cast<const uint4 *>(p.k + at) + i);
-                vx[u][i] = __ldg(reinterpret_cast<const uint4 *>(p.v + at) + i);
+                kx[u][i] = __ldg(reinterpret_cast<const uint4 *>(p.k + dense[u] * (F32 ? 4 : 2)) + i);
+                vx[u][i] = __ldg(reinterpret_cast<const uint4 *>(p.v + dense[u] * (F32 ? 4 : 2)) + i);
             }
         }
     }
@@ -91,32 +99,31 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
         }
         __syncthreads();
     }
-    const int32_t *starts = staged ? s_starts : p.t.starts;
-    // slot of each vector in the pool (-1: none), then the cells
+    if (threadIdx.x < kRowsCta) {
+        const int32_t *starts = staged ? s_starts : p.t.starts;
+        const int row = row0 + threadIdx.x;
+        int64_t base = -1;
+        const int i = row < p.t.rows ? find_seq(starts, n_seqs, row) : -1;
+        if (i >= 0) {
+            PgSeq s;
+            const bool ok = pg_seq(starts[i], starts[i + 1], staged ? s_lens[i] : __ldg(p.t.lens + i), p.t.rows, p.t.max_new,
+                                   p.t.cap, &s);
+            const int pos = s.len - s.n + (row - s.first);
+            if (ok && s.n <= s.len) {
+                const int32_t g = __ldg(p.t.pages + (int64_t)i * p.t.page_stride + (pos >> lg));
+                if (g >= 0 && g < p.c.n_pages) base = pg_vec(p.c, g, 0, pos & ((1 << lg) - 1));
+            }
+            if (base < 0) batch_fail(p.err);
+        }
+        s_base[threadIdx.x] = base;
+    }
+    __syncthreads();
     int64_t cell[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        cell[u] = -1;
-        if (vec[u] >= total) continue;
-        const uint32_t row = vec[u] / (uint32_t)p.c.heads, head = vec[u] - row * (uint32_t)p.c.heads;
-        const int i = find_seq(starts, n_seqs, (int32_t)row);
-        if (i < 0) continue;
-        PgSeq s;
-        if (!pg_seq(starts[i], starts[i + 1], staged ? s_lens[i] : __ldg(p.t.lens + i), p.t.rows, p.t.max_new, p.t.cap, &s)) {
-            batch_fail(p.err);
-            continue;
-        }
-        const int pos = s.len - s.n + ((int)row - s.first);
-        if (s.n > s.len || pos < 0) {
-            batch_fail(p.err);
-            continue;
-        }
-        const int32_t g = __ldg(p.t.pages + (int64_t)i * p.t.page_stride + (pos >> p.c.page_log2));
-        if (g < 0 || g >= p.c.n_pages) {
-            batch_fail(p.err);
-            continue;
-        }
-        cell[u] = pg_vec(p.c, g, (int)head, pos & ((1 << p.c.page_log2) - 1));
+        const int v = u * VPB + threadIdx.x / LPV;
+        const int64_t base = s_base[v % kRowsCta];
+        cell[u] = on[u] && base >= 0 ? base + ((int64_t)(head0 + v / kRowsCta) << lg) : -1;
     }
     if constexpr (!READ) {
 #pragma unroll
@@ -134,16 +141,23 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
                     }
                     if (cell[u] >= 0) *reinterpret_cast<uint4 *>(pool + (cell[u] * D + lane_v * 8) * 2) = out;
                 } else {
-                    float x[8];
-                    to_f32(raw, F32, x);
-                    uint32_t amax = 0;
+                    uint32_t amax = 0;  // bits of the largest magnitude, fp32
+                    if constexpr (F32) {
 #pragma unroll
-                    for (int i = 0; i < 8; i++) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+                        for (int i = 0; i < 8; i++) amax = max(amax, reinterpret_cast<const uint32_t *>(raw)[i] & 0x7fffffffu);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            amax = __vmaxu2(amax, reinterpret_cast<const uint32_t *>(raw)[i] & 0x7fff7fffu);
+                        amax = max(amax << 16, amax & 0xffff0000u);
+                    }
 #pragma unroll
                     for (int o = LPV / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                     const uint32_t b = scale_byte(amax);
-                    // 2^-(b - 127): normal for every b that scale_byte makes; 0 where the vector is NaN
-                    const float inv = b == 255u ? 0.f : __uint_as_float((254u - b) << 23);
+                    // 2^-(b - 127): normal for every b that scale_byte makes
+                    const float inv = __uint_as_float((254u - b) << 23);
+                    float x[8];
+                    to_f32(raw, F32, x);
                     uint32_t code[2];
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
@@ -153,12 +167,19 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
                                                                     __NV_SATFINITE, __NV_E4M3);
                         code[i] = lo | (hi << 16);
                     }
-                    if (b == 255u) code[0] = code[1] = 0u;
-                    if (cell[u] >= 0) {
-                        *reinterpret_cast<uint2 *>(pool + cell[u] * D + lane_v * 8) = make_uint2(code[0], code[1]);
-                        if (lane_v == 0) (w ? p.c.vs : p.c.ks)[cell[u]] = (uint8_t)b;
-                    }
+                    if (b == 255u) code[0] = code[1] = 0u;  // NaN
+                    if (cell[u] >= 0) *reinterpret_cast<uint2 *>(pool + cell[u] * D + lane_v * 8) = make_uint2(code[0], code[1]);
+                    const int v = u * VPB + threadIdx.x / LPV;
+                    if (lane_v == 0) s_scale[w][v / kRowsCta][v % kRowsCta] = (uint8_t)b;
                 }
+            }
+        }
+        if constexpr (E4M3) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * HEADS * kRowsCta; i += kThreads) {
+                const int r = i % kRowsCta, h = i / kRowsCta % HEADS, w = i / (kRowsCta * HEADS);
+                if (s_base[r] >= 0 && head0 + h < heads)
+                    (w ? p.c.vs : p.c.ks)[s_base[r] + ((int64_t)(head0 + h) << lg)] = s_scale[w][h][r];
             }
         }
     } else {
@@ -182,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
             if (cell[u] < 0) continue;
 #pragma unroll
             for (int w = 0; w < 2; w++) {
-                char *dst = (w ? p.v : p.k) + ((int64_t)vec[u] * D + lane_v * 8) * (F32 ? 4 : 2);
+                char *dst = (w ? p.v : p.k) + dense[u] * (F32 ? 4 : 2);
                 float x[8];
                 if constexpr (E4M3) {
                     const uint2 c = w ? vc[u] : kc[u];
@@ -213,18 +234,19 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
 
 template <int D, bool F32, bool E4M3, int U>
 cudaError_t launch_u(const PgRows &p, int64_t *ctas, cudaStream_t st) {
-    constexpr int per = U * kThreads / (D / 8);  // vectors of a CTA
-    *ctas = (p.t.rows * p.c.heads + per - 1) / per;
-    if (p.read) cache_rows_kernel<D, F32, E4M3, true, U><<<(unsigned)*ctas, kThreads, 0, st>>>(p);
-    else cache_rows_kernel<D, F32, E4M3, false, U><<<(unsigned)*ctas, kThreads, 0, st>>>(p);
+    constexpr int hc = U * kThreads / (D / 8) / kRowsCta;
+    const dim3 grid((unsigned)((p.t.rows + kRowsCta - 1) / kRowsCta), (unsigned)((p.c.heads + hc - 1) / hc));
+    *ctas = (int64_t)grid.x * grid.y;
+    if (p.read) cache_rows_kernel<D, F32, E4M3, true, U><<<grid, kThreads, 0, st>>>(p);
+    else cache_rows_kernel<D, F32, E4M3, false, U><<<grid, kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 template <int D, bool F32, bool E4M3>
 cudaError_t launch(const PgRows &p, int64_t *ctas, cudaStream_t st) {
-    // 4 vectors a thread once they make 8 CTAs for each of some 150 SMs
+    // two vectors a thread once they make 8 CTAs for each of some 150 SMs
     const int64_t threads = p.t.rows * p.c.heads * (D / 8);
-    return threads >= (int64_t)4 * 8 * 150 * kThreads ? launch_u<D, F32, E4M3, 4>(p, ctas, st) : launch_u<D, F32, E4M3, 1>(p, ctas, st);
+    return threads >= (int64_t)2 * 8 * 150 * kThreads ? launch_u<D, F32, E4M3, 2>(p, ctas, st) : launch_u<D, F32, E4M3, 1>(p, ctas, st);
 }
 
 }  // namespace
