@@ -67,7 +67,9 @@ struct Cfg {
 __device__ __forceinline__ void cp16n(uint32_t dst, const void *src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on) { cp16n(dst, src, on ? 16 : 0); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -165,15 +167,20 @@ struct Loader {
             if (C::G == 1 && nv <= 0) break;
             const int64_t vec = pg_vec(p.c, check_page(page[g], p.c.n_pages, p.err), w.head, key0 & ((1 << p.c.page_log2) - 1));
             const char *kp = p.c.k + vec * C::ROWB, *vp = p.c.v + vec * C::ROWB;
+            if (nv >= 16) {
 #pragma unroll
-            for (int i = 0; i < IT; i++) {
-                const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
-                cp16(ks + chunk_at<C::ROWB, E4M3>(g * 16 + r, c), kp + x * 16, r < nv);
-            }
+                for (int i = 0; i < IT; i++) {
+                    const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
+                    cp16(ks + chunk_at<C::ROWB, E4M3>(g * 16 + r, c), kp + x * 16);
+                    cp16(vs + chunk_at<C::ROWB, false>(g * 16 + r, c), vp + x * 16);
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i < IT; i++) {
-                const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
-                cp16(vs + chunk_at<C::ROWB, false>(g * 16 + r, c), vp + x * 16, r < nv);
+                for (int i = 0; i < IT; i++) {
+                    const int x = i * 32 + lane, r = x / CPR, c = x % CPR, n = r < nv ? 16 : 0;
+                    cp16n(ks + chunk_at<C::ROWB, E4M3>(g * 16 + r, c), kp + x * 16, n);
+                    cp16n(vs + chunk_at<C::ROWB, false>(g * 16 + r, c), vp + x * 16, n);
+                }
             }
             // a warp's scale bytes: K's runs, then V's
             if (E4M3 && lane < 2)
@@ -242,7 +249,8 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             for (int h = 0; h < 2; h++) {
                 const int r = m * 16 + h * 8 + gid, tok = tok0 + r / sp.group;
                 const bool in = r < nrows;
-                lim[m][h] = !in ? 0 : sp.causal ? max(0, min(w.s.len, w.s.len - w.s.n + tok + 1)) : w.s.len;
+                // rows without a token (Q = 0) keep all: they must not make the others look at every key
+                lim[m][h] = !in ? INT32_MAX : sp.causal ? max(0, min(w.s.len, w.s.len - w.s.n + tok + 1)) : w.s.len;
                 const char *src = p.q + ((int64_t)(w.s.first + (in ? tok : 0)) * p.qheads + w.head * sp.group +
                                          (in ? r % sp.group : 0)) * D * 2;
                 if constexpr (E4M3) {
@@ -315,6 +323,9 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 l[m][h] = 0.f;
                 if constexpr (!E4M3) qs[m][h] = 1.f;
             }
+        int least = INT32_MAX;  // keys that all of the thread's rows keep
+#pragma unroll
+        for (int m = 0; m < MT; m++) least = min(least, min(lim[m][0], lim[m][1]));
         int vref = 0;  // e4m3: the accumulators are in units of 2^(vref - 127 - 7)
 
         for (int b = b0; b < b1; b++) {
@@ -372,56 +383,47 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 float vsc[N][2];    // what V's scales make of the probabilities
                 float shift = 1.f;  // what a new vref makes of the accumulators
                 if constexpr (E4M3) {
-                    const uint8_t *sc = smem + C::S * C::STAGE + slot * C::SCALES + warp * 32 * C::G, *scv = sc + 16 * C::G;
-                    // bytes of keys beyond the end are 0 here; NaN vectors (255) do not move vref
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int g = 0; g < C::G; g++) {
-                        const uint4 all = *reinterpret_cast<const uint4 *>(scv + 16 * g);
-                        const uint32_t w4[4] = {all.x, all.y, all.z, all.w};
-#pragma unroll
-                        for (int i = 0; i < 4; i++) top = __vmaxu4(top, w4[i] & ~__vcmpeq4(w4[i], 0xffffffffu));
-                    }
-                    top = __vmaxu4(top, top >> 16);
-                    const int vmax = (int)max(top & 255u, (top >> 8) & 255u);
+                    // a lane's key: its scale bytes (0 beyond the end), turned into factors once and passed around.  NaN
+                    // vectors (255) do not move vref.
+                    const uint8_t *sc = smem + C::S * C::STAGE + slot * C::SCALES + warp * 32 * C::G;
+                    const int mine = C::G == 2 ? lane : lane & 15;
+                    const uint32_t kb = sc[mine], vb = sc[16 * C::G + mine];
+                    const int vmax = (int)__reduce_max_sync(0xffffffffu, vb == 255u ? 0u : vb);
                     if (vmax > vref) {
                         shift = pow2(vref - vmax);
                         vref = vmax;
                     }
+                    const float kf = scale_value(kb), vf = vb == 255u ? __uint_as_float(0x7fffffffu) : pow2((int)vb - vref + 7);
 #pragma unroll
-                    for (int n = 0; n < N; n++) {
-                        const uint32_t kb = *reinterpret_cast<const uint16_t *>(sc + n * 8 + 2 * tig);
-                        const uint32_t vb = *reinterpret_cast<const uint16_t *>(scv + n * 8 + 2 * tig);
-                        const float k0 = scale_value(kb & 255u), k1 = scale_value(kb >> 8);
+                    for (int n = 0; n < N; n++)
 #pragma unroll
                         for (int i = 0; i < 2; i++) {
-                            const uint32_t v = (vb >> (8 * i)) & 255u;
-                            vsc[n][i] = v == 255u ? __uint_as_float(0x7fffffffu) : pow2((int)v - vref + 7);
+                            const float k0 = __shfl_sync(0xffffffffu, kf, n * 8 + 2 * tig + i);
+                            vsc[n][i] = __shfl_sync(0xffffffffu, vf, n * 8 + 2 * tig + i);
+#pragma unroll
+                            for (int m = 0; m < MT; m++)
+#pragma unroll
+                                for (int h = 0; h < 2; h++) s[m][n][2 * h + i] *= k0;
                         }
-#pragma unroll
-                        for (int m = 0; m < MT; m++)
-#pragma unroll
-                            for (int h = 0; h < 2; h++) {
-                                s[m][n][2 * h] *= k0;
-                                s[m][n][2 * h + 1] *= k1;
-                            }
-                    }
                 }
+                const bool cut = __any_sync(0xffffffffu, least < key0 + 16 * C::G);  // some row drops some key
                 uint32_t pf[MT][C::G][4];
 #pragma unroll
                 for (int m = 0; m < MT; m++) {
                     float mx[2];
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const int keep = lim[m][h] - key0 - 2 * tig;  // of the thread's keys 0, 1, 8, 9, ..
+                        if (cut) {
+                            const int keep = lim[m][h] - key0 - 2 * tig;  // of the thread's keys 0, 1, 8, 9, ..
+#pragma unroll
+                            for (int n = 0; n < N; n++)
+#pragma unroll
+                                for (int e = 0; e < 2; e++)
+                                    if (n * 8 + e >= keep) s[m][n][2 * h + e] = -INFINITY;
+                        }
                         mx[h] = -INFINITY;
 #pragma unroll
-                        for (int n = 0; n < N; n++) {
-#pragma unroll
-                            for (int e = 0; e < 2; e++)
-                                if (n * 8 + e >= keep) s[m][n][2 * h + e] = -INFINITY;
-                            mx[h] = fmaxf(mx[h], fmaxf(s[m][n][2 * h], s[m][n][2 * h + 1]));
-                        }
+                        for (int n = 0; n < N; n++) mx[h] = fmaxf(mx[h], fmaxf(s[m][n][2 * h], s[m][n][2 * h + 1]));
                         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
                         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
                         mmax[m][h] = fmaxf(mmax[m][h], mx[h]);
@@ -456,9 +458,9 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         for (int n = 0; n < N; n++) {
                             float e0 = ex2(fmaf(s[m][n][2 * h], cq, nb)), e1 = ex2(fmaf(s[m][n][2 * h + 1], cq, nb));
                             l[m][h] += e0 + e1;
-                            if constexpr (E4M3) {  // a dropped key's scale byte may hold anything
-                                e0 = e0 == 0.f ? 0.f : e0 * vsc[n][0];
-                                e1 = e1 == 0.f ? 0.f : e1 * vsc[n][1];
+                            if constexpr (E4M3) {
+                                e0 *= vsc[n][0];
+                                e1 *= vsc[n][1];
                             }
                             pf[m][n >> 1][h + 2 * (n & 1)] = E4M3 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
                         }
