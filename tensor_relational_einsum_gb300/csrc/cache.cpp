@@ -391,7 +391,7 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
             ctas += a.tokens.ctas;
             launches++;
         }
-        PgMerge m{{wc, wt}, {a.chunks.split, a.tokens.split}, {wc.cut ? a.chunks.ctas - 1 : 0, wt.cut ? a.tokens.ctas - 1 : 0},
+        PgMerge m{{wc, wt}, {wc.cut ? a.chunks.ctas - 1 : 0, wt.cut ? a.tokens.ctas - 1 : 0},
                   {a.chunks.rows, a.tokens.rows}};
         if (m.cuts[0] + m.cuts[1] > 0) {
             e = launch_cache_merge(p, m, (cudaStream_t)stream);

@@ -481,7 +481,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             // ------------------------------------------------ parts
             PgWalk w;
             w.begin(ctl->share, sp);
-            note_cut(ws, ctl->share, w);
+            note_cut(ws, sp, ctl->share, w);
             for (uint32_t i = 0;; i++) {
                 const int b = i % kParts;
                 if (!mbar_wait(&ctl->part_empty[b], ((i / kParts) & 1) ^ 1, abort, p.err, kDevTimeoutProducer)) break;

@@ -32,11 +32,10 @@ __device__ __forceinline__ void load_acc(const float *src, int lane, float *v) {
 }
 
 template <int D>
-__device__ __forceinline__ void finish(const PgAttn &p, const PgSplit &sp, const PgSeq &s, const PgCut &c, int row, int lane,
-                                       float m, float l, const float *a) {
+__device__ __forceinline__ void finish(const PgAttn &p, const PgCut &c, int row, int lane, float m, float l, const float *a) {
     constexpr int C = D / 32;
     const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays NaN
-    const int64_t at = (int64_t)(s.first + c.item * sp.tok + row / sp.group) * p.qheads + c.head * sp.group + row % sp.group;
+    const int64_t at = (int64_t)(c.row0 + row / p.group) * p.qheads + c.head * p.group + row % p.group;
     uint32_t w[C / 2];
 #pragma unroll
     for (int k = 0; k < C / 2; k++) {
@@ -53,7 +52,7 @@ __device__ __forceinline__ void finish(const PgAttn &p, const PgSplit &sp, const
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, 4)
 cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgMerge mg) {
     constexpr int C = D / 32;
     __shared__ float s_l[kWarps], s_a[kWarps][D];
@@ -61,21 +60,17 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
     const int k = (int)blockIdx.x < mg.cuts[0] ? 0 : 1;
     const int x = blockIdx.x - (k ? mg.cuts[0] : 0) + 1;
     const PgWork &w = mg.w[k];
-    const PgSplit &sp = mg.split[k];
     const int rows = mg.rows[k];
     if ((int)blockIdx.y * kRowsPerCta >= rows) return;
     wait_for_previous();
     const PgCut c = w.cut[x];
     if (c.we == 0 || pg_first(c.total, c.parts, x - 1) > c.wi) return;  // not cut here, or merged by an earlier cut
-    const PgSeq s = load_seq(p.t, c.seq, p.err);
-    const int n = min(sp.tok, s.n - c.item * sp.tok) * sp.group;  // the item's rows
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int r0 = blockIdx.y * kRowsPerCta, r1 = min(n, r0 + kRowsPerCta);
+    const int r0 = blockIdx.y * kRowsPerCta, r1 = min(c.rows, r0 + kRowsPerCta);
     if (r0 >= r1) return;
     // parts: the last of CTA x - 1 (its only one if the item begins with it), then the first of x, x + 1, ...
     const int slot0 = 2 * (x - 1) + (pg_first(c.total, c.parts, x - 1) < c.wi ? 1 : 0);
-    int count = 1;
-    while (x - 1 + count < c.parts && pg_first(c.total, c.parts, x - 1 + count) < c.we) count++;
+    const int count = pg_before(c.total, c.parts, c.we) - (x - 1);
     auto at = [&](int i, int row) { return (int64_t)(i == 0 ? slot0 : 2 * (x - 1 + i)) * rows + row; };
 
     if (count <= 4) {
@@ -110,7 +105,7 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
 #pragma unroll
                     for (int k = 0; k < C; k++) a[k] = fmaf(f, v[y][i][k], a[k]);
                 }
-                finish<D>(p, sp, s, c, row + y, lane, m, l, a);
+                finish<D>(p, c, row + y, lane, m, l, a);
             }
         }
         return;
@@ -159,7 +154,7 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
                 for (int k = 0; k < C; k++) a[k] += s_a[warp + i][lane * C + k];
             }
         }
-        if (in && sub == 0) finish<D>(p, sp, s, c, row, lane, m, l, a);
+        if (in && sub == 0) finish<D>(p, c, row, lane, m, l, a);
         if (share > 1) __syncthreads();
     }
 }

@@ -91,7 +91,7 @@ struct Seqs {
 
 // Say where this CTA's share begins, if that is inside an item (no workspace:
 // the plan cuts no item).
-__device__ __forceinline__ void note_cut(const PgWork &w, const PgShare &sh, const PgWalk &k) {
+__device__ __forceinline__ void note_cut(const PgWork &w, const PgSplit &sp, const PgShare &sh, const PgWalk &k) {
     if (!w.cut) return;
     PgCut c{};
     c.total = sh.total;
@@ -99,9 +99,9 @@ __device__ __forceinline__ void note_cut(const PgWork &w, const PgShare &sh, con
     if (sh.count > 0 && k.u0 > 0) {
         c.wi = sh.w0 - k.u0;
         c.we = c.wi + k.units;
-        c.seq = k.seq;
         c.head = k.head;
-        c.item = k.item;
+        c.row0 = k.s.first + k.item * sp.tok;
+        c.rows = min(sp.tok, k.s.n - k.item * sp.tok) * sp.group;
     }
     w.cut[blockIdx.x] = c;
 }

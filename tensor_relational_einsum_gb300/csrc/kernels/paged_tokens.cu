@@ -214,7 +214,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     Loader<D, E4M3, MT> ld;
     ld.w.begin(share, sp);
     PgWalk w = ld.w;
-    if (threadIdx.x == 0) note_cut(ws, share, w);
+    if (threadIdx.x == 0) note_cut(ws, sp, share, w);
     if (share.count == 0) {
         wait_for_previous();
         return;

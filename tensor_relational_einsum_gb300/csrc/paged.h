@@ -86,8 +86,10 @@ struct PgSplit {
 struct PgCut {
     int64_t wi, we;              // the item's units [wi, we); we = 0: the range begins with an item, or is empty
     int64_t total;               // units of the batch
-    int32_t seq, head, item;
     int32_t parts;               // CTAs with units
+    int32_t head;
+    int32_t row0;                // the item's first dense row, and its rows (tokens x group)
+    int32_t rows;
 };
 
 struct PgWork {                  // the call's workspace
@@ -139,7 +141,6 @@ cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps 
 // The merge of both kernels' cut items.
 struct PgMerge {
     PgWork w[2];
-    PgSplit split[2];
     int32_t cuts[2];             // CTAs - 1; 0: none
     int32_t rows[2];
 };
@@ -250,6 +251,12 @@ EA_HD int64_t pg_first(int64_t total, int parts, int x) {
         return (int64_t)q * x + r * (uint32_t)x / (uint32_t)parts;
     }
     return total / parts * x + total % parts * x / parts;
+}
+// The CTAs whose first unit lies before unit u (0 < u <= total): total x / parts < u.
+EA_HD int pg_before(int64_t total, int parts, int64_t u) {
+    const int64_t a = u * parts;  // u <= 2^48, parts < 2^11
+    if (a <= INT32_MAX && total <= INT32_MAX) return (int)(((uint32_t)a + (uint32_t)total - 1u) / (uint32_t)total);
+    return (int)((a + total - 1) / total);
 }
 EA_HD int64_t pg_div(int64_t a, int b) { return a <= INT32_MAX ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b; }
 EA_HD int pg_parts(int64_t total, int ctas) { return (int)(total < ctas ? total : ctas); }
