@@ -634,20 +634,18 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 }
                 if (!mine) continue;
                 if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + (at * D + 32 * cc) * 2);
+                    uint32_t h[16];
 #pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        const float *g = reinterpret_cast<const float *>(o + 8 * q);
-                        dst[q] = make_uint4(pack_bf16(g[0] * f, g[1] * f), pack_bf16(g[2] * f, g[3] * f),
-                                            pack_bf16(g[4] * f, g[5] * f), pack_bf16(g[6] * f, g[7] * f));
-                    }
+                    for (int i = 0; i < 16; i++) h[i] = pack_bf16(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
+                    char *dst = p.o + (at * D + 32 * cc) * 2;
+                    st_32(dst, h);
+                    st_32(dst + 32, h + 8);
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(ws.acc + prow * D + 32 * cc);
 #pragma unroll
-                    for (int q = 0; q < 8; q++) {
-                        const float *g = reinterpret_cast<const float *>(o + 4 * q);
-                        dst[q] = make_float4(g[0] * f, g[1] * f, g[2] * f, g[3] * f);
-                    }
+                    for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    float *dst = ws.acc + prow * D + 32 * cc;
+#pragma unroll
+                    for (int q = 0; q < 4; q++) st_32(dst + 8 * q, o + 8 * q);
                 }
             }
             tc_fence_before();

@@ -52,6 +52,13 @@ __device__ __forceinline__ int32_t check_page(int32_t g, int64_t n_pages, int *e
     return 0;
 }
 
+// 32 bytes at once: as two stores of 16 each of them fills half a sector.
+__device__ __forceinline__ void st_32(void *dst, const uint32_t *x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 // The value of a scale byte: 2^(b - 127), NaN for 255.
 __device__ __forceinline__ float scale_value(uint32_t b) {
     return b == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(b ? b << 23 : 0x00400000u);

@@ -56,17 +56,20 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgMerge mg) {
     constexpr int C = D / 32;
     __shared__ float s_l[kWarps], s_a[kWarps][D];
-    // the cuts of the first kernel, then those of the second
-    const int k = (int)blockIdx.x < mg.cuts[0] ? 0 : 1;
-    const int x = blockIdx.x - (k ? mg.cuts[0] : 0) + 1;
+    // the cuts of the first kernel by groups of rows, then those of the second
+    int at_cut = blockIdx.x, k = 0;
+    if (at_cut >= mg.cuts[0] * mg.groups[0]) {
+        at_cut -= mg.cuts[0] * mg.groups[0];
+        k = 1;
+    }
+    const int x = at_cut / mg.groups[k] + 1, group = at_cut % mg.groups[k];
     const PgWork &w = mg.w[k];
     const int rows = mg.rows[k];
-    if ((int)blockIdx.y * kRowsPerCta >= rows) return;
     wait_for_previous();
     const PgCut c = w.cut[x];
     if (c.we == 0 || pg_first(c.total, c.parts, x - 1) > c.wi) return;  // not cut here, or merged by an earlier cut
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int r0 = blockIdx.y * kRowsPerCta, r1 = min(c.rows, r0 + kRowsPerCta);
+    const int r0 = group * kRowsPerCta, r1 = min(c.rows, r0 + kRowsPerCta);
     if (r0 >= r1) return;
     // parts: the last of CTA x - 1 (its only one if the item begins with it), then the first of x, x + 1, ...
     const int slot0 = 2 * (x - 1) + (pg_first(c.total, c.parts, x - 1) < c.wi ? 1 : 0);
@@ -162,9 +165,11 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
 }  // namespace
 
 cudaError_t launch_cache_merge(const PgAttn &p, const PgMerge &m, cudaStream_t st) {
-    const dim3 grid(m.cuts[0] + m.cuts[1], (std::max(m.rows[0], m.rows[1]) + kRowsPerCta - 1) / kRowsPerCta);
-    if (p.c.dim == 64) return launch_after(cache_merge_kernel<64>, grid, 32 * kWarps, 0, st, true, p, m);
-    return launch_after(cache_merge_kernel<128>, grid, 32 * kWarps, 0, st, true, p, m);
+    PgMerge g = m;
+    for (int k = 0; k < 2; k++) g.groups[k] = std::max(1, (m.rows[k] + kRowsPerCta - 1) / kRowsPerCta);
+    const dim3 grid(g.cuts[0] * g.groups[0] + g.cuts[1] * g.groups[1]);
+    if (p.c.dim == 64) return launch_after(cache_merge_kernel<64>, grid, 32 * kWarps, 0, st, true, p, g);
+    return launch_after(cache_merge_kernel<128>, grid, 32 * kWarps, 0, st, true, p, g);
 }
 
 }  // namespace ea

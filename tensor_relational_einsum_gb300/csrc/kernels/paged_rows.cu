@@ -63,13 +63,6 @@ __device__ __forceinline__ uint4 to_bf16(const float *x) {
     return u;
 }
 
-// 32 bytes at once: as two stores of 16 each of them fills half a sector.
-__device__ __forceinline__ void st_32(char *dst, const float *x) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]), "f"(x[1]), "f"(x[2]),
-                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
-}
-
 template <int D, bool F32, bool E4M3, bool READ, int U>
 __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_constant__ PgRows p) {
     constexpr int LPV = D / 8;                // lanes of a vector
@@ -227,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
                     to_f32(w ? vx[u] : kx[u], false, x);
                 }
                 if constexpr (F32) {
-                    st_32(dst, x);
+                    st_32(dst, reinterpret_cast<const uint32_t *>(x));
                 } else if constexpr (E4M3) {
                     *reinterpret_cast<uint4 *>(dst) = to_bf16(x);
                 } else {

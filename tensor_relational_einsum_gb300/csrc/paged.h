@@ -143,6 +143,7 @@ struct PgMerge {
     PgWork w[2];
     int32_t cuts[2];             // CTAs - 1; 0: none
     int32_t rows[2];
+    int32_t groups[2];           // CTAs of a cut (set by the launch)
 };
 cudaError_t launch_cache_merge(const PgAttn &p, const PgMerge &m, cudaStream_t st);
 
@@ -168,26 +169,36 @@ EA_HD bool pg_seq(int32_t a, int32_t b, int32_t len, int64_t rows, int32_t max_n
 // SUM_{i < n} floor((a i + b) / m) for a, b >= 0, m > 0 (Euclid's way: whole
 // parts of a / m and b / m are summed in closed form, then i and the value
 // change places).
-EA_HD int64_t pg_floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+template <class T>
+EA_HD int64_t pg_floor_sum_t(T n, T m, T a, T b) {
     int64_t s = 0;
     while (n > 0) {
         if (a >= m) {
-            s += n * (n - 1) / 2 * (a / m);
-            a %= m;
+            const T q = a / m;
+            s += (int64_t)n * (n - 1) / 2 * q;
+            a -= q * m;
         }
         if (b >= m) {
-            s += n * (b / m);
-            b %= m;
+            const T q = b / m;
+            s += (int64_t)n * q;
+            b -= q * m;
         }
-        const int64_t y = a * n + b;
+        const T y = a * n + b;
         if (y < m) break;
         n = y / m;
-        b = y % m;
-        const int64_t t = m;
+        b = y - n * m;
+        const T t = m;
         m = a;
         a = t;
     }
     return s;
+}
+// The values only shrink: what fits 32 bits at the start stays there, and
+// takes a GPU thread a fifth of the time.
+EA_HD int64_t pg_floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    if (n <= INT32_MAX && a * n + b <= INT32_MAX && m <= INT32_MAX)
+        return pg_floor_sum_t<uint32_t>((uint32_t)n, (uint32_t)m, (uint32_t)a, (uint32_t)b);
+    return pg_floor_sum_t<int64_t>(n, m, a, b);
 }
 
 EA_HD bool pg_served(const PgSeq &s, const PgSplit &sp) {
@@ -219,7 +230,7 @@ EA_HD int64_t pg_units_before(const PgSeq &s, const PgSplit &sp, int j) {
     if (j <= 0) return 0;
     if (!sp.causal) return (int64_t)j * pg_item_units(s, sp, 0);
     const int64_t c = (int64_t)s.len - s.n;
-    int64_t none = c < 0 ? -c / sp.tok : 0;  // items whose tokens all stand before position 0: one unit each
+    int64_t none = c < 0 ? (int64_t)((uint32_t)-c / (uint32_t)sp.tok) : 0;  // items whose tokens all stand before position 0: one unit each
     if (none > j) none = j;
     return none + pg_floor_sum(j - none, sp.kt, sp.tok, c + (none + 1) * sp.tok + sp.kt - 1);
 }
