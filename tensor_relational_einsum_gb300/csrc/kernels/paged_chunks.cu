@@ -64,6 +64,7 @@ template <bool E4M3>
 constexpr float kLazy = E4M3 ? 8.0f : 64.0f;
 constexpr int kParts = 4;         // ring of parts
 constexpr int kMaxStages = 4;
+constexpr int kWhole = 1024;      // sequences of up to so many positions are not cut
 
 // Register split (setmaxnreg): the softmax threads keep a row of 128 scores.
 // The shares add up to the launch's registers exactly.
@@ -93,7 +94,7 @@ struct Part {
 __device__ __forceinline__ Part part_of(const PgWalk &w, const PgSplit &sp) {
     Part q;
     const int np = w.part(), half = sp.tok / 2;
-    q.u0 = w.u0;
+    q.u0 = w.u0 * (sp.kt / kKeys);
     q.whole = w.u0 == 0 && np == w.units;
     q.tok0 = w.item * sp.tok;
     q.end = pg_item_end(w.s, sp, w.item);
@@ -103,12 +104,12 @@ __device__ __forceinline__ Part part_of(const PgWalk &w, const PgSplit &sp) {
     q.ntok = w.s.n - q.tok0;
     q.len = w.s.len;
     q.pos0 = w.s.len - w.s.n + q.tok0;
-    const int units = (q.end + kKeys - 1) / kKeys, u1 = w.u0 + np;
+    const int tiles = (q.end + kKeys - 1) / kKeys, u1 = q.u0 + np * (sp.kt / kKeys);
     const bool two = half < q.ntok;
     // keys of tile 0: up to its own last token's
     const int e0 = two && sp.causal ? max(0, q.pos0 + half) : q.end;
-    q.n[0] = max(0, min(u1, (e0 + kKeys - 1) / kKeys) - w.u0);
-    q.n[1] = two ? max(0, min(u1, units) - w.u0) : 0;
+    q.n[0] = max(0, min(u1, (e0 + kKeys - 1) / kKeys) - q.u0);
+    q.n[1] = two ? max(0, min(u1, tiles) - q.u0) : 0;
     q.tiles = max(q.n[0], q.n[1]);
     return q;
 }
@@ -827,15 +828,18 @@ PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causa
     sp.heads = c.heads;
     sp.group = group;
     sp.tok = 2 * tpt;
-    sp.kt = kKeys;
+    // Short sequences are not cut: the tiles of an item cost less than the merge (2 x 64 tokens in 600 positions, 32 heads
+    // over 8: 26.2 us cut, 21.5 us whole).
+    const bool whole = t.cap <= kWhole;
+    sp.kt = whole ? kWhole : kKeys;
     sp.causal = causal;
     sp.min_rows = min_rows;
     sp.max_rows = INT32_MAX;
     pl.rows = sp.tok * group;
     const int64_t items = std::min<int64_t>((int64_t)t.n_seqs * ((t.max_new + sp.tok - 1) / sp.tok), t.rows / sp.tok + t.n_seqs);
-    const int64_t units = ((((int64_t)t.max_pages << c.page_log2) + kKeys - 1) / kKeys) * items * c.heads;
+    const int64_t units = (t.cap + sp.kt - 1) / sp.kt * items * c.heads;
     pl.ctas = (int)std::min<int64_t>(units, num_sms);
-    pl.bytes = pg_work_bytes(pl.ctas, pl.rows, c.dim);
+    pl.bytes = whole ? 0 : pg_work_bytes(pl.ctas, pl.rows, c.dim);
     return pl;
 }
 

@@ -224,7 +224,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     ld.keys = keys;
     ld.off = off;
     ld.enter(p, sp);
-#pragma unroll
+#pragma unroll 1  // one copy of the code: small calls wait for their instructions
     for (int s = 0; s < C::S - 1; s++) {
         ld.issue(p, sp, base + s * C::STAGE, base + C::S * C::STAGE + s * C::SCALES, warp, lane);
         cp_commit();
@@ -668,7 +668,7 @@ PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causa
     sp.min_rows = 1;
     sp.max_rows = pl.rows;
     // Short sequences are not cut: another block adds less than the merge's launch.
-    const int64_t longest = (int64_t)t.max_pages << c.page_log2;
+    const int64_t longest = t.cap;
     sp.kt = longest <= 512 ? 512 : c.fmt == EA_CACHE_E4M3 || c.dim == 64 ? 128 : 64;  // a block
     const int64_t units = (longest + sp.kt - 1) / sp.kt * t.n_seqs * c.heads;
     // Many short sequences: a warp an item, without barriers or a merge between warps.
