@@ -10,6 +10,7 @@
 // one row and eight parts at a time, and rows that leave warps idle are shared.
 #include <algorithm>
 
+#include "attn_common.cuh"
 #include "paged_common.cuh"
 
 namespace ea {
@@ -51,6 +52,51 @@ __device__ __forceinline__ void finish(const PgAttn &p, const PgCut &c, int row,
     }
 }
 
+// An item of N parts: a warp two rows at a time, all parts at once.  The first
+// row of part 0 is n0, that of part i n1 + (i - 1) step.
+template <int D, int N>
+__device__ __forceinline__ void merge_few(const PgAttn &p, const PgWork &w, const PgCut &c, int64_t n0, int64_t n1, int64_t step,
+                                          int row, int r1, int lane) {
+    constexpr int C = D / 32;
+    const float2 *ml_at[N];
+    const float *acc_at[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int64_t n = i == 0 ? n0 : n1 + (i - 1) * step;
+        ml_at[i] = w.ml + n;
+        acc_at[i] = w.acc + n * D;
+    }
+    for (; row < r1; row += 2 * kWarps) {
+        float2 ml[2][N];
+        float v[2][N][C];
+#pragma unroll
+        for (int y = 0; y < 2; y++) {
+            const int r = min(row + y, r1 - 1);  // a single last row twice: its second result is not stored
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                ml[y][i] = __ldcg(ml_at[i] + r);
+                load_acc<D>(acc_at[i] + r * D, lane, v[y][i]);
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; y++) {
+            float m = ml[y][0].x;
+#pragma unroll
+            for (int i = 1; i < N; i++) m = fmaxf(m, ml[y][i].x);
+            const float base = m == -INFINITY ? 0.f : m;
+            float l = 0.f, a[C] = {};
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const float f = attn::ex2((ml[y][i].x - base) * p.scale_log2);
+                l = fmaf(f, ml[y][i].y, l);
+#pragma unroll
+                for (int k = 0; k < C; k++) a[k] = fmaf(f, v[y][i][k], a[k]);
+            }
+            if (row + y < r1) finish<D>(p, c, row + y, lane, m, l, a);
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(32 * kWarps, 4)
 cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgMerge mg) {
@@ -77,40 +123,10 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
     auto at = [&](int i, int row) { return (int64_t)(i == 0 ? slot0 : 2 * (x - 1 + i)) * rows + row; };
 
     if (count <= 4) {
-        // a warp a row, two rows at a time, all parts at once
-        for (int row = r0 + 2 * warp; row < r1; row += 2 * kWarps) {
-            float2 ml[2][4];
-            float v[2][4][C];
-#pragma unroll
-            for (int y = 0; y < 2; y++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    ml[y][i] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-                    for (int k = 0; k < C; k++) v[y][i][k] = 0.f;
-                    if (i < count && row + y < r1) {
-                        const int64_t a = at(i, row + y);
-                        ml[y][i] = __ldcg(&w.ml[a]);
-                        load_acc<D>(w.acc + a * D, lane, v[y][i]);
-                    }
-                }
-#pragma unroll
-            for (int y = 0; y < 2; y++) {
-                if (row + y >= r1) break;
-                const float m = fmaxf(fmaxf(ml[y][0].x, ml[y][1].x), fmaxf(ml[y][2].x, ml[y][3].x));
-                const float base = m == -INFINITY ? 0.f : m;
-                float l = 0.f, a[C] = {};
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    if (i >= count) break;
-                    const float f = exp2f((ml[y][i].x - base) * p.scale_log2);
-                    l = fmaf(f, ml[y][i].y, l);
-#pragma unroll
-                    for (int k = 0; k < C; k++) a[k] = fmaf(f, v[y][i][k], a[k]);
-                }
-                finish<D>(p, c, row + y, lane, m, l, a);
-            }
-        }
+        const int64_t n0 = (int64_t)slot0 * rows, n1 = (int64_t)2 * x * rows, step = (int64_t)2 * rows;
+        if (count == 2) merge_few<D, 2>(p, w, c, n0, n1, step, r0 + 2 * warp, r1, lane);
+        else if (count == 3) merge_few<D, 3>(p, w, c, n0, n1, step, r0 + 2 * warp, r1, lane);
+        else merge_few<D, 4>(p, w, c, n0, n1, step, r0 + 2 * warp, r1, lane);
         return;
     }
     // many parts, eight at a time; with few rows several warps share a row's parts
@@ -140,7 +156,7 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
             }
 #pragma unroll
             for (int y = 0; y < 8; y++) {
-                const float f = exp2f((ml[y].x - base) * p.scale_log2);
+                const float f = attn::ex2((ml[y].x - base) * p.scale_log2);
                 l = fmaf(f, ml[y].y, l);
 #pragma unroll
                 for (int k = 0; k < C; k++) a[k] = fmaf(f, v[y][k], a[k]);
