@@ -478,13 +478,22 @@ ea_status ea_cache_attention_workspace(ea_cache cache, const ea_page_batch *batc
  *   t <= p (a causal row with p < 0, and any row with lens[i] = 0, keeps no
  *   key: O = 0, m = -inf, l = 0).  Without causal n_i may exceed lens[i].
  * Cells at and beyond lens[i] and unlisted pages never reach a result,
- * whatever they hold.  A kept position's infinity or NaN reaches every row
- * of its sequence that shares a tile with a row that keeps it.
+ * whatever they hold.  A position that a row drops (t > p) must be finite:
+ * its infinity or NaN may reach rows of its own sequence before it.
  *   out    bf16, extents of q, not overlapping q; m_out, l_out (both or
  *          neither): f32, extents of q without the head dim.
  * Scores, statistics and sums are fp32; the probabilities enter the second
- * product as bf16.  Results do not depend on what else is in the batch by
- * more than the fp32 order of the sums.
+ * product as 16-bit values (8 significant bits over bf16 cells; 11 over 8-bit
+ * cells, or 8 where the pages are expanded first).  8-bit cells are exact
+ * where the scale of their vector is within 2^21 of the largest scale of V so
+ * far in the sequence's part (of K in the tile); smaller ones lose bits
+ * relative to that largest one.  Bit for bit the same on every run of one
+ * batch; a row's result depends on what else is in the batch by no more than
+ * the order of fp32 sums and the reference of its exponentials.
+ * How it runs: sequences with few rows (n_i * g <= 16, or <= 32 when max_new
+ * allows that many) and the others are served by kernels of their own, each
+ * sharing its work out evenly over the GPU whatever the lengths are; a merge
+ * follows where items were cut.
  * Errors: as ea_cache_append; EA_ERR_ARG for a missing or small workspace. */
 ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *batch, ea_relation q, const ea_cache_attn_opts *opts,
                              void *stream, ea_relation out);

@@ -12,6 +12,8 @@ All arithmetic runs in libea.so.
                       the key tiles of a query tile aggregated with the
                       merge of (max, sum of exp, weighted sum) triples in one
                       tcgen05 kernel.
+* ``CachedAttention`` the same for generation: new rows of K and V appended to
+                      a paged cache, the new rows of Q attending to it.
 * ``SwigluFFN``       gate/up contractions (SUM over model-dim blocks),
                       SiLU(gate) * up elementwise join, down contraction.
 * ``MatrixChain``     the pages' matrix-chain workloads (chains A-E): a
@@ -34,6 +36,7 @@ import numpy as np
 import torch
 
 from . import _abi
+from .cache import PageBatch, PagedCache, cache_append, cache_attention
 from .relation import Relation, attention, exchange, joinagg
 
 
@@ -165,6 +168,29 @@ class FusedAttention:
         c = rec.call if rec is not None else _direct
         c("attn.fused", lambda: attention(self.spec, self.Q, self.K, self.V, scale=self.scale, causal=self.causal,
                                           out=self.O))
+        return self.O
+
+
+class CachedAttention:
+    """Attention of new rows over a paged cache: append K and V, then attend.
+
+    ``q`` [rows.., query heads, d], ``k`` and ``v`` [rows.., heads, d] (bf16)
+    are the relations that the projections fill on every step; ``batch`` names
+    the rows' sequences.  Its tensors may change between runs, which is how one
+    captured graph serves every step: lengths grow in place, pages are added to
+    the table."""
+
+    def __init__(self, q: Relation, k: Relation, v: Relation, cache: PagedCache, batch: PageBatch, scale: float = 0.0,
+                 causal: bool = True):
+        self.q, self.k, self.v, self.cache, self.batch = q, k, v, cache, batch
+        self.scale, self.causal = scale, causal
+        self.O = Relation("bf16", q.dims, q.bounds, device=q.storage.device)
+
+    def run(self, rec: Recorder | None = None):
+        c = rec.call if rec is not None else _direct
+        c("cache.append", lambda: cache_append(self.cache, self.batch, self.k, self.v))
+        c("attn.cached", lambda: cache_attention(self.q, self.cache, self.batch, scale=self.scale, causal=self.causal,
+                                                 out=self.O))
         return self.O
 
 

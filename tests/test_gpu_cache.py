@@ -746,3 +746,107 @@ def test_large_pool_offsets():
         for rows, pos in ((slice(0, n), np.arange(n)), (slice(n, n + 1), np.arange(1))):
             wo, _, _, big, slack = cu.softmax_attention(q[rows, h], x[0][rows, h], x[1][rows, h], pos, sc, True)
             assert (np.abs(out[rows, h] - wo) <= cu.out_bound(wo, big, slack, n)).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_cached_attention_as_one_captured_graph(fmt):
+    """The step of a generation loop -- append and attend -- captured once and replayed while lengths grow and a page is
+    added; an eager pass of other calls lives at the same time."""
+    from tensor_relational_einsum_gb300 import PageBatch, PagedCache
+    from tensor_relational_einsum_gb300.graphs import CachedAttention, capture
+    from tensor_relational_einsum_gb300.relation import check
+    kv, group, d, page, seqs = 2, 4, 64, 16, 3
+    rng = np.random.default_rng(25)
+    c = PagedCache(32, page, kv, d, fmt)
+    table = torch.full((seqs, 4), -1, dtype=torch.int32, device="cuda")
+    table[:, :2] = torch.from_numpy(rng.permutation(32)[:6].reshape(3, 2).astype(np.int32))
+    starts, lens = torch.arange(seqs + 1, dtype=torch.int32, device="cuda"), torch.tensor([1, 29, 7], dtype=torch.int32, device="cuda")
+    batch = PageBatch(table, starts, lens, max_new=1)
+    q, k, v = (torch.zeros(seqs, h, d, dtype=torch.bfloat16, device="cuda") for h in (kv * group, kv, kv))
+    step = CachedAttention(relation(q), relation(k), relation(v), c, batch)
+    old = lens.cpu().numpy()
+    held = [[values(rng, (int(t) - 1, kv, d)) for _ in range(2)] for t in old]
+    from tensor_relational_einsum_gb300 import cache_append
+    for i, t in enumerate(old):       # what was there before
+        if t > 1:
+            b = PageBatch(table[i:i + 1], torch.tensor([0, t - 1], dtype=torch.int32, device="cuda"),
+                          torch.tensor([t - 1], dtype=torch.int32, device="cuda"))
+            cache_append(c, b, *(relation(torch.from_numpy(x).to(torch.bfloat16).cuda()) for x in held[i]))
+        if fmt == "e4m3":
+            for w in range(2):
+                e = np.exp2(cu.e4m3_scale(held[i][w]))[..., None]
+                held[i][w] = cu.e4m3_round(held[i][w] / e) * e
+    graph = capture(step.run)
+    for n in range(6):
+        x = [values(rng, (seqs, h, d)) for h in (kv * group, kv, kv)]
+        for t, y in zip((q, k, v), x):
+            t.copy_(torch.from_numpy(y).to(torch.bfloat16))
+        if n == 4:
+            table[1, 2] = 31 if 31 not in table.cpu().tolist()[0] + table.cpu().tolist()[1] + table.cpu().tolist()[2] else 30
+        if fmt == "e4m3":
+            for w in (1, 2):
+                e = np.exp2(cu.e4m3_scale(x[w]))[..., None]
+                x[w] = cu.e4m3_round(x[w] / e) * e
+        graph.replay()
+        check()
+        got = step.O.to_dense().double().cpu().numpy()
+        for i in range(seqs):
+            held[i] = [np.concatenate([held[i][w], x[w + 1][i:i + 1]]) for w in range(2)]
+            t = len(held[i][0])
+            assert t == int(lens[i])
+            for h in range(kv * group):
+                wo, _, _, big, slack = cu.softmax_attention(x[0][i:i + 1, h], held[i][0][:, h // group], held[i][1][:, h // group],
+                                                            np.array([t - 1]), 0.125, True)
+                assert (np.abs(got[i, h] - wo[0]) <= cu.out_bound(wo, big, slack, t)[0]).all()
+        lens += 1
+        if n == 2:                    # other calls between replays
+            cache_append(c, PageBatch(table[:1, :2], torch.tensor([0, 0], dtype=torch.int32, device="cuda"),
+                                      torch.tensor([1], dtype=torch.int32, device="cuda")), step.k, step.v)
+
+
+def test_empty_relations_and_batches():
+    """No rows at all, and a batch whose sequences have none: nothing is written, nothing is raised."""
+    from tensor_relational_einsum_gb300 import PageBatch, PagedCache, Relation, cache_append, cache_attention, cache_read
+    from tensor_relational_einsum_gb300.relation import check
+    c = PagedCache(4, 16, 2, 64)
+    z = torch.zeros(2, dtype=torch.int32, device="cuda")
+    b = PageBatch(torch.full((1, 1), -1, dtype=torch.int32, device="cuda"), z, z[:1])
+    for rows in (0, 5):
+        k, v, q = (Relation("bf16", (rows, h, 64), [1, 1, 1], device="cuda") for h in (2, 2, 4))
+        k.storage.zero_(), v.storage.zero_(), q.storage.zero_()
+        out = Relation("bf16", (rows, 4, 64), [1, 1, 1], device="cuda")
+        out.storage.fill_(MARK)
+        cache_append(c, b, k, v)
+        cache_read(c, b, k, v)
+        cache_attention(q, c, b, out=out)
+        check()
+        assert (out.storage == MARK).all() and not c.k.any()
+
+
+def test_python_refusals():
+    from tensor_relational_einsum_gb300 import PageBatch, PagedCache, cache_append, cache_read
+    i32 = dict(dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        PagedCache(4, 16, 2, 64, "fp8")
+    with pytest.raises(ValueError):
+        PagedCache(4, 16, 2, 64, k=torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda"))
+    x = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        PagedCache(4, 16, 2, 64, k=x, v=x.float())
+    with pytest.raises(ValueError):
+        PagedCache(4, 16, 2, 64, k=x, v=x.transpose(0, 1).contiguous().transpose(0, 1))
+    c = PagedCache(4, 16, 2, 64)
+    good = (torch.zeros(2, 3, **i32), torch.zeros(3, **i32), torch.zeros(2, **i32))
+    PageBatch(*good)
+    for spoil in range(3):
+        for bad in (good[spoil].long(), good[spoil].cpu(), good[spoil][:1] if spoil else good[0].t()):
+            args = list(good)
+            args[spoil] = bad
+            with pytest.raises(ValueError):
+                PageBatch(*args)
+    b = PageBatch(*good)
+    with pytest.raises(ValueError):
+        cache_read(c, b)
+    k = relation(torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        cache_read(c, b, k=k)
