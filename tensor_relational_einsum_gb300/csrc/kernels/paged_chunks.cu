@@ -13,14 +13,27 @@
 // Key tiles come page by page.  bf16 pages are copied by TMA straight into
 // the swizzled operand tiles (a box of up to 128 positions x 64 columns: a
 // page is contiguous for a head, so a page is one box per 64 columns).
-// 8-bit pages are copied with bulk copies into raw tiles and rewritten as f16 operands by a warpgroup of their own: a conversion and
-// a product for two codes (twice as many integer instructions lead to bf16).
-// f16's range is kept by powers of two, so that the operands are exact: K's
-// vectors are brought to the largest scale of their tile, V's to the largest
-// of the part so far (exact down to 2^-21 of it), Q's rows to [2^14, 2^15),
-// the probabilities to 2^7.  All of these are one number a tile or a row to
-// the softmax.  (Scales left to the softmax, a number a key, cost it 64
-// broadcast reads of shared memory a row and tile: 6200 cycles a tile.)
+// 8-bit pages are copied with bulk copies into raw tiles and rewritten as f16
+// operands by a warpgroup of their own: a conversion and a product for two
+// codes (twice as many integer instructions lead to bf16).  f16's range is
+// kept by powers of two, so that the operands are exact: K's vectors are
+// brought to the largest scale of their tile, V's to the largest of the part
+// so far (exact down to 2^-21 of it), Q's rows to [2^14, 2^15), the
+// probabilities to 2^7.  All of these are one number a tile or a row to the
+// softmax.  (Scales left to the softmax, a number a key, cost it 64 broadcast
+// reads of shared memory a row and tile: 6200 cycles a tile at head dim 64,
+// which takes 3800 this way.)  From 256 rows of a sequence on the pages are
+// expanded to bf16 first (paged_expand.cu), and this kernel reads those.
+//
+// What bounds it: shared memory.  The products of 256 rows with a key tile
+// take 2048 cycles of the tensor pipe at head dim 128 and read 192 KB of
+// operands, to which the copies add 64 KB: 2000 cycles at 128 bytes a cycle.
+// They get in each other's way: a tile takes 3080 cycles, 2820 with the
+// softmax left out, which itself takes 1220 behind each product.  2048 tokens
+// after 14336, 32 heads over 8: 386 us, 1330 TFLOP/s, 0.70 of the measured
+// bf16 rate.  At head dim 64 the softmax is as long as the products (312 us
+// there, 0.43).  Short items pay for a part's ends, about 5000 cycles: prompts
+// of 2048 tokens with 32 heads of their own, 0.39.
 //
 // Keys at and beyond the sequence's end lie in the last tile only.  Their
 // scores are dropped by position whatever they are; the second product stops
@@ -34,8 +47,8 @@
 //              scores; A is rescaled in TMEM when the reference maximum moves
 //              by more than 2^64 (fp32 and bf16 have the same 8 exponent
 //              bits, so P, l and A stay in range and their relative rounding
-//              is the same at any magnitude; 2^8 with f16); at the part's end A / l to the
-//              output, or (m, l, A) to the workspace.
+//              is the same at any magnitude; 2^8 with f16); at the part's end
+//              A / l to the output, or (m, l, A) to the workspace.
 //   warp 8     copies: Q tiles; K and V pages (or the raw tiles).
 //   warp 9     TMEM and MMA issue: per key tile and X, A_X (+)= P_X V, then
 //              S_X = Q_X K^T of the next key tile, so that one tile's products
@@ -120,6 +133,7 @@ struct Ctl {
     uint64_t raw_full[2][2], raw_empty[2][2];  // of K, of V
     uint64_t s_full[2], p_full[2], o_fin[2];
     uint64_t part_full[kParts], part_empty[kParts];
+    uint64_t top_full[2];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
@@ -225,6 +239,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             mbar_init(&ctl->part_full[b], 1);
             mbar_init(&ctl->part_empty[b], E4M3 ? 14 : 10);  // the warps that read parts
         }
+        for (int b = 0; b < 2; b++) mbar_init(&ctl->top_full[b], 4);
         mbar_init(&ctl->mma_done, 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -732,8 +747,14 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         const bool in = row0 + lane < nv;
                         const uint32_t tk = __reduce_max_sync(0xffffffffu, in && kb != 255u ? kb : 0u);
                         const uint32_t tv = __reduce_max_sync(0xffffffffu, in && vb != 255u ? vb : 0u);
-                        if (lane == 0) ctl->top[ct & 1][warp - 12] = make_int2((int)tk, (int)tv);
-                        named_bar(1, 128);
+                        if (lane == 0) {
+                            ctl->top[ct & 1][warp - 12] = make_int2((int)tk, (int)tv);
+                            mbar_arrive(&ctl->top_full[ct & 1]);
+                        }
+                        if (!warp_wait(&ctl->top_full[ct & 1], (ct >> 1) & 1, abort, p.err, kDevTimeoutProducer)) {
+                            ok = false;
+                            break;
+                        }
                         int kref = 0;
                         if (j == 0) vref = 0;
 #pragma unroll

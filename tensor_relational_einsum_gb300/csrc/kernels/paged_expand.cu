@@ -4,12 +4,13 @@
 //
 // The chunk kernel can rewrite 8-bit tiles itself, but does so once for every
 // 256 rows, next to products that take all of shared memory's bandwidth: a
-// tile then takes 6000 cycles instead of 3800.  Writing 2 bytes and reading
+// tile then takes 6000 cycles instead of 3080.  Writing 2 bytes and reading
 // them from L2 once for 256 rows is cheaper from about that many rows on
-// (2048 tokens after 14336, 32 heads over 8: 620 us there, 410 us here with
-// this kernel; 32 tokens after 8160 in 8 sequences: 120 us there, 160 here).
-// Every cell is a bf16 value, so nothing is lost.  Bound by HBM: one byte read
-// and two written a cell.
+// (2048 tokens after 14336, 32 heads over 8: 620 us there, 405 us with this
+// kernel; with 32 tokens after 8160 in 8 sequences, 128 rows, the 8-bit cells
+// alone are 20 us of HBM time: 120 us there, and 3 bytes more a cell here).
+// Every cell is a bf16 value, so nothing is lost.  Bound by HBM and L2: one
+// byte read and two written a cell, 21 us for 31.6 million of them.
 #include "paged_common.cuh"
 
 namespace ea {

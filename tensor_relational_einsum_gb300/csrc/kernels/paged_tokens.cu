@@ -33,6 +33,12 @@
 //     vref the largest that the warp has met: 11 bits down to 2^-21 of the
 //     row's largest term, steps of 2^-31 of it below that.
 // Powers of two cost nothing in exactness: the f16 products are exact in fp32.
+//
+// Measured: 64 sequences of 8192 positions, 32 heads over 8 of 128: bf16 323
+// us, 6.6 TB/s (0.98 of the measured copy rate); 8-bit 188 us, 5.7 TB/s (0.85;
+// 36% of issue slots, the integer pipe at a third); head dim 64 bf16 0.93,
+// 8-bit 0.56, where a block's fixed work weighs twice.  A small call takes 6.5
+// us: a chain of reads (bounds, pages, cells), one block and the code itself.
 #include "attn_common.cuh"
 #include "paged_sched.cuh"
 
