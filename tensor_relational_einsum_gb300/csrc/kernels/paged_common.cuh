@@ -53,10 +53,17 @@ __device__ __forceinline__ int32_t check_page(int32_t g, int64_t n_pages, int *e
 }
 
 // 32 bytes at once: as two stores of 16 each of them fills half a sector.
+// Relations are aligned to 16 bytes only; off a 32-byte boundary it is two
+// stores after all.
 __device__ __forceinline__ void st_32(void *dst, const uint32_t *x) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                 : "memory");
+    if (((uintptr_t)dst & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                     "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
 }
 
 // The value of a scale byte: 2^(b - 127), NaN for 255.

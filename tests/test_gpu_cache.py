@@ -850,3 +850,49 @@ def test_python_refusals():
     k = relation(torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError):
         cache_read(c, b, k=k)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_relations_off_a_32_byte_boundary(fmt, dtype):
+    """Relations promise 16 bytes: inputs, outputs and the workspace at odd multiples of it, through every kernel."""
+    import ctypes
+    from tensor_relational_einsum_gb300 import _abi, cache_append, cache_read
+    from tensor_relational_einsum_gb300.relation import check
+
+    def off(t):
+        flat = torch.empty(t.numel() + 16, dtype=t.dtype, device="cuda")
+        flat = flat[16 // t.element_size():][:t.numel()]
+        assert flat.data_ptr() % 32 == 16
+        flat.copy_(t.reshape(-1))
+        return flat.view(t.shape)
+
+    seqs = [(1, 3000), (300, 1200), (40, 40), (2, 9)]
+    b = cu.Batch(seqs, 32)
+    rng = np.random.default_rng(26)
+    for dim in (64, 128):
+        c = nan_cache(b, 2, dim, fmt)
+        held = fill(c, b, rng)
+        batch = on_gpu(b)
+        outs = [off(torch.full((b.rows, 2, dim), MARK, dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda"))
+                for _ in range(2)]
+        rel_kv = [relation(t) for t in outs]
+        cache_read(c, batch, *rel_kv)
+        check()
+        for w in range(2):
+            want = np.concatenate([held[i][w][-n:] for i, (n, _) in enumerate(seqs)])
+            assert np.array_equal(outs[w].double().cpu().numpy(), want)
+        cache_append(c, batch, *rel_kv)                     # what was read: nothing changes
+        q = values(rng, (b.rows, 4, dim))
+        tq = off(torch.from_numpy(q).to(torch.bfloat16).cuda())
+        out = off(torch.full((b.rows, 4, dim), MARK, dtype=torch.bfloat16, device="cuda"))
+        rq, ro = relation(tq), relation(out)
+        need = ctypes.c_size_t()
+        L = _abi.lib()
+        _abi.check_status(L.ea_cache_attention_workspace(c.handle, batch.ref, rq.handle, ctypes.byref(need)))
+        ws = off(torch.empty(need.value, dtype=torch.uint8, device="cuda"))
+        opts = _abi.CacheAttnOpts(0.0, 1, None, None, ws.data_ptr(), need.value)
+        _abi.check_status(L.ea_cache_attention(c.handle, batch.ref, rq.handle, ctypes.byref(opts),
+                                               ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), ro.handle))
+        check()
+        verify(b, c, held, 2, q, out.double().cpu().numpy(), None, None, True, 0.0, False, np.ones(b.rows, dtype=bool))
