@@ -249,7 +249,8 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     tc_fence_before();
     let_next_start();
     take_shares<R::THREADS>(p.t, sp, p.err, ctl->scan, 1, &ctl->share);
-    wait_for_previous();  // expanded pages
+    wait_for_previous();  // expanded pages, read through the async proxy
+    asm volatile("fence.proxy.async;" ::: "memory");
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
