@@ -83,7 +83,8 @@ class PageBatch:
     its position p is in slot p % page of page ``pages[i, p // page]``.
 
     int32 CUDA tensors: ``pages`` [sequences, most pages] (rows may be
-    strided), ``starts`` [sequences + 1], ``lens`` [sequences].  ``max_new``:
+    strided), ``starts`` [sequences + 1], ``lens`` [sequences].  They are kept;
+    write into them for the next step.  ``max_new``:
     an upper bound of starts[i + 1] - starts[i], if known (it spares the
     attention the kernel for longer chunks); 0: the dense rows."""
 
@@ -170,7 +171,7 @@ def cache_attention(q: Relation, cache: PagedCache, batch: PageBatch, scale: flo
     call's stream, one per call."""
     _same_device(cache, batch, q, out, m_out, l_out)
     L = lib()
-    shape = (cache.pages, cache.page, cache.heads, cache.dim, q.dims)
+    shape = (cache.format, cache.pages, cache.page, cache.heads, cache.dim, q.dims)
     need = batch._workspace.get(shape)
     if need is None:
         n = ctypes.c_size_t()

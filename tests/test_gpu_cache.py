@@ -896,3 +896,20 @@ def test_relations_off_a_32_byte_boundary(fmt, dtype):
                                                ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), ro.handle))
         check()
         verify(b, c, held, 2, q, out.double().cpu().numpy(), None, None, True, 0.0, False, np.ones(b.rows, dtype=bool))
+
+
+def test_one_batch_over_two_caches():
+    """The same batch object with a bf16 and an 8-bit cache of the same shape, whose workspaces differ."""
+    b = cu.Batch([(300, 2000), (1, 700)], 16)
+    rng = np.random.default_rng(27)
+    from tensor_relational_einsum_gb300 import cache_attention
+    from tensor_relational_einsum_gb300.relation import check
+    batch = on_gpu(b)
+    q = values(rng, (b.rows, 2, 64))
+    r = relation(torch.from_numpy(q).to(torch.bfloat16).cuda())
+    for fmt in ("bf16", "e4m3", "bf16"):
+        c = nan_cache(b, 1, 64, fmt)
+        held = fill(c, b, rng)
+        out = cache_attention(r, c, batch).to_dense().double().cpu().numpy()
+        check()
+        verify(b, c, held, 2, q, out, None, None, True, 0.0, False, np.ones(b.rows, dtype=bool))
