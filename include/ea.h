@@ -393,8 +393,8 @@ ea_status ea_attention_run(const char *spec, ea_relation q, ea_relation k, ea_re
  *                  before the rounding and the product after it exact, so a
  *                  code's rounding (2^-4 relative, 2^-10 * 2^(b - 127) where
  *                  the code is subnormal) is the only one, and every cell is
- *                  a bf16 value.  ea_cache_append writes no NaN code; a cache
- *                  filled by other means must hold none either. */
+ *                  a bf16 value.  ea_cache_append writes no NaN code; one that
+ *                  was put there by other means reads as NaN. */
 typedef struct ea_cache_s *ea_cache; /* opaque handle */
 
 typedef enum { EA_CACHE_BF16 = 0, EA_CACHE_E4M3 = 1 } ea_cache_format;

@@ -913,3 +913,53 @@ def test_one_batch_over_two_caches():
         out = cache_attention(r, c, batch).to_dense().double().cpu().numpy()
         check()
         verify(b, c, held, 2, q, out, None, None, True, 0.0, False, np.ones(b.rows, dtype=bool))
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("n,max_new", [(1, 1), (10, 10), (40, 40), (200, 200)])
+def test_a_nan_code_reads_as_nan(n, max_new, which):
+    """A NaN code under a finite scale: NaN in a read, and in every row that keeps it, in each kernel."""
+    from tensor_relational_einsum_gb300 import cache_attention, cache_read
+    from tensor_relational_einsum_gb300.relation import check
+    b = cu.Batch([(n, 400), (n, 450)], 16)
+    rng = np.random.default_rng(28)
+    c = nan_cache(b, 1, 64, "e4m3")
+    held = fill(c, b, rng)
+    getattr(c, which).view(torch.uint8)[int(b.pages[0, 3]), 0, 5, 7] = 0x7f      # position 53, component 7
+    q = torch.from_numpy(values(rng, (b.rows, 2, 64))).to(torch.bfloat16).cuda()
+    out = torch.zeros_like(q)
+    cache_attention(relation(q), c, on_gpu(b, max_new=max_new), out=relation(out))
+    check()
+    out = out.double().cpu().numpy()
+    assert 400 - n > 53
+    assert np.isnan(out[:n, :, 7]).all() and (which == "v" or np.isnan(out[:n]).all())
+    qd = q.double().cpu().numpy()
+    for h in range(2):
+        k, v = (x[:, 0] for x in held[1])
+        wo, _, _, big, slack = cu.softmax_attention(qd[n:, h], k, v, 450 - n + np.arange(n), 0.125, True)
+        assert (np.abs(out[n:, h] - wo) <= cu.out_bound(wo, big, slack, 450)).all()
+    whole = cu.Batch([(400, 400), (450, 450)], 16)
+    whole.pages = b.pages
+    kv = [torch.zeros(850, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cache_read(c, on_gpu(whole), *(relation(t) for t in kv))
+    check()
+    for w, t in zip("kv", kv):
+        g = torch.isnan(t)
+        assert int(g.sum()) == (1 if w == which else 0) and (w != which or bool(g[53, 0, 7]))
+
+
+def test_slots_that_rows_share_spare_the_others():
+    """Two rows of one append that name one slot: only that slot is unspecified."""
+    from tensor_relational_einsum_gb300 import cache_append
+    from tensor_relational_einsum_gb300.relation import check
+    b = cu.Batch([(4, 20), (4, 20)], 16)
+    b.pages[1, 1] = b.pages[0, 1]                           # positions 16..19 of both
+    c = nan_cache(b, 1, 64, "bf16")
+    before = bits(c.k).copy()
+    x = torch.ones(8, 1, 64, dtype=torch.bfloat16, device="cuda")
+    cache_append(c, on_gpu(b), relation(x), relation(x.clone()))
+    check()
+    changed = (bits(c.k) != before).any(axis=(1, 3))
+    allowed = np.zeros_like(changed)
+    allowed[b.pages[0, 1], :4] = True
+    assert np.array_equal(changed, allowed)
