@@ -460,7 +460,7 @@ typedef struct {
     int32_t causal;          /* nonzero: a query at position p keeps only positions <= p        */
     ea_relation m_out;       /* optional f32 relation: row maximum of the scaled scores         */
     ea_relation l_out;       /* optional f32 relation: row sum of exp(score - maximum)          */
-    void *workspace;         /* device memory, 16-byte aligned; its content means nothing       */
+    void *workspace;         /* device memory, 16-byte aligned, apart from operands and cache   */
     size_t workspace_bytes;  /* at least what ea_cache_attention_workspace says                 */
     int64_t reserved[4];
 } ea_cache_attn_opts;

@@ -68,11 +68,13 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     return a && b && na && nb && (const char *)a < (const char *)b + nb && (const char *)b < (const char *)a + na;
 }
 
-bool in_cache(const ea_cache_s *c, const ea_relation_s *r) {
+bool in_cache(const ea_cache_s *c, const void *p, size_t bytes) {
     const size_t n = cache_bytes(c), ns = (size_t)c->n_pages * c->heads * c->page;
-    return overlap(c->k, n, r->arena, r->bytes) || overlap(c->v, n, r->arena, r->bytes) ||
-           overlap(c->ks, c->ks ? ns : 0, r->arena, r->bytes) || overlap(c->vs, c->vs ? ns : 0, r->arena, r->bytes);
+    return overlap(c->k, n, p, bytes) || overlap(c->v, n, p, bytes) || overlap(c->ks, c->ks ? ns : 0, p, bytes) ||
+           overlap(c->vs, c->vs ? ns : 0, p, bytes);
 }
+
+bool in_cache(const ea_cache_s *c, const ea_relation_s *r) { return in_cache(c, r->arena, r->bytes); }
 
 ea_status here(const ea_cache_s *c, DevCtx **ctx) {
     ea_status s = get_ctx(ctx);
@@ -356,6 +358,11 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
         const AttnPlans a = plans_of(cache, batch, rows, heads, p.causal);
         if (a.bytes > 0 && (!o.workspace || o.workspace_bytes < a.bytes || ((uintptr_t)o.workspace & 15) != 0))
             return set_error(EA_ERR_ARG, "ea_cache_attention: workspace of %zu bytes, 16-byte aligned, needed", a.bytes);
+        if (a.bytes > 0) {
+            bool bad = in_cache(cache, o.workspace, a.bytes) || overlap(o.workspace, a.bytes, q->arena, q->bytes);
+            for (const ea_relation_s *r : outs) bad |= r && overlap(o.workspace, a.bytes, r->arena, r->bytes);
+            if (bad) return set_error(EA_ERR_ARG, "ea_cache_attention: the workspace overlaps an operand or the cache");
+        }
         // (expansion,) chunks, tokens, merge: the tokens' CTAs fill the SMs that the chunks' leave
         char *ws = (char *)o.workspace;
         const PgWork wc = pg_work(a.chunks, ws), wt = pg_work(a.tokens, ws + a.chunks.bytes);

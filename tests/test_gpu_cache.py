@@ -963,3 +963,34 @@ def test_slots_that_rows_share_spare_the_others():
     allowed = np.zeros_like(changed)
     allowed[b.pages[0, 1], :4] = True
     assert np.array_equal(changed, allowed)
+
+
+def test_a_workspace_over_an_operand_is_refused():
+    import ctypes
+    from tensor_relational_einsum_gb300 import _abi
+    b = cu.Batch([(1, 2000), (40, 900)], 16)
+    c = nan_cache(b, 1, 64, "bf16")
+    q = torch.zeros(b.rows, 2, 64, dtype=torch.bfloat16, device="cuda")
+    rq = relation(q)
+    need = ctypes.c_size_t()
+    batch = on_gpu(b)
+    L = _abi.lib()
+    _abi.check_status(L.ea_cache_attention_workspace(c.handle, batch.ref, rq.handle, ctypes.byref(need)))
+    room = torch.zeros(need.value + q.numel() * 2, dtype=torch.uint8, device="cuda")
+    over = room[need.value - 16:][:q.numel() * 2].view(torch.bfloat16).view(q.shape)    # shares the workspace's last bytes
+    beyond = room[need.value:][:q.numel() * 2].view(torch.bfloat16).view(q.shape)
+    assert over.data_ptr() % 16 == 0
+    opts = _abi.CacheAttnOpts(0.0, 1, None, None, room.data_ptr(), need.value)
+
+    def call(o, rel):
+        return L.ea_cache_attention(c.handle, batch.ref, rel.handle, ctypes.byref(o),
+                                    ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), out.handle)
+
+    out = relation(over)
+    assert call(opts, rq) == 7                              # EA_ERR_ARG
+    out = relation(torch.zeros_like(q))
+    assert call(opts, relation(over)) == 7
+    assert call(_abi.CacheAttnOpts(0.0, 1, None, None, c.v.data_ptr(), need.value), rq) == 7
+    out = relation(beyond)
+    assert call(opts, rq) == 0
+    torch.cuda.synchronize()
