@@ -66,6 +66,22 @@ __device__ __forceinline__ void st_32(void *dst, const uint32_t *x) {
     }
 }
 
+// Four e4m3 bytes as f16: bytes 0 and 1, bytes 2 and 3.
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// 2^e for -126 <= e <= 127; 0 below.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)max(e + 127, 0) << 23); }
+
 // The value of a scale byte: 2^(b - 127), NaN for 255.
 __device__ __forceinline__ float scale_value(uint32_t b) {
     return b == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(b ? b << 23 : 0x00400000u);

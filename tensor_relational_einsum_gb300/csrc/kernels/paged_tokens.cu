@@ -105,22 +105,6 @@ __device__ __forceinline__ void mma16(float *d, const uint32_t *a, uint32_t b0, 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four e4m3 bytes as f16: bytes 0 and 1, bytes 2 and 3.
-__device__ __forceinline__ void to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 l, h;\n\t"
-        "mov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-// 2^e for -126 <= e <= 127; 0 below.
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)max(e + 127, 0) << 23); }
-
 // Byte offset of 16-byte chunk c of row r in a warp's tile.  bf16, and V's
 // 8-bit cells: ldmatrix reads one chunk of 8 rows, which must lie in 8
 // different 16-byte columns of 128 bytes.  K's 8-bit cells: 8 lanes read 4

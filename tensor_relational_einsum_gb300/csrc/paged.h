@@ -122,6 +122,7 @@ inline PgWork pg_work(const PgPlan &pl, char *b) {
 constexpr int kPgTokenRows = 32;     // the most rows of a sequence (tokens x group) that it takes
 PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causal, int num_sms);
 cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, const PgWork &w, bool early, cudaStream_t st);
+
 // 8-bit pages as bf16 vectors in the workspace, in blocks of 128 positions.
 struct PgExpand {
     int32_t blocks;              // of a sequence; 0: the chunk kernel reads the 8-bit pages itself
