@@ -7,8 +7,11 @@
 // tile then takes 6000 cycles instead of 3080.  Writing 2 bytes and reading
 // them from L2 once for 256 rows is cheaper from about that many rows on
 // (2048 tokens after 14336, 32 heads over 8: 620 us there, 405 us with this
-// kernel; with 32 tokens after 8160 in 8 sequences, 128 rows, the 8-bit cells
-// alone are 20 us of HBM time: 120 us there, and 3 bytes more a cell here).
+// kernel).  Below, the 3 bytes more a cell cost more than the rewriting: 8
+// sequences of 8192, 8 heads, 48 / 128 / 240 rows: 123 / 122 / 128 us there,
+// 152 / 157 / 167 us expanded; at head dim 64 71 / 74 / 79 against 93 / 95 /
+// 104 us; of 22 shapes with 48 to 240 rows two were equal (4 sequences of
+// 2048, 128 rows: 47 us, 36 us at head dim 64), none clearly faster expanded.
 // Every cell is a bf16 value, so nothing is lost.  Bound by HBM and L2: one
 // byte read and two written a cell, 21 us for 31.6 million of them.
 #include "paged_common.cuh"
