@@ -412,8 +412,11 @@ typedef enum { EA_CACHE_BF16 = 0, EA_CACHE_E4M3 = 1 } ea_cache_format;
  * rows or more than max_new apart, or with lens negative or beyond max_pages
  * * page, or with a needed page number outside the cache is left out (its
  * rows unspecified for reads and attention, nothing written outside its own
- * rows and pages) and the device error word is raised: ea_check reports
- * EA_ERR_BOUNDS.  ea_cache_check_batch is the same check on the host. */
+ * rows and pages) and the device error word is raised, whether or not the
+ * sequence has rows: ea_check reports EA_ERR_BOUNDS.  Where starts decrease,
+ * an append or a read may leave out rows of other sequences too.  A call
+ * without dense rows launches nothing and checks nothing on the device.
+ * ea_cache_check_batch is the same check on the host. */
 typedef struct {
     const int32_t *pages;   /* [n_seqs][page_stride], the first max_pages of a row in use */
     const int32_t *starts;  /* [n_seqs + 1], nondecreasing */

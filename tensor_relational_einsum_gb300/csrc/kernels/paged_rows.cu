@@ -22,6 +22,8 @@
 // Measured, 32768 rows of 16 heads of 128, of the measured copy rate: append
 // 0.96 (bf16 to bf16), 0.90 (to 8 bits), 0.99 (fp32 to 8 bits); read 0.95,
 // 0.90, 0.92 (8 bits to fp32).  A step's append takes 4.8 us.
+#include <algorithm>
+
 #include "paged_common.cuh"
 
 namespace ea {
@@ -233,12 +235,23 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
             }
         }
     }
+    // A sequence out of range is reported whether or not a row led to it (idle ones, those beyond the rows, bounds that
+    // decrease, which the search does not expect).  A thread each, behind the copies.
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    if (blockIdx.y == 0 && i < n_seqs) {
+        PgSeq s;
+        const bool ok = staged ? pg_seq(s_starts[i], s_starts[i + 1], s_lens[i], p.t.rows, p.t.max_new, p.t.cap, &s)
+                               : pg_seq(__ldg(p.t.starts + i), __ldg(p.t.starts + i + 1), __ldg(p.t.lens + i), p.t.rows,
+                                        p.t.max_new, p.t.cap, &s);
+        if (!ok || (!READ && s.n > s.len)) batch_fail(p.err);
+    }
 }
 
 template <int D, bool F32, bool E4M3, int U>
 cudaError_t launch_u(const PgRows &p, int64_t *ctas, cudaStream_t st) {
     constexpr int hc = U * kThreads / (D / 8) / kRowsCta;
-    const dim3 grid((unsigned)((p.t.rows + kRowsCta - 1) / kRowsCta), (unsigned)((p.c.heads + hc - 1) / hc));
+    const int64_t by_rows = (p.t.rows + kRowsCta - 1) / kRowsCta, by_seqs = (p.t.n_seqs + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)std::max(by_rows, by_seqs), (unsigned)((p.c.heads + hc - 1) / hc));
     *ctas = (int64_t)grid.x * grid.y;
     if (p.read) cache_rows_kernel<D, F32, E4M3, true, U><<<grid, kThreads, 0, st>>>(p);
     else cache_rows_kernel<D, F32, E4M3, false, U><<<grid, kThreads, 0, st>>>(p);
