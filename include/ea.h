@@ -454,7 +454,8 @@ ea_status ea_cache_append(ea_cache cache, const ea_page_batch *batch, ea_relatio
 
 /* Read the batch's positions out of the pages into the rows of k and v (f32
  * or bf16 relations as in ea_cache_append, overwritten; exact for both
- * formats).  Errors: as ea_cache_append. */
+ * formats).  Rows before position 0 (n_i > lens[i]) stay as they were.
+ * Errors: as ea_cache_append. */
 ea_status ea_cache_read(ea_cache cache, const ea_page_batch *batch, ea_relation k, ea_relation v, void *stream);
 
 /* Options of ea_cache_attention; zero-initialise. */

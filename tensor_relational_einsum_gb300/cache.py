@@ -144,7 +144,8 @@ def cache_read(cache: PagedCache, batch: PageBatch, k: Relation | None = None, v
                rows: int | None = None, dtype: str = "bf16", stream=None):
     """Read the batch's positions into the rows of ``k`` and ``v`` (relations
     [rows.., heads, dim], f32 or bf16); without them, into new relations of
-    ``rows`` rows.  Rows of no sequence stay as they are.  Returns (k, v)."""
+    ``rows`` rows.  Rows of no sequence, and rows before position 0, stay as
+    they are.  Returns (k, v)."""
     if k is None and v is None:
         if rows is None:
             raise ValueError("give k and v, or the number of rows")

@@ -115,11 +115,12 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
             const bool ok = pg_seq(starts[i], starts[i + 1], staged ? s_lens[i] : __ldg(p.t.lens + i), p.t.rows, p.t.max_new,
                                    p.t.cap, &s);
             const int pos = s.len - s.n + (row - s.first);
-            if (ok && s.n <= s.len) {
+            const bool before = ok && READ && pos < 0;  // a row that no position belongs to: nothing to read
+            if (ok && pos >= 0 && (READ || s.n <= s.len)) {
                 const int32_t g = __ldg(p.t.pages + (int64_t)i * p.t.page_stride + (pos >> lg));
                 if (g >= 0 && g < p.c.n_pages) base = pg_vec(p.c, g, 0, pos & ((1 << lg) - 1));
             }
-            if (base < 0) batch_fail(p.err);
+            if (base < 0 && !before) batch_fail(p.err);
         }
         s_base[threadIdx.x] = base;
     }

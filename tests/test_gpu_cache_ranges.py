@@ -4,7 +4,8 @@ Results are exact, or within cache_util.out_bound as in test_gpu_cache."""
 import numpy as np
 import pytest
 
-from test_gpu_cache import MARK, _built, bits, relation  # noqa: F401
+import cache_util as cu
+from test_gpu_cache import MARK, _built, bits, fill, nan_cache, on_gpu, relation  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -75,3 +76,30 @@ def test_append_and_read_check_every_sequence(spoil):
     assert e.value.code == 10
     for t in outs:
         assert (t[torch.from_numpy(~mine)] == MARK).all()
+
+
+# ------------------------------------------------- reads before position 0
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_read_leaves_rows_before_position_0(fmt, dtype):
+    """A batch may hold more rows of a sequence than positions (the attention takes it, the host check accepts it): the
+    rows before position 0 stay as they were, the others are read, nothing is raised."""
+    from tensor_relational_einsum_gb300 import cache_read
+    from tensor_relational_einsum_gb300.relation import check
+    b = cu.Batch([(5, 3), (2, 0), (4, 40), (20, 17), (0, 7)], 16, behind=1)
+    c = nan_cache(b, 3, 64, fmt)
+    held = fill(c, b, np.random.default_rng(31))
+    batch = on_gpu(b)
+    batch.check(c, b.rows)
+    want = np.full((2, b.rows, 3, 64), MARK)
+    for i, (n, t) in enumerate(b.seqs):
+        k = min(n, t)
+        for w in range(2):
+            want[w, int(b.starts[i + 1]) - k:int(b.starts[i + 1])] = held[i][w][t - k:]
+    outs = [torch.full((b.rows, 3, 64), MARK, dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda")
+            for _ in range(2)]
+    cache_read(c, batch, *(relation(t) for t in outs))
+    check()
+    for t, w in zip(outs, want):
+        assert np.array_equal(t.double().cpu().numpy(), w)
