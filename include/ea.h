@@ -494,6 +494,8 @@ ea_status ea_cache_attention_workspace(ea_cache cache, const ea_page_batch *batc
  * relative to that largest one.  Bit for bit the same on every run of one
  * batch; a row's result depends on what else is in the batch by no more than
  * the order of fp32 sums and the reference of its exponentials.
+ * The sums are held up to 2^8 times what they are with the row's true maximum:
+ * a result is finite where 2^8 * lens[i] * max|V| is below 2^128.
  * How it runs: sequences with few rows (n_i * g <= 16, or <= 32 when max_new
  * allows that many) and the others are served by kernels of their own, each
  * sharing its work out evenly over the GPU whatever the lengths are; a merge

@@ -44,11 +44,11 @@
 //   warps 0-3, 4-7  softmax of tile X = 0, 1: a query row per thread (TMEM
 //              lane = row), its 128 scores in registers: mask by position,
 //              row maximum, p = 2^(c s - c m), row sum, P as 16 bits over the
-//              scores; A is rescaled in TMEM when the reference maximum moves
-//              by more than 2^64 (fp32 and bf16 have the same 8 exponent
-//              bits, so P, l and A stay in range and their relative rounding
-//              is the same at any magnitude; 2^8 with f16); at the part's end
-//              A / l to the output, or (m, l, A) to the workspace.
+//              scores; A is rescaled in TMEM when the reference maximum is
+//              exceeded by more than 2^8 (P is an f16 value then, and A at
+//              most 2^8 times what it is with the true maximum: the limit on
+//              V is that of the token kernel); at the part's end A / l to the
+//              output, or (m, l, A) to the workspace.
 //   warp 8     copies: Q tiles; K and V pages (or the raw tiles).
 //   warp 9     TMEM and MMA issue: per key tile and X, A_X (+)= P_X V, then
 //              S_X = Q_X K^T of the next key tile, so that one tile's products
@@ -73,8 +73,7 @@ constexpr int kRows = 128;        // rows of a tile (TMEM lanes)
 constexpr int kKeys = 128;        // keys of a key tile
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;   // S_0 [0, 128), S_1 [128, 256), A_0 [256, 256 + D), A_1 [256 + D, ..)
-template <bool E4M3>
-constexpr float kLazy = E4M3 ? 8.0f : 64.0f;
+constexpr float kLazy = 8.f;      // a running maximum moves when it is exceeded by this much (log2)
 constexpr int kParts = 4;         // ring of parts
 constexpr int kMaxStages = 4;
 constexpr int kWhole = 1024;      // sequences of up to so many positions are not cut
@@ -572,7 +571,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 if constexpr (E4M3) mx *= ft;
                 m_max = fmaxf(m_max, mx);
                 float alpha = 1.f;
-                if (mx != -INFINITY && (m_ref == -INFINITY || (mx - m_ref) * c > kLazy<E4M3>)) {
+                if (mx != -INFINITY && (m_ref == -INFINITY || (mx - m_ref) * c > kLazy)) {
                     alpha = m_ref == -INFINITY ? 0.f : ex2((m_ref - mx) * c);
                     m_ref = mx;
                 }

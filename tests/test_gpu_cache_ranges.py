@@ -5,10 +5,39 @@ import numpy as np
 import pytest
 
 import cache_util as cu
-from test_gpu_cache import MARK, _built, bits, fill, nan_cache, on_gpu, relation  # noqa: F401
+from test_gpu_cache import MARK, _built, attend, bits, fill, nan_cache, on_gpu, relation  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
+
+
+def put(c, b, held):
+    """Write held[i] = [k, v] (float64 [t, heads, dim]) into the cache by the definitions; held becomes what it holds."""
+    e4m3 = c.format == "e4m3"
+    cells = [x.view(torch.uint8).cpu() if e4m3 else x.cpu() for x in (c.k, c.v)]
+    scales = [x.cpu() for x in (c.k_scale, c.v_scale)] if e4m3 else None
+    for i in range(len(b.lens)):
+        pg, sl = b.places(i)
+        if len(pg) == 0:
+            continue
+        for w in range(2):
+            x = held[i][w]
+            if e4m3:
+                e = cu.e4m3_scale(x)
+                y = cu.e4m3_round(x / np.exp2(e)[..., None])
+                cells[w][pg, :, sl] = torch.from_numpy(y).to(torch.float8_e4m3fn).view(torch.uint8)
+                scales[w][pg, :, sl] = torch.from_numpy((e + 127).astype(np.uint8))
+                held[i][w] = y * np.exp2(e)[..., None]
+            else:
+                r = torch.from_numpy(x).to(torch.bfloat16)
+                cells[w][pg, :, sl] = r
+                held[i][w] = r.double().numpy()
+    for x, y in zip((c.k, c.v), cells):
+        x.copy_(y.view(torch.float8_e4m3fn) if e4m3 else y)
+    if e4m3:
+        c.k_scale.copy_(scales[0])
+        c.v_scale.copy_(scales[1])
+    return held
 
 
 # ------------------------------------------------------------ whole batches
@@ -103,3 +132,49 @@ def test_read_leaves_rows_before_position_0(fmt, dtype):
     check()
     for t, w in zip(outs, want):
         assert np.array_equal(t.double().cpu().numpy(), w)
+
+
+# ------------------------------------------------------- ends of the range
+
+def rising(rng, b, heads, dim, step, size):
+    """Keys whose scores with a query of 1 along axis 3 rise by `step` every 128 positions; values of `size`."""
+    held = []
+    for t in b.lens:
+        k = np.zeros((int(t), heads, dim))
+        k[:, :, 3] = (np.arange(t) // 128)[:, None] * step
+        held.append([k, rng.normal(size=(int(t), heads, dim)) * size])
+    return held
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,max_new", [(1, 1), (40, 40), (200, 200), (300, 0)])
+def test_large_values_under_rising_scores(n, max_new, dim, fmt):
+    """V near 2^80, every key tile's scores 50 (log2) above the one before: the sums that a running maximum leaves
+    behind stay in range, in each kernel."""
+    b = cu.Batch([(n, 700), (n, 1000)], 16)       # not cut: one running maximum from the first tile to the last
+    c = nan_cache(b, 1, dim, fmt)
+    rng = np.random.default_rng(32)
+    held = put(c, b, rising(rng, b, 1, dim, 1.0, 2.0 ** 80))
+    with ones_queries(50 * np.log(2.0), dim):
+        attend(b, c, held, 2, rng, scale=1.0, max_new=max_new)
+
+
+class ones_queries:
+    """Within it, test_gpu_cache.values gives queries of `size` along axis 3 and nothing else."""
+
+    def __init__(self, size, dim):
+        self.size, self.dim = size, dim
+
+    def __enter__(self):
+        import test_gpu_cache as m
+        self.module, self.was = m, m.values
+
+        def q(rng, shape, spread=1.0):
+            x = np.zeros(shape)
+            x[..., 3] = self.size
+            return torch.from_numpy(x).to(torch.bfloat16).double().numpy()
+        m.values = q
+
+    def __exit__(self, *a):
+        self.module.values = self.was
