@@ -534,7 +534,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             }
             const bool mine = at >= 0;
             float m_ref = -INFINITY, m_max = -INFINITY, l = 0.f;
-            float qs = 1.f;  // e4m3: Q is qs times its f16 values
+            int qe = 0;      // e4m3: Q is 2^-qe times its f16 values
             int vref = 0;    // e4m3: A is in units of 2^(vref - 133 - 7), l in units of 2^-7
             for (int j = 0; j < n; j++) {
                 if (!warp_wait(&ctl->s_full[x], (ct + j) & 1, abort, p.err, kDevTimeoutSoftmax)) {
@@ -549,17 +549,22 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 tmem_ld32_max(srow + 32, u + 32, hm1);
                 tmem_ld32_max(srow + 64, u + 64, hm2);
                 tmem_ld32_max(srow + 96, u + 96, hm3);
-                float ft = 1.f, cr = c, shift = 1.f;  // a score is ft times what the product gives
+                float ft = 1.f, ft2 = 1.f, cr = c, shift = 1.f;  // a score is ft * ft2 times what the product gives
                 if constexpr (E4M3) {
                     const Refs rf = reinterpret_cast<const Refs *>(smem + C::SC_OFF)[(gt0 + j) % (2 * C::ST)];
                     if (j == 0) {
-                        qs = pow2(-(int)reinterpret_cast<const int8_t *>(smem + C::QS_OFF)[((ci & 1) * 2 + x) * kRows + row]);
+                        qe = reinterpret_cast<const int8_t *>(smem + C::QS_OFF)[((ci & 1) * 2 + x) * kRows + row];
                         vref = rf.v;
                     }
                     shift = pow2(vref - rf.v);
                     vref = rf.v;
-                    ft = pow2(max(rf.k - 133, -126)) * qs;
-                    cr = fmaxf(c * ft, 1.2e-38f);  // not 0: a dropped score is -inf
+                    // Both powers in one: each alone may lie beyond fp32's where the other brings it back.  Neither factor
+                    // is 0, which would make NaN of a dropped score: below 2^-126 the exponentials take 2^-126 (scores of
+                    // less than 2^-95 either way), and the maximum a second factor.
+                    const int e = rf.k - 133 - qe;
+                    ft = pow2(min(127, max(e, -126)));
+                    ft2 = pow2(min(0, max(e + 126, -126)));
+                    cr = fmaxf(c * ft, 1.2e-38f);
                 }
                 tmem_wait_ld();
                 float mx = fmaxf(max3(hm0, hm1, hm2), hm3);
@@ -568,7 +573,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
 #pragma unroll
                     for (int q = 0; q < kKeys; q += 32) mx = fmaxf(mx, mask_chunk(u + q, q, 0, jhi));
                 }
-                if constexpr (E4M3) mx *= ft;
+                if constexpr (E4M3) mx = mx * ft * ft2;
                 m_max = fmaxf(m_max, mx);
                 float alpha = 1.f;
                 if (mx != -INFINITY && (m_ref == -INFINITY || (mx - m_ref) * c > kLazy)) {

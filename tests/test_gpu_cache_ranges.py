@@ -178,3 +178,29 @@ class ones_queries:
 
     def __exit__(self, *a):
         self.module.values = self.was
+
+
+@pytest.mark.parametrize("power", [-118, -112, 105, 110, 118])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", [50])
+def test_keys_to_the_ends_of_the_scales(n, dim, power):
+    """8-bit K at 2^power and Q at 2^-power: ordinary scores, whatever the scales are."""
+    b = cu.Batch([(n, 333), (n, 1200)], 16)
+    c = nan_cache(b, 1, dim, "e4m3")
+    rng = np.random.default_rng(33)
+    held = [[rng.normal(size=(int(t), 1, dim)) * s for s in (2.0 ** power, 1.0)] for t in b.lens]
+    put(c, b, held)
+    for max_new in (n, 0):
+        attend(b, c, held, 4, rng, spread=2.0 ** -power, max_new=max_new)
+
+
+@pytest.mark.parametrize("n", [60])
+def test_rows_without_keys_next_to_tiny_scores(n):
+    """Rows that keep no key where Q and K are so small that a score's unit is not an fp32 number."""
+    b = cu.Batch([(n, n - 4), (n, 2)], 16)
+    c = nan_cache(b, 1, 64, "e4m3")
+    rng = np.random.default_rng(34)
+    held = [[rng.normal(size=(int(t), 1, 64)) * s for s in (2.0 ** -118, 1.0)] for t in b.lens]
+    put(c, b, held)
+    out = attend(b, c, held, 2, rng, spread=2.0 ** -12, max_new=n)
+    assert not out[:4].any() and np.isfinite(out).all()
