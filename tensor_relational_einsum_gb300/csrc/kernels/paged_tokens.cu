@@ -25,7 +25,8 @@
 // f16 value exactly), and that is all that is done to them: 4 integer
 // instructions a pair, as the way to bf16 takes, bound this kernel at 3.5
 // TB/s.  The scales go where there is less to multiply: K's to the columns of
-// the scores, V's to the probabilities.  What f16 lacks is range, so
+// the scores (relative to the largest of the warp's keys, whose power joins
+// that of the row's Q), V's to the probabilities.  What f16 lacks is range, so
 //   - Q's rows are brought to [2^14, 2^15) by a power of two (a bf16 value is
 //     an f16 value down to 2^-28 of its row's largest, and 2^-39 of it is the
 //     step below);
@@ -231,7 +232,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         const int tok0 = w.item * sp.tok, nrows = min(sp.tok, w.s.n - tok0) * sp.group;
         // Q's fragments, and the keys that each of the thread's rows keeps
         uint32_t q[MT][KS][4];  // (a row tile alone; else written to shared memory at once)
-        float qs[MT][2];  // e4m3: a score in units of the row's scaled Q, times this, is the score
+        int qe[MT][2];    // e4m3: the row's Q is 2^-qe times its f16 values
         int lim[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; m++)
@@ -262,7 +263,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
                     const int e = big == 0 || big >= 0x7f80u ? 0 : min(126, 14 - ((int)(big >> 7) - 127));
                     const float up = pow2(e);
-                    qs[m][h] = pow2(-e);
+                    qe[m][h] = e;
 #pragma unroll
                     for (int x = 0; x < D / 64; x++)
 #pragma unroll
@@ -311,7 +312,6 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             for (int h = 0; h < 2; h++) {
                 mref[m][h] = mmax[m][h] = -INFINITY;
                 l[m][h] = 0.f;
-                if constexpr (!E4M3) qs[m][h] = 1.f;
             }
         int least = INT32_MAX;  // keys that all of the thread's rows keep
 #pragma unroll
@@ -372,18 +372,21 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 }
                 float vsc[N][2];    // what V's scales make of the probabilities
                 float shift = 1.f;  // what a new vref makes of the accumulators
+                int kref = 0;       // the largest scale byte of the warp's keys of K: the scores' unit
                 if constexpr (E4M3) {
                     // a lane's key: its scale bytes (0 beyond the end), turned into factors once and passed around.  NaN
-                    // vectors (255) do not move vref.
+                    // vectors (255) move neither reference.
                     const uint8_t *sc = smem + C::S * C::STAGE + slot * C::SCALES + warp * 32 * C::G;
                     const int mine = C::G == 2 ? lane : lane & 15;
                     const uint32_t kb = sc[mine], vb = sc[16 * C::G + mine];
                     const int vmax = (int)__reduce_max_sync(0xffffffffu, vb == 255u ? 0u : vb);
+                    kref = (int)__reduce_max_sync(0xffffffffu, kb == 255u ? 0u : kb);
                     if (vmax > vref) {
                         shift = pow2(vref - vmax);
                         vref = vmax;
                     }
-                    const float kf = scale_value(kb), vf = vb == 255u ? __uint_as_float(0x7fffffffu) : pow2((int)vb - vref + 7);
+                    const float kf = kb == 255u ? __uint_as_float(0x7fffffffu) : pow2((int)kb - kref);
+                    const float vf = vb == 255u ? __uint_as_float(0x7fffffffu) : pow2((int)vb - vref + 7);
 #pragma unroll
                     for (int n = 0; n < N; n++)
 #pragma unroll
@@ -400,7 +403,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 uint32_t pf[MT][C::G][4];
 #pragma unroll
                 for (int m = 0; m < MT; m++) {
-                    float mx[2];
+                    float mx[2], cr[2];  // cr: what makes exponents (log2) of the products
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
                         if (cut) {
@@ -416,19 +419,29 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         for (int n = 0; n < N; n++) mx[h] = fmaxf(mx[h], fmaxf(s[m][n][2 * h], s[m][n][2 * h + 1]));
                         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
                         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                        cr[h] = c;
+                        if constexpr (E4M3) {
+                            // K's power and Q's in one: each alone may lie beyond fp32's where the other brings it back.
+                            // No factor is 0, which would make NaN of a dropped score: below 2^-126 the exponentials take
+                            // 2^-126 (scores of less than 2^-95 either way), and the maximum a second factor.
+                            const int e = kref - 127 - qe[m][h];
+                            const float ft = pow2(min(127, max(e, -126)));
+                            mx[h] = mx[h] * ft * pow2(min(0, max(e + 126, -126)));
+                            cr[h] = fmaxf(c * ft, 1.2e-38f);
+                        }
                         mmax[m][h] = fmaxf(mmax[m][h], mx[h]);
                     }
                     bool move = false;
 #pragma unroll
                     for (int h = 0; h < 2; h++)
-                        move |= mx[h] != -INFINITY && (mref[m][h] == -INFINITY || (mx[h] - mref[m][h]) * (c * qs[m][h]) > kLazy);
+                        move |= mx[h] != -INFINITY && (mref[m][h] == -INFINITY || (mx[h] - mref[m][h]) * c > kLazy);
                     if constexpr (E4M3) move |= shift != 1.f;
                     if (__any_sync(0xffffffffu, move)) {
                         float f[2];
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
                             const float to = mmax[m][h];
-                            f[h] = mref[m][h] == -INFINITY ? 0.f : ex2((mref[m][h] - to) * (c * qs[m][h]));
+                            f[h] = mref[m][h] == -INFINITY ? 0.f : ex2((mref[m][h] - to) * c);
                             mref[m][h] = to;
                             l[m][h] *= f[h];
                             if constexpr (E4M3) f[h] *= shift;
@@ -443,10 +456,10 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     }
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const float cq = c * qs[m][h], nb = mref[m][h] == -INFINITY ? 0.f : -mref[m][h] * cq;
+                        const float nb = mref[m][h] == -INFINITY ? 0.f : -mref[m][h] * c;
 #pragma unroll
                         for (int n = 0; n < N; n++) {
-                            float e0 = ex2(fmaf(s[m][n][2 * h], cq, nb)), e1 = ex2(fmaf(s[m][n][2 * h + 1], cq, nb));
+                            float e0 = ex2(fmaf(s[m][n][2 * h], cr[h], nb)), e1 = ex2(fmaf(s[m][n][2 * h + 1], cr[h], nb));
                             l[m][h] += e0 + e1;
                             if constexpr (E4M3) {
                                 e0 *= vsc[n][0];
@@ -526,8 +539,8 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                                 pack_bf16(o[m][n][2 * h] * inv, o[m][n][2 * h + 1] * inv);
                     }
                     if (p.m_out && tig == 0) {
-                        const float f = mref[m][h] == -INFINITY ? 0.f : ex2((mref[m][h] - mmax[m][h]) * (c * qs[m][h]));
-                        p.m_out[at] = mmax[m][h] * qs[m][h] * p.scale;
+                        const float f = mref[m][h] == -INFINITY ? 0.f : ex2((mref[m][h] - mmax[m][h]) * c);
+                        p.m_out[at] = mmax[m][h] * p.scale;
                         p.l_out[at] = sum * f;
                     }
                 }
@@ -542,7 +555,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
 #pragma unroll
             for (int h = 0; h < 2; h++)
                 if (tig == 0)
-                    s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h] * qs[m][h], l[m][h], mmax[m][h] * qs[m][h], unit);
+                    s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h], l[m][h], mmax[m][h], unit);
         const bool whole = w.u0 == 0 && np == w.units;
         const int64_t part = 2 * (int64_t)blockIdx.x + (first_part ? 0 : 1);
         constexpr int H = 256 * D > C::STAGE ? 2 : 1, DH = D / H;  // a smaller slot holds half of the columns at a time

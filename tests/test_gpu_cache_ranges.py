@@ -182,7 +182,7 @@ class ones_queries:
 
 @pytest.mark.parametrize("power", [-118, -112, 105, 110, 118])
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("n", [50])
+@pytest.mark.parametrize("n", [1, 5, 50])
 def test_keys_to_the_ends_of_the_scales(n, dim, power):
     """8-bit K at 2^power and Q at 2^-power: ordinary scores, whatever the scales are."""
     b = cu.Batch([(n, 333), (n, 1200)], 16)
@@ -194,7 +194,7 @@ def test_keys_to_the_ends_of_the_scales(n, dim, power):
         attend(b, c, held, 4, rng, spread=2.0 ** -power, max_new=max_new)
 
 
-@pytest.mark.parametrize("n", [60])
+@pytest.mark.parametrize("n", [5, 60])
 def test_rows_without_keys_next_to_tiny_scores(n):
     """Rows that keep no key where Q and K are so small that a score's unit is not an fp32 number."""
     b = cu.Batch([(n, n - 4), (n, 2)], 16)
