@@ -33,6 +33,7 @@ using namespace pg;
 
 constexpr int kThreads = 256;
 constexpr int kRowsCta = 16;   // rows of a CTA
+constexpr int kCheckers = kThreads - 32;  // sequences that a CTA checks
 constexpr int kStaged = 1024;  // sequence bounds staged in shared memory; longer batches are searched in global memory
 
 // The sequence that holds dense row r (starts[i] <= r < starts[i + 1]), or -1.
@@ -123,6 +124,16 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
             if (base < 0 && !before) batch_fail(p.err);
         }
         s_base[threadIdx.x] = base;
+    }
+    // A sequence out of range is reported whether or not a row led to it (idle ones, those beyond the rows, bounds that
+    // decrease, which the search does not expect).  The warps that wait for the first one's look-up check one each.
+    const int i = blockIdx.x * kCheckers + (int)threadIdx.x - 32;
+    if (blockIdx.y == 0 && threadIdx.x >= 32 && i < n_seqs) {
+        PgSeq s;
+        const bool ok = staged ? pg_seq(s_starts[i], s_starts[i + 1], s_lens[i], p.t.rows, p.t.max_new, p.t.cap, &s)
+                               : pg_seq(__ldg(p.t.starts + i), __ldg(p.t.starts + i + 1), __ldg(p.t.lens + i), p.t.rows,
+                                        p.t.max_new, p.t.cap, &s);
+        if (!ok || (!READ && s.n > s.len)) batch_fail(p.err);
     }
     __syncthreads();
     int64_t cell[U];
@@ -236,22 +247,12 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
             }
         }
     }
-    // A sequence out of range is reported whether or not a row led to it (idle ones, those beyond the rows, bounds that
-    // decrease, which the search does not expect).  A thread each, behind the copies.
-    const int i = blockIdx.x * kThreads + threadIdx.x;
-    if (blockIdx.y == 0 && i < n_seqs) {
-        PgSeq s;
-        const bool ok = staged ? pg_seq(s_starts[i], s_starts[i + 1], s_lens[i], p.t.rows, p.t.max_new, p.t.cap, &s)
-                               : pg_seq(__ldg(p.t.starts + i), __ldg(p.t.starts + i + 1), __ldg(p.t.lens + i), p.t.rows,
-                                        p.t.max_new, p.t.cap, &s);
-        if (!ok || (!READ && s.n > s.len)) batch_fail(p.err);
-    }
 }
 
 template <int D, bool F32, bool E4M3, int U>
 cudaError_t launch_u(const PgRows &p, int64_t *ctas, cudaStream_t st) {
     constexpr int hc = U * kThreads / (D / 8) / kRowsCta;
-    const int64_t by_rows = (p.t.rows + kRowsCta - 1) / kRowsCta, by_seqs = (p.t.n_seqs + kThreads - 1) / kThreads;
+    const int64_t by_rows = (p.t.rows + kRowsCta - 1) / kRowsCta, by_seqs = (p.t.n_seqs + kCheckers - 1) / kCheckers;
     const dim3 grid((unsigned)std::max(by_rows, by_seqs), (unsigned)((p.c.heads + hc - 1) / hc));
     *ctas = (int64_t)grid.x * grid.y;
     if (p.read) cache_rows_kernel<D, F32, E4M3, true, U><<<grid, kThreads, 0, st>>>(p);
