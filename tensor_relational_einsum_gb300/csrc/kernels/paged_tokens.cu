@@ -195,7 +195,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PgShare shares[4];
     __shared__ int64_t scan[kThreads / 32];
-    __shared__ float4 s_ml[4][16 * MT];  // a warp's reference maximum, sum, maximum of its rows; unit of its output
+    __shared__ float4 s_ml[4][16 * MT];  // a warp's reference maximum, sum, maximum of its rows; its vref
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     let_next_start();
@@ -514,8 +514,8 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 1);
                 l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 2);
             }
-        const float unit = E4M3 ? ldexpf(1.f, vref - 127 - 7) : 1.f;
         if (solo) {
+            const float unit = E4M3 ? ldexpf(1.f, vref - 127 - 7) : 1.f;
             // ---- the warp has the item to itself
 #pragma unroll
             for (int m = 0; m < MT; m++)
@@ -524,13 +524,15 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     const int r = m * 16 + h * 8 + gid;
                     if (r >= nrows) continue;
                     const int64_t at = (int64_t)(w.s.first + tok0 + r / sp.group) * p.qheads + w.head * sp.group + r % sp.group;
-                    const float sum = l[m][h], inv = (sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum) * unit;
+                    // 1 / l first, then the unit: their product can lie below fp32's normal numbers where the result does not
+                    const float sum = l[m][h], inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
                     if constexpr (E4M3) {
 #pragma unroll
                         for (int x = 0; x < D / 16; x++) {
                             const float *a = o[m][2 * x], *d = o[m][2 * x + 1];
                             *reinterpret_cast<uint2 *>(p.o + (at * D + 16 * x + 4 * tig) * 2) = make_uint2(
-                                pack_bf16(a[2 * h] * inv, d[2 * h] * inv), pack_bf16(a[2 * h + 1] * inv, d[2 * h + 1] * inv));
+                                pack_bf16(a[2 * h] * inv * unit, d[2 * h] * inv * unit),
+                                pack_bf16(a[2 * h + 1] * inv * unit, d[2 * h + 1] * inv * unit));
                         }
                     } else {
 #pragma unroll
@@ -555,7 +557,7 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
 #pragma unroll
             for (int h = 0; h < 2; h++)
                 if (tig == 0)
-                    s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h], l[m][h], mmax[m][h], unit);
+                    s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h], l[m][h], mmax[m][h], (float)vref);
         const bool whole = w.u0 == 0 && np == w.units;
         const int64_t part = 2 * (int64_t)blockIdx.x + (first_part ? 0 : 1);
         constexpr int H = 256 * D > C::STAGE ? 2 : 1, DH = D / H;  // a smaller slot holds half of the columns at a time
@@ -586,19 +588,23 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 }
                 __syncthreads();
                 const int r = m * 16 + row;
-                float f[4], top = -INFINITY, sum = 0.f;
+                float f[4], top = -INFINITY, sum = 0.f, vtop = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; i++) top = fmaxf(top, s_ml[i][r].z);
+                for (int i = 0; i < 4; i++) {
+                    top = fmaxf(top, s_ml[i][r].z);
+                    if constexpr (E4M3) vtop = fmaxf(vtop, s_ml[i][r].w);
+                }
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const float4 v = s_ml[i][r];
                     f[i] = v.x == -INFINITY ? 0.f : ex2((v.x - top) * c);
                     sum = fmaf(f[i], v.y, sum);
-                    if constexpr (E4M3) f[i] *= v.w;
+                    if constexpr (E4M3) f[i] *= pow2((int)(v.w - vtop));  // to the largest of the warps' units
                 }
                 if (r < nrows) {
                     const int64_t at = ((int64_t)(w.s.first + tok0 + r / sp.group) * p.qheads + w.head * sp.group + r % sp.group);
                     const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+                    const float unit = E4M3 ? ldexpf(1.f, (int)vtop - 127 - 7) : 1.f;
 #pragma unroll
                     for (int x = 0; x < DH / 32; x++) {
                         const int d = 32 * x + col;
@@ -610,6 +616,10 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                             a[1] = fmaf(f[i], v.y, a[1]);
                             a[2] = fmaf(f[i], v.z, a[2]);
                             a[3] = fmaf(f[i], v.w, a[3]);
+                        }
+                        if constexpr (E4M3) {
+#pragma unroll
+                            for (int i = 0; i < 4; i++) a[i] *= unit;
                         }
                         if (whole) {
                             *reinterpret_cast<uint2 *>(p.o + (at * D + half * DH + d) * 2) =

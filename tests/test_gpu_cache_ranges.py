@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import cache_util as cu
-from test_gpu_cache import MARK, _built, attend, bits, fill, nan_cache, on_gpu, relation  # noqa: F401
+from test_gpu_cache import MARK, _built, attend, bits, fill, nan_cache, on_gpu, relation, values, verify  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -204,3 +204,24 @@ def test_rows_without_keys_next_to_tiny_scores(n):
     put(c, b, held)
     out = attend(b, c, held, 2, rng, spread=2.0 ** -12, max_new=n)
     assert not out[:4].any() and np.isfinite(out).all()
+
+
+@pytest.mark.parametrize("kv,n,t,max_new", [(64, 1, 3000, 1), (160, 1, 512, 1), (4, 1, 500, 1), (2, 8, 6000, 8),
+                                            (3, 60, 1000, 60), (2, 60, 4000, 60), (2, 300, 1000, 0)])
+def test_small_values_keep_their_bits(kv, n, t, max_new):
+    """8-bit V near 2^-120: the quotient by the row's sum and the unit of the sums meet far below fp32's normal
+    numbers, and must not lose the result's bits."""
+    b = cu.Batch([(n, t)] * 4, 16)
+    c = nan_cache(b, kv, 64, "e4m3")
+    rng = np.random.default_rng(35)
+    held = [[rng.normal(size=(t, kv, 64)) * 0.125, (1.0 + rng.random((t, kv, 64))) * 2.0 ** -120] for _ in range(4)]
+    put(c, b, held)
+    q = values(rng, (b.rows, kv, 64))
+    tq = torch.from_numpy(q).to(torch.bfloat16).cuda()
+    from tensor_relational_einsum_gb300 import cache_attention
+    from tensor_relational_einsum_gb300.relation import check
+    out = cache_attention(relation(tq), c, on_gpu(b, max_new=max_new)).to_dense().double().cpu().numpy() * 2.0 ** 120
+    check()
+    for h in held:
+        h[1] = h[1] * 2.0 ** 120
+    verify(b, c, held, 1, q, out, None, None, True, 0.0, False, np.ones(b.rows, dtype=bool))
