@@ -469,9 +469,15 @@ typedef struct {
     int64_t reserved[4];
 } ea_cache_attn_opts;
 
-/* Bytes of workspace an ea_cache_attention of this shape needs (partial
- * results of the splits along the positions).  The call reads nothing that
- * another left there; calls that may run at the same time need one each. */
+/* Bytes of workspace an ea_cache_attention of this shape needs: partial
+ * results of the splits along the positions and, over 8-bit cells where
+ * max_new * g >= 256, the pages of longer chunks as bf16 (4 bytes * head dim *
+ * heads for each of max_pages * page positions of every sequence that can have
+ * more rows than the kernel for few rows takes: the dense rows bound their
+ * number).  Were those more than 4 GB, chunks read the 8-bit pages themselves,
+ * in about half as much time again.  A step of single tokens should therefore
+ * say so by max_new.  The call reads nothing that another left there; calls
+ * that may run at the same time need one each. */
 ea_status ea_cache_attention_workspace(ea_cache cache, const ea_page_batch *batch, ea_relation q, size_t *bytes);
 
 /* Attention of the batch's rows over their sequences' pages.  q: bf16, last

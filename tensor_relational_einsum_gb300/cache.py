@@ -86,7 +86,8 @@ class PageBatch:
     strided), ``starts`` [sequences + 1], ``lens`` [sequences].  They are kept;
     write into them for the next step.  ``max_new``:
     an upper bound of starts[i + 1] - starts[i], if known (it spares the
-    attention the kernel for longer chunks); 0: the dense rows."""
+    attention the kernel for longer chunks and, over 8-bit pages, the memory
+    where it expands theirs); 0: the dense rows."""
 
     def __init__(self, pages: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor, max_new: int = 0):
         if not isinstance(pages, torch.Tensor) or pages.dim() != 2 or pages.dtype != torch.int32 or not pages.is_cuda or \

@@ -249,7 +249,7 @@ AttnPlans plans_of(const ea_cache_s *cache, const ea_page_batch *batch, int64_t 
     a.tokens = plan_cache_tokens(t, pool_of(cache), group, causal, cache->num_sms);
     a.chunks = plan_cache_chunks(t, pool_of(cache), group, causal, cache->num_sms,
                                  a.tokens.ctas ? a.tokens.split.max_rows + 1 : 1);
-    if (a.chunks.ctas > 0) a.expand = plan_cache_expand(t, pool_of(cache), group);
+    if (a.chunks.ctas > 0) a.expand = plan_cache_expand(t, pool_of(cache), group, a.chunks.split.min_rows);
     a.bytes = a.tokens.bytes + a.chunks.bytes + a.expand.bytes;
     return a;
 }
@@ -374,17 +374,18 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
             PgAttn pc = p;
             if (a.expand.blocks > 0) {
                 char *wide = ws + a.chunks.bytes + a.tokens.bytes;
-                pc.c = PgPool{wide, wide + a.expand.bytes / 2, nullptr, nullptr, (int64_t)p.t.n_seqs * a.expand.blocks, 7,
+                pc.c = PgPool{wide, wide + a.expand.bytes / 2, nullptr, nullptr, (int64_t)a.expand.places * a.expand.blocks, 7,
                               p.c.heads, p.c.dim, EA_CACHE_BF16};
                 pc.t.pages = nullptr;
                 pc.t.page_stride = a.expand.blocks;
+                pc.t.place_rows = a.expand.place_rows;
             }
             s = chunk_maps(c, cache, q, heads, rows, a.chunks.split, a.expand.blocks > 0 ? &pc.c : nullptr, &maps);
             if (s) return s;
             if (a.expand.blocks > 0) {
                 e = launch_cache_expand(p, a.chunks.split, a.expand, pc.c.k, (cudaStream_t)stream);
                 if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");
-                ctas += (int64_t)p.t.n_seqs * a.expand.blocks * p.c.heads;
+                ctas += (int64_t)a.expand.places * a.expand.blocks * p.c.heads;
                 launches++;
             }
             e = launch_cache_chunks(pc, a.chunks, maps, wc, launches > 0, (cudaStream_t)stream);

@@ -261,10 +261,12 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         while (ok && next_part(P, kDevTimeoutProducer)) {
             // The number of this lane's page of tile j, read a tile ahead: the reads of a tile's pages do not wait for
             // one another, nor the copies for them.
+            int place = P.seq;
+            if (!E4M3 && p.t.place_rows > 0) place = (P.row0 - P.tok0) / p.t.place_rows;  // expanded pages
             auto look = [&](int j) -> int32_t {
                 const int key = (P.u0 + j) * kKeys + (lane << lg);
                 if (j >= P.tiles || (lane << lg) >= kKeys || key >= P.end) return 0;
-                const int64_t at = (int64_t)P.seq * p.t.page_stride + (key >> lg);
+                const int64_t at = (int64_t)place * p.t.page_stride + (key >> lg);
                 return p.t.pages ? __ldg(p.t.pages + at) : (int32_t)at;
             };
             int32_t next = look(0);
@@ -865,14 +867,19 @@ PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causa
     return pl;
 }
 
-PgExpand plan_cache_expand(const PgTable &t, const PgPool &c, int group) {
+PgExpand plan_cache_expand(const PgTable &t, const PgPool &c, int group, int min_rows) {
     PgExpand x{};
     if (c.fmt != EA_CACHE_E4M3 || (int64_t)t.max_new * group < 2 * kRows) return x;
-    const int64_t blocks = (t.cap + kKeys - 1) / kKeys, vectors = blocks * kKeys * t.n_seqs * c.heads;
+    const int64_t least = (min_rows + group - 1) / group;  // rows of a sequence served; <= max_new <= t.rows
+    const bool by_row = t.rows / least < t.n_seqs;
+    const int64_t places = by_row ? t.rows / least : t.n_seqs;
+    const int64_t blocks = (t.cap + kKeys - 1) / kKeys, vectors = blocks * kKeys * places * c.heads;
     // Up to 4 GB.  A batch that could need more has so many long sequences that few of them can have long chunks; it
     // keeps to the 8-bit pages.
     if (vectors * c.dim * 4 > (int64_t)1 << 32) return x;
     x.blocks = (int32_t)blocks;
+    x.places = (int32_t)places;
+    x.place_rows = by_row ? (int32_t)least : 0;
     x.bytes = (size_t)vectors * c.dim * 4;
     return x;
 }

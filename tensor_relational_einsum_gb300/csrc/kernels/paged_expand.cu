@@ -25,11 +25,25 @@ constexpr int kThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-cache_expand_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgSplit sp, char *wk, char *wv, int blocks) {
+cache_expand_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgSplit sp, char *wk, char *wv, int blocks,
+                    int place_rows) {
     constexpr int CPR = D / 16, IT = 128 * CPR / kThreads;  // 16-code chunks of a vector; of a thread and tensor
     let_next_start();
-    const int head = blockIdx.x % p.c.heads, at = blockIdx.x / p.c.heads, x = at % blocks, i = at / blocks;
+    const int head = blockIdx.x % p.c.heads, at = blockIdx.x / p.c.heads, x = at % blocks, place = at / blocks;
+    int i = place;
+    if (place_rows > 0) {
+        // The last sequence whose first row lies before the next place's.  One that is served has place_rows rows or
+        // more, so those behind it start at or beyond the next place.
+        const int64_t next = (int64_t)(place + 1) * place_rows;
+        int b = p.t.n_seqs - 1;
+        for (i = 0; i < b;) {
+            const int mid = (i + b + 1) >> 1;
+            if (__ldg(p.t.starts + mid) < next) i = mid;
+            else b = mid - 1;
+        }
+    }
     const PgSeq s = load_seq(p.t, i, p.err);
+    if (place_rows > 0 && s.first / place_rows != place) return;
     const int key0 = x * 128, lg = p.c.page_log2;
     if (!pg_served(s, sp) || key0 >= s.len) return;
     const int64_t out0 = ((int64_t)at * p.c.heads + head) * 128;  // first vector of the block in the workspace
@@ -63,10 +77,10 @@ cache_expand_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
 }  // namespace
 
 cudaError_t launch_cache_expand(const PgAttn &p, const PgSplit &sp, const PgExpand &x, char *ws, cudaStream_t st) {
-    const unsigned grid = (unsigned)((int64_t)p.t.n_seqs * x.blocks * p.c.heads);
+    const unsigned grid = (unsigned)((int64_t)x.places * x.blocks * p.c.heads);
     char *wv = ws + x.bytes / 2;
-    if (p.c.dim == 64) cache_expand_kernel<64><<<grid, kThreads, 0, st>>>(p, sp, ws, wv, x.blocks);
-    else cache_expand_kernel<128><<<grid, kThreads, 0, st>>>(p, sp, ws, wv, x.blocks);
+    if (p.c.dim == 64) cache_expand_kernel<64><<<grid, kThreads, 0, st>>>(p, sp, ws, wv, x.blocks, x.place_rows);
+    else cache_expand_kernel<128><<<grid, kThreads, 0, st>>>(p, sp, ws, wv, x.blocks, x.place_rows);
     return cudaGetLastError();
 }
 

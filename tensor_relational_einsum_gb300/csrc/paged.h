@@ -44,11 +44,12 @@ struct PgPool {
 };
 
 struct PgTable {
-    const int32_t *pages, *starts, *lens;  // pages NULL: page x of sequence i is number i * page_stride + x
+    const int32_t *pages, *starts, *lens;  // pages NULL: page x of sequence i is number place(i) * page_stride + x
     int64_t page_stride;
     int64_t rows;        // dense rows
     int64_t cap;         // positions that a sequence can have
     int32_t n_seqs, max_pages, max_new;
+    int32_t place_rows;  // pages NULL: the place of sequence i; 0: i; else first row / place_rows
 };
 
 struct PgRows {          // append and read
@@ -124,11 +125,18 @@ PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causa
 cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, const PgWork &w, bool early, cudaStream_t st);
 
 // 8-bit pages as bf16 vectors in the workspace, in blocks of 128 positions.
+// There are places for as many sequences as the chunk kernel can serve: one
+// has at least `least` rows, so `rows / least` of them at most.  Where the
+// batch has more sequences than that, a sequence's place is its first row
+// divided by `least`: the first rows of two that are served lie at least so
+// far apart.
 struct PgExpand {
     int32_t blocks;              // of a sequence; 0: the chunk kernel reads the 8-bit pages itself
+    int32_t places;
+    int32_t place_rows;          // 0: a sequence's place is its number
     size_t bytes;                // K's vectors and V's
 };
-PgExpand plan_cache_expand(const PgTable &t, const PgPool &c, int group);
+PgExpand plan_cache_expand(const PgTable &t, const PgPool &c, int group, int min_rows);
 cudaError_t launch_cache_expand(const PgAttn &p, const PgSplit &sp, const PgExpand &x, char *ws, cudaStream_t st);
 
 // Chunk kernel: tiles of 128 rows on the tensor cores.

@@ -1,6 +1,8 @@
 """GPU tests of the paged cache at the ends of its ranges.
 
 Results are exact, or within cache_util.out_bound as in test_gpu_cache."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -225,3 +227,62 @@ def test_small_values_keep_their_bits(kv, n, t, max_new):
     for h in held:
         h[1] = h[1] * 2.0 ** 120
     verify(b, c, held, 1, q, out, None, None, True, 0.0, False, np.ones(b.rows, dtype=bool))
+
+
+# --------------------------------------------------------- the workspace
+
+def scaled_fill(c, b, rng):
+    """Values of every sequence at a size of its own (8-bit scales that differ between the items of a CTA)."""
+    held = [[rng.normal(size=(int(t), c.heads, c.dim)), rng.normal(size=(int(t), c.heads, c.dim)) * 2.0 ** rng.integers(-12, 13)]
+            for t in b.lens]
+    return put(c, b, held)
+
+
+def workspace(c, batch, rows, heads):
+    from tensor_relational_einsum_gb300 import Relation, _abi
+    need = ctypes.c_size_t()
+    q = Relation("bf16", (rows, heads, c.dim), [1, 1, 1], device="cuda")
+    _abi.check_status(_abi.lib().ea_cache_attention_workspace(c.handle, batch.ref, q.handle, ctypes.byref(need)))
+    return need.value
+
+
+def test_workspace_of_a_step_without_a_promise():
+    """64 single tokens, 64 heads over 8 of 128, room for 8192 positions, max_new not given: 8-bit pages are expanded for
+    at most the 12 sequences that 64 rows can bring above 32 rows of a group, not for all 64."""
+    from tensor_relational_einsum_gb300 import PageBatch, PagedCache
+    c = PagedCache(8, 128, 8, 128, "e4m3")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = PageBatch(torch.zeros(64, 64, **i32), torch.arange(65, **i32), torch.ones(64, **i32))
+    wide = 12 * 8192 * 8 * 128 * 4
+    assert wide <= workspace(c, batch, 64, 64) <= wide + (100 << 20)
+    short = PageBatch(torch.zeros(64, 64, **i32), torch.arange(65, **i32), torch.ones(64, **i32), max_new=1)
+    assert workspace(c, short, 64, 64) <= 100 << 20
+
+
+@pytest.mark.parametrize("group,dim", [(1, 64), (4, 128), (40, 64)])
+def test_chunks_among_many_idle_sequences(group, dim):
+    """Far more sequences than rows could serve: the expanded pages are numbered by rows."""
+    n = -(-256 // group)
+    seqs = [(0, 30)] * 40 + [(n, n + 200)] + [(0, 0)] * 30 + [(2, 50)] * 3 + [(0, 9)] * 5 + [(n + 5, n + 5), (0, 3), (n // 4 + 1, 300)]
+    seqs += [(0, 5)] * 600 + [(1, 7)]
+    b = cu.Batch(seqs, 16, before=3, behind=5)
+    c = nan_cache(b, 2, dim, "e4m3")
+    rng = np.random.default_rng(40)
+    attend(b, c, scaled_fill(c, b, rng), group, rng)
+
+
+def test_overlapping_sequences_of_expanded_pages_are_reported():
+    """Bounds that go back and forth, so that more sequences seem to have long chunks than the rows allow: the error is
+    raised and rows of no sequence stay as they were."""
+    from tensor_relational_einsum_gb300 import EaError, PageBatch, PagedCache, cache_attention
+    from tensor_relational_einsum_gb300.relation import check
+    c = PagedCache(8, 16, 2, 64, "e4m3")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = PageBatch(torch.zeros(200, 8, **i32), torch.tensor([0, 60] * 100 + [0], **i32), torch.full((200,), 100, **i32))
+    q = torch.randn(64, 16, 64, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, MARK)
+    cache_attention(relation(q), c, batch, out=relation(out))
+    with pytest.raises(EaError) as e:
+        check()
+    assert e.value.code == 10
+    assert (out[60:] == MARK).all()
