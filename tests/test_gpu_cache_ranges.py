@@ -286,3 +286,53 @@ def test_overlapping_sequences_of_expanded_pages_are_reported():
         check()
     assert e.value.code == 10
     assert (out[60:] == MARK).all()
+
+
+# -------------------------------------------------- CTAs with many items
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("max_new", [60, 0])
+def test_chunks_many_whole_items_a_cta(max_new, dim, fmt):
+    """More than 900 items of up to 1024 positions: a CTA takes six or more, one after the other (max_new 60: 8-bit pages
+    are read as they are; 0: they are expanded)."""
+    rng = np.random.default_rng(36)
+    seqs = [(int(n), int(n + t)) for n, t in zip(rng.integers(33, 61, size=120), rng.integers(0, 300, size=120))]
+    seqs[7], seqs[50], seqs[90] = (60, 1000), (40, 0), (60, 37)
+    b = cu.Batch(seqs, 16, behind=2)
+    c = nan_cache(b, 8, dim, fmt)
+    attend(b, c, scaled_fill(c, b, rng), 1, rng, max_new=max_new)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("max_new", [85, 0])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunks_tails_wholes_and_heads_a_cta(causal, max_new, dim, fmt):
+    """More than 600 units of 128 keys in items of 1 to 12 of them, several items to a head (84 tokens each): a CTA holds
+    an item's tail, whole items and another's head."""
+    rng = np.random.default_rng(37)
+    seqs = [(int(n), int(n + t)) for n, t in zip(rng.integers(70, 86, size=12), rng.integers(0, 700, size=12))]
+    seqs[3], seqs[5], seqs[8] = (85, 1500), (85, 60), (20, 900)
+    b = cu.Batch(seqs, 32, before=1)
+    c = nan_cache(b, 8, dim, fmt)
+    attend(b, c, scaled_fill(c, b, rng), 3, rng, max_new=max_new, causal=causal)
+
+
+@pytest.mark.parametrize("group,n", [(3, 85), (5, 51), (33, 7), (127, 2)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_raw_pages_under_several_items(group, n, dim):
+    """Fewer than 256 rows of a sequence in two items a head, 8-bit pages read as they are."""
+    b = cu.Batch([(n, 400), (n, n), (n - 1, 1300), (n, 3)], 16)
+    c = nan_cache(b, 2, dim, "e4m3")
+    rng = np.random.default_rng(38)
+    attend(b, c, scaled_fill(c, b, rng), group, rng, max_new=n)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_raw_pages_where_the_expansion_has_no_room(dim):
+    """A table so wide that expanded pages could pass 4 GB: long chunks over the 8-bit pages themselves."""
+    b = cu.Batch([(600, 900), (1, 50), (300, 2500)], 128, extra_pages=1 << 16)
+    c = nan_cache(b, 2, dim, "e4m3")
+    rng = np.random.default_rng(39)
+    attend(b, c, scaled_fill(c, b, rng), 2, rng)
