@@ -415,7 +415,8 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
 extern "C" ea_status ea_cache_attention_split(const ea_page_batch *batch, int32_t page, int64_t rows, const int32_t *split,
                                               int32_t ctas, int64_t capacity, int64_t *parts, int64_t *n_parts) {
     return entry([&]() -> ea_status {
-        if (!split || !parts || !n_parts || ctas < 1 || page < 1) return set_error(EA_ERR_ARG, "ea_cache_attention_split: arguments");
+        if (!split || !parts || !n_parts || ctas < 1 || page < 1 || capacity < 0 || rows < 0)
+            return set_error(EA_ERR_ARG, "ea_cache_attention_split: arguments");
         ea_status s = batch_args(batch, page, rows);
         if (s) return s;
         const PgTable t = table_of(batch, page, rows);
