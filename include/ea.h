@@ -423,7 +423,7 @@ typedef struct {
     const int32_t *lens;    /* [n_seqs] */
     int64_t page_stride;    /* elements between the rows of pages, >= max_pages */
     int32_t n_seqs;         /* 1 .. 65536 */
-    int32_t max_pages;      /* pages a sequence can have: lens[i] <= max_pages * page */
+    int32_t max_pages;      /* pages a sequence can have: lens[i] <= max_pages * page <= 2^31 - 8192 */
     int32_t max_new;        /* an upper bound of n_i known to the caller; 0: the dense rows */
     int32_t reserved;
 } ea_page_batch;

@@ -35,10 +35,11 @@ ea_status batch_args(const ea_page_batch *b, int32_t page, int64_t rows) {
     if (b->n_seqs < 1 || b->n_seqs > 65536) return set_error(EA_ERR_ARG, "cache: n_seqs %d out of [1, 65536]", b->n_seqs);
     if (b->max_pages < 1 || b->page_stride < b->max_pages)
         return set_error(EA_ERR_ARG, "cache: max_pages %d, page_stride %lld", b->max_pages, (long long)b->page_stride);
-    if ((int64_t)b->max_pages * page > INT32_MAX)
-        return set_error(EA_ERR_UNSUPPORTED, "cache: a sequence of more than 2^31 - 1 positions");
+    // The kernels step over an end by a tile, or a warp's pages of a tile, in 32 bits.
+    constexpr int64_t most = INT32_MAX - 8191;
+    if ((int64_t)b->max_pages * page > most) return set_error(EA_ERR_UNSUPPORTED, "cache: a sequence of more than %lld positions", (long long)most);
     if (b->max_new < 0) return set_error(EA_ERR_ARG, "cache: max_new %d", b->max_new);
-    if (rows > INT32_MAX) return set_error(EA_ERR_UNSUPPORTED, "cache: more than 2^31 - 1 rows");
+    if (rows > most) return set_error(EA_ERR_UNSUPPORTED, "cache: more than %lld rows", (long long)most);
     return EA_OK;
 }
 

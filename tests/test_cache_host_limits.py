@@ -6,7 +6,7 @@ import numpy as np
 
 import cache_util as cu
 from tensor_relational_einsum_gb300 import _abi
-from test_cache_host import ARG, L, host_batch  # noqa: F401
+from test_cache_host import ARG, BASE, UNSUP, L, batch, cache, host_batch, rel  # noqa: F401
 
 
 def test_split_refuses_a_negative_capacity(L):  # noqa: F811
@@ -21,3 +21,25 @@ def test_split_refuses_a_negative_capacity(L):  # noqa: F811
     assert run(-1) == ARG and (parts == -5).all()
     assert run(0) == ARG and run(1) == ARG and run(64, rows=-1) == ARG
     assert run(64) == 0 and n.value > 1
+
+
+def test_positions_and_rows_near_2_to_the_31_are_refused(L):  # noqa: F811
+    """The kernels step over a sequence's end by a few thousand positions at most (a warp's pages of a tile) and by a
+    tile of rows: what could pass 2^31 - 1 that way is refused."""
+    c = cache(L)[1]
+    k, v = rel(L, "bf16", (10, 2, 64)), rel(L, "bf16", (10, 2, 64), at=BASE + (1 << 20))
+    q, o = rel(L, "bf16", (10, 6, 64)), rel(L, "bf16", (10, 6, 64), at=BASE + (1 << 20))
+    need = ctypes.c_size_t()
+    for pages in ((1 << 27) - 1, ((1 << 31) - 4096) // 16):
+        b = ctypes.byref(batch(max_pages=pages))
+        assert L.ea_cache_append(c, b, k, v, None) == UNSUP and L.ea_cache_read(c, b, k, v, None) == UNSUP
+        assert L.ea_cache_attention_workspace(c, b, q, ctypes.byref(need)) == UNSUP
+        assert L.ea_cache_attention(c, b, q, None, None, o) == UNSUP
+        a, keep = host_batch(cu.Batch([(1, 1)], 16))
+        a.max_pages = a.page_stride = pages
+        assert L.ea_cache_check_batch(8, 16, ctypes.byref(a), 1, 1) == UNSUP
+    big = 1 << 40
+    one = cache(L, heads=1, k=BASE << 3, v=BASE << 4)[1]
+    rows = (1 << 31) - 4096
+    k, v = rel(L, "bf16", (rows, 1, 64), at=big), rel(L, "bf16", (rows, 1, 64), at=2 * big)
+    assert L.ea_cache_append(one, ctypes.byref(batch(pages=BASE << 6, starts=BASE << 6, lens=BASE << 6)), k, v, None) == UNSUP
