@@ -416,6 +416,7 @@ typedef enum { EA_CACHE_BF16 = 0, EA_CACHE_E4M3 = 1 } ea_cache_format;
  * sequence has rows: ea_check reports EA_ERR_BOUNDS.  Where starts decrease,
  * an append or a read may leave out rows of other sequences too.  A call
  * without dense rows launches nothing and checks nothing on the device.
+ * The arrays lie apart from what a call writes (EA_ERR_ARG).
  * ea_cache_check_batch is the same check on the host. */
 typedef struct {
     const int32_t *pages;   /* [n_seqs][page_stride], the first max_pages of a row in use */

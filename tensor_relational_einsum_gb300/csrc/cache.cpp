@@ -77,6 +77,18 @@ bool in_cache(const ea_cache_s *c, const void *p, size_t bytes) {
 
 bool in_cache(const ea_cache_s *c, const ea_relation_s *r) { return in_cache(c, r->arena, r->bytes); }
 
+// The batch's arrays share bytes with [p, p + bytes).
+bool in_batch(const ea_page_batch *b, const void *p, size_t bytes) {
+    const size_t n = b->n_seqs;
+    return overlap(b->pages, ((n - 1) * b->page_stride + b->max_pages) * 4, p, bytes) || overlap(b->starts, (n + 1) * 4, p, bytes) ||
+           overlap(b->lens, n * 4, p, bytes);
+}
+
+bool in_batch(const ea_page_batch *b, const ea_cache_s *c) {
+    const size_t n = cache_bytes(c), ns = (size_t)c->n_pages * c->heads * c->page;
+    return in_batch(b, c->k, n) || in_batch(b, c->v, n) || in_batch(b, c->ks, c->ks ? ns : 0) || in_batch(b, c->vs, c->vs ? ns : 0);
+}
+
 ea_status here(const ea_cache_s *c, DevCtx **ctx) {
     ea_status s = get_ctx(ctx);
     if (s) return s;
@@ -114,6 +126,8 @@ ea_status rows_call(const char *what, bool read, ea_cache cache, const ea_page_b
     if (rows * heads > INT32_MAX) return set_error(EA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 vectors", what);
     if (in_cache(cache, k) || in_cache(cache, v)) return set_error(EA_ERR_ARG, "%s: K or V overlaps the cache", what);
     if (read && overlap(k->arena, k->bytes, v->arena, v->bytes)) return set_error(EA_ERR_ARG, "%s: K and V overlap", what);
+    if (read ? in_batch(batch, k->arena, k->bytes) || in_batch(batch, v->arena, v->bytes) : in_batch(batch, cache))
+        return set_error(EA_ERR_ARG, "%s: the batch's arrays lie in what the call writes", what);
     std::lock_guard<std::mutex> lk(g_mu);
     DevCtx *c;
     s = here(cache, &c);
@@ -337,7 +351,8 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
             if (!outs[i]) continue;
             bool bad = in_cache(cache, outs[i]) || overlap(outs[i]->arena, outs[i]->bytes, q->arena, q->bytes);
             for (int j = 0; j < i; j++) bad |= outs[j] && overlap(outs[i]->arena, outs[i]->bytes, outs[j]->arena, outs[j]->bytes);
-            if (bad) return set_error(EA_ERR_ARG, "ea_cache_attention: an output overlaps Q, the cache or another output");
+            bad |= in_batch(batch, outs[i]->arena, outs[i]->bytes);
+            if (bad) return set_error(EA_ERR_ARG, "ea_cache_attention: an output overlaps Q, the cache, the batch or another output");
         }
         std::lock_guard<std::mutex> lk(g_mu);
         DevCtx *c;
@@ -362,7 +377,8 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
         if (a.bytes > 0) {
             bool bad = in_cache(cache, o.workspace, a.bytes) || overlap(o.workspace, a.bytes, q->arena, q->bytes);
             for (const ea_relation_s *r : outs) bad |= r && overlap(o.workspace, a.bytes, r->arena, r->bytes);
-            if (bad) return set_error(EA_ERR_ARG, "ea_cache_attention: the workspace overlaps an operand or the cache");
+            bad |= in_batch(batch, o.workspace, a.bytes);
+            if (bad) return set_error(EA_ERR_ARG, "ea_cache_attention: the workspace overlaps an operand, the cache or the batch");
         }
         // (expansion,) chunks, tokens, merge: the tokens' CTAs fill the SMs that the chunks' leave
         char *ws = (char *)o.workspace;

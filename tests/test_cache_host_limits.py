@@ -43,3 +43,29 @@ def test_positions_and_rows_near_2_to_the_31_are_refused(L):  # noqa: F811
     rows = (1 << 31) - 4096
     k, v = rel(L, "bf16", (rows, 1, 64), at=big), rel(L, "bf16", (rows, 1, 64), at=2 * big)
     assert L.ea_cache_append(one, ctypes.byref(batch(pages=BASE << 6, starts=BASE << 6, lens=BASE << 6)), k, v, None) == UNSUP
+
+
+def test_what_a_call_writes_may_not_hold_the_batch(L):  # noqa: F811
+    """The kernels read the table throughout a call: outputs and (append) the cache lie apart from it.  Only refusals:
+    the addresses are never read."""
+    at = BASE << 6
+    c = cache(L)[1]
+    k, v = rel(L, "bf16", (10, 2, 64)), rel(L, "bf16", (10, 2, 64), at=BASE + (1 << 20))
+    q, o = rel(L, "bf16", (10, 6, 64)), rel(L, "bf16", (10, 6, 64), at=BASE + (1 << 20))
+    m, l = rel(L, "f32", (10, 6), at=BASE + (1 << 21)), rel(L, "f32", (10, 6), at=BASE + (1 << 22))
+    size, pool = 10 * 2 * 64 * 2, 8 * 2 * 16 * 64 * 2
+    opts = _abi.CacheAttnOpts(0.0, 1, m.value, l.value, None, 0)
+    for field, n in (("pages", (2 * 7 + 4) * 4), ("starts", 16), ("lens", 12)):
+        def b(where):
+            kw = dict(pages=at, starts=at + (1 << 16), lens=at + (1 << 17))
+            kw[field] = where
+            return ctypes.byref(batch(n_seqs=3, stride=7, **kw))
+        for lo in (BASE << 1, BASE << 2):                            # the cache's K and V
+            for where in (lo, lo + pool - 4, lo - n + 4):
+                assert L.ea_cache_append(c, b(where), k, v, None) == ARG
+        for lo in (BASE, BASE + (1 << 20)):                          # what a read writes
+            for where in (lo, lo + size - 4, lo - n + 4):
+                assert L.ea_cache_read(c, b(where), k, v, None) == ARG
+        for lo in (BASE + (1 << 20), BASE + (1 << 21), BASE + (1 << 22)):
+            for where in (lo, lo - n + 4):
+                assert L.ea_cache_attention(c, b(where), q, ctypes.byref(opts), None, o) == ARG

@@ -336,3 +336,30 @@ def test_raw_pages_where_the_expansion_has_no_room(dim):
     c = nan_cache(b, 2, dim, "e4m3")
     rng = np.random.default_rng(39)
     attend(b, c, scaled_fill(c, b, rng), 2, rng)
+
+
+def test_a_workspace_over_the_batch_is_refused():
+    from tensor_relational_einsum_gb300 import PageBatch, _abi
+    from tensor_relational_einsum_gb300.relation import check
+    b = cu.Batch([(1, 2000), (40, 900)], 16)
+    c = nan_cache(b, 1, 64, "bf16")
+    rng = np.random.default_rng(41)
+    held = fill(c, b, rng)
+    q = values(rng, (b.rows, 2, 64))
+    rq = relation(torch.from_numpy(q).to(torch.bfloat16).cuda())
+    out = torch.full((b.rows, 2, 64), MARK, dtype=torch.bfloat16, device="cuda")
+    ro, L = relation(out), _abi.lib()
+    first = on_gpu(b)
+    need = workspace(c, first, b.rows, 2)
+    room = torch.zeros(need + 64, dtype=torch.uint8, device="cuda")
+    opts = _abi.CacheAttnOpts(0.0, 1, None, None, room.data_ptr(), need)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for at, want in ((need - 4, 7), (0, 7), (need, 0)):             # the lengths' place in the buffer; beyond the workspace
+        lens = room[at:at + 8].view(torch.int32)
+        batch = PageBatch(first.pages, first.starts, lens)
+        lens.copy_(first.lens)
+        assert L.ea_cache_attention(c.handle, batch.ref, rq.handle, ctypes.byref(opts), stream, ro.handle) == want
+        if want:
+            assert (out == MARK).all()
+    check()
+    verify(b, c, held, 2, q, out.double().cpu().numpy(), None, None, True, 0.0, False, np.ones(b.rows, dtype=bool))
