@@ -393,7 +393,10 @@ ea_status ea_attention_run(const char *spec, ea_relation q, ea_relation k, ea_re
  *                  before the rounding and the product after it exact, so a
  *                  code's rounding (2^-4 relative, 2^-10 * 2^(b - 127) where
  *                  the code is subnormal) is the only one, and every cell is
- *                  a bf16 value.  ea_cache_append writes no NaN code; one that
+ *                  a bf16 value, but at the ends of bf16: where b < 3 the
+ *                  smallest codes have bits below its least step, 2^-133, and
+ *                  a vector from 1.9375 * 2^127 on has a cell of 2^128, which
+ *                  is infinity.  ea_cache_append writes no NaN code; one that
  *                  was put there by other means reads as NaN. */
 typedef struct ea_cache_s *ea_cache; /* opaque handle */
 
@@ -454,8 +457,8 @@ ea_status ea_cache_destroy(ea_cache cache);
 ea_status ea_cache_append(ea_cache cache, const ea_page_batch *batch, ea_relation k, ea_relation v, void *stream);
 
 /* Read the batch's positions out of the pages into the rows of k and v (f32
- * or bf16 relations as in ea_cache_append, overwritten; exact for both
- * formats).  Rows before position 0 (n_i > lens[i]) stay as they were.
+ * or bf16 relations as in ea_cache_append, overwritten; exact, but that cells
+ * with bits below 2^-133 are rounded to the nearest even bf16).  Rows before position 0 (n_i > lens[i]) stay as they were.
  * Errors: as ea_cache_append. */
 ea_status ea_cache_read(ea_cache cache, const ea_page_batch *batch, ea_relation k, ea_relation v, void *stream);
 

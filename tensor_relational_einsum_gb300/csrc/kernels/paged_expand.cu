@@ -12,7 +12,8 @@
 // 152 / 157 / 167 us expanded; at head dim 64 71 / 74 / 79 against 93 / 95 /
 // 104 us; of 22 shapes with 48 to 240 rows two were equal (4 sequences of
 // 2048, 128 rows: 47 us, 36 us at head dim 64), none clearly faster expanded.
-// Every cell is a bf16 value, so nothing is lost.  Bound by HBM and L2: one
+// Every cell is a bf16 value (but for bits below 2^-133, under scale bytes of
+// less than 3), so nothing is lost.  Bound by HBM and L2: one
 // byte read and two written a cell, 21 us for 31.6 million of them.
 #include "paged_common.cuh"
 

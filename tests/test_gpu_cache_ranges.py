@@ -229,6 +229,54 @@ def test_small_values_keep_their_bits(kv, n, t, max_new):
     verify(b, c, held, 1, q, out, None, None, True, 0.0, False, np.ones(b.rows, dtype=bool))
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_read_of_the_smallest_cells(dim):
+    """Every code under the least scales: an fp32 read is exact, a bf16 read (whose least step is 2^-133) the nearest
+    bf16 value."""
+    from tensor_relational_einsum_gb300 import PageBatch, PagedCache, cache_read
+    from tensor_relational_einsum_gb300.relation import check
+    c = PagedCache(4, 16, 4, dim, "e4m3")
+    codes = torch.arange(256, dtype=torch.int64).repeat(16 * 4 * 4 * dim // 256)
+    codes[codes % 128 == 127] = 0                                 # no NaN codes
+    c.k.copy_(codes.to(torch.uint8).view(torch.float8_e4m3fn).view(4, 4, 16, dim))
+    c.v.copy_(c.k)
+    byte = (torch.arange(4 * 4 * 16) // 4 % 4).to(torch.uint8).view(4, 4, 16)
+    c.k_scale.copy_(byte)
+    c.v_scale.copy_(byte)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = PageBatch(torch.arange(4, **i32)[None], torch.tensor([0, 64], **i32), torch.tensor([64], **i32))
+    exact = c.k.cpu().double() * torch.exp2(byte.double() - 127)[..., None]
+    exact = exact.permute(0, 2, 1, 3).reshape(64, 4, dim)
+    k, v = cache_read(c, batch, rows=64, dtype="f32")
+    check()
+    assert torch.equal(k.to_dense().cpu().double(), exact) and torch.equal(v.to_dense().cpu().double(), exact)
+    k, v = cache_read(c, batch, rows=64)
+    check()
+    # the nearest multiple of 2^-133, ties to even (all values lie below 2^-117: steps of more than 2^-133 hold 4 bits exactly)
+    near = np.where(np.abs(exact.numpy()) < 2.0 ** -126, np.round(exact.numpy() * 2.0 ** 133) * 2.0 ** -133, exact.numpy())
+    for t in (k, v):
+        assert np.array_equal(t.to_dense().cpu().double().numpy(), near)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_largest_finite_rows(dtype):
+    """Rows up to the largest finite value: from 1.9375 * 2^127 on the nearest code is 256 under 2^120, infinity in fp32;
+    below, the cell is the nearest code's value."""
+    from tensor_relational_einsum_gb300 import cache_append, cache_read
+    from tensor_relational_einsum_gb300.relation import check
+    b = cu.Batch([(3, 3)], 16)
+    c = nan_cache(b, 1, 64, "e4m3")
+    x = torch.ones(3, 1, 64, dtype=torch.float64) * 2.0 ** 120
+    x[:, 0, 7] = torch.tensor([1.9375 * 2.0 ** 127, 1.9296875 * 2.0 ** 127, 1.75 * 2.0 ** 127], dtype=torch.float64)
+    t = x.to(torch.float32 if dtype == "f32" else torch.bfloat16).cuda()
+    cache_append(c, on_gpu(b), relation(t), relation(t.clone()))
+    k, v = cache_read(c, on_gpu(b), rows=3, dtype="f32")
+    check()
+    for g in (k.to_dense().cpu().double(), v.to_dense().cpu().double()):
+        assert g[0, 0, 7] == float("inf") and (g[0, 0, 8:] == 2.0 ** 120).all()
+        assert g[1, 0, 7] == 1.875 * 2.0 ** 127 and g[2, 0, 7] == 1.75 * 2.0 ** 127
+
+
 # --------------------------------------------------------- the workspace
 
 def scaled_fill(c, b, rng):
