@@ -678,7 +678,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         }
     } else if (E4M3 && warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::CONV));
-        // ------------------------------------------------ raw half tiles to bf16 operands
+        // ------------------------------------------------ raw tiles to f16 operands
         const int tid = threadIdx.x - 384;
         constexpr int CPR = D / 16;  // 16-byte chunks (16 codes) of a row
         uint32_t ct = 0, qx0 = 0, qx1 = 0;

@@ -560,81 +560,78 @@ cache_tokens_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     s_ml[warp][m * 16 + h * 8 + gid] = make_float4(mref[m][h], l[m][h], mmax[m][h], (float)vref);
         const bool whole = w.u0 == 0 && np == w.units;
         const int64_t part = 2 * (int64_t)blockIdx.x + (first_part ? 0 : 1);
-        constexpr int H = 256 * D > C::STAGE ? 2 : 1, DH = D / H;  // a smaller slot holds half of the columns at a time
+        static_assert(4 * 16 * D * 4 <= C::STAGE, "a slot holds the four warps' rows");
         float *scratch = reinterpret_cast<float *>(smem + (slot == 0 ? C::S - 1 : slot - 1) * C::STAGE);
         const int row = threadIdx.x / 8, col = (threadIdx.x % 8) * 4;
 #pragma unroll
         for (int m = 0; m < MT; m++) {
+            __syncthreads();  // the slot (or the scratch of the pass before) has been read by every warp
+            float *mine = scratch + warp * 16 * D;
 #pragma unroll
-            for (int half = 0; half < H; half++) {
-                __syncthreads();  // the slot (or the scratch of the pass before) has been read by every warp
-                float *mine = scratch + warp * 16 * DH;
+            for (int h = 0; h < 2; h++) {
+                const int r = h * 8 + gid, sw = (r << 3) & (D - 8);
+                if constexpr (E4M3) {
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int r = h * 8 + gid, sw = (r << 3) & (DH - 8);
+                    for (int x = 0; x < D / 16; x++) {
+                        const int n = 2 * x;
+                        *reinterpret_cast<float4 *>(mine + r * D + ((16 * x + 4 * tig) ^ sw)) =
+                            make_float4(o[m][n][2 * h], o[m][n + 1][2 * h], o[m][n][2 * h + 1], o[m][n + 1][2 * h + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+                        *reinterpret_cast<float2 *>(mine + r * D + ((8 * n + 2 * tig) ^ sw)) =
+                            make_float2(o[m][n][2 * h], o[m][n][2 * h + 1]);
+                }
+            }
+            __syncthreads();
+            const int r = m * 16 + row;
+            float f[4], top = -INFINITY, sum = 0.f, vtop = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                top = fmaxf(top, s_ml[i][r].z);
+                if constexpr (E4M3) vtop = fmaxf(vtop, s_ml[i][r].w);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float4 v = s_ml[i][r];
+                f[i] = v.x == -INFINITY ? 0.f : ex2((v.x - top) * c);
+                sum = fmaf(f[i], v.y, sum);
+                if constexpr (E4M3) f[i] *= pow2((int)(v.w - vtop));  // to the largest of the warps' units
+            }
+            if (r < nrows) {
+                const int64_t at = ((int64_t)(w.s.first + tok0 + r / sp.group) * p.qheads + w.head * sp.group + r % sp.group);
+                const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+                const float unit = E4M3 ? ldexpf(1.f, (int)vtop - 127 - 7) : 1.f;
+#pragma unroll
+                for (int x = 0; x < D / 32; x++) {
+                    const int d = 32 * x + col;
+                    float a[4] = {};
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const float4 v = *reinterpret_cast<const float4 *>(scratch + (i * 16 + row) * D + (d ^ ((row << 3) & (D - 8))));
+                        a[0] = fmaf(f[i], v.x, a[0]);
+                        a[1] = fmaf(f[i], v.y, a[1]);
+                        a[2] = fmaf(f[i], v.z, a[2]);
+                        a[3] = fmaf(f[i], v.w, a[3]);
+                    }
                     if constexpr (E4M3) {
 #pragma unroll
-                        for (int x = 0; x < DH / 16; x++) {
-                            const int n = 2 * (half * (DH / 16) + x);
-                            *reinterpret_cast<float4 *>(mine + r * DH + ((16 * x + 4 * tig) ^ sw)) =
-                                make_float4(o[m][n][2 * h], o[m][n + 1][2 * h], o[m][n][2 * h + 1], o[m][n + 1][2 * h + 1]);
-                        }
+                        for (int i = 0; i < 4; i++) a[i] *= unit;
+                    }
+                    if (whole) {
+                        *reinterpret_cast<uint2 *>(p.o + (at * D + d) * 2) =
+                            make_uint2(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[2] * inv, a[3] * inv));
                     } else {
-#pragma unroll
-                        for (int n = 0; n < NT; n++)
-                            *reinterpret_cast<float2 *>(mine + r * DH + ((8 * n + 2 * tig) ^ sw)) =
-                                make_float2(o[m][n][2 * h], o[m][n][2 * h + 1]);
+                        *reinterpret_cast<float4 *>(ws.acc + (part * 16 * MT + r) * D + d) =
+                            make_float4(a[0], a[1], a[2], a[3]);
                     }
                 }
-                __syncthreads();
-                const int r = m * 16 + row;
-                float f[4], top = -INFINITY, sum = 0.f, vtop = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    top = fmaxf(top, s_ml[i][r].z);
-                    if constexpr (E4M3) vtop = fmaxf(vtop, s_ml[i][r].w);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float4 v = s_ml[i][r];
-                    f[i] = v.x == -INFINITY ? 0.f : ex2((v.x - top) * c);
-                    sum = fmaf(f[i], v.y, sum);
-                    if constexpr (E4M3) f[i] *= pow2((int)(v.w - vtop));  // to the largest of the warps' units
-                }
-                if (r < nrows) {
-                    const int64_t at = ((int64_t)(w.s.first + tok0 + r / sp.group) * p.qheads + w.head * sp.group + r % sp.group);
-                    const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-                    const float unit = E4M3 ? ldexpf(1.f, (int)vtop - 127 - 7) : 1.f;
-#pragma unroll
-                    for (int x = 0; x < DH / 32; x++) {
-                        const int d = 32 * x + col;
-                        float a[4] = {};
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const float4 v = *reinterpret_cast<const float4 *>(scratch + (i * 16 + row) * DH + (d ^ ((row << 3) & (DH - 8))));
-                            a[0] = fmaf(f[i], v.x, a[0]);
-                            a[1] = fmaf(f[i], v.y, a[1]);
-                            a[2] = fmaf(f[i], v.z, a[2]);
-                            a[3] = fmaf(f[i], v.w, a[3]);
-                        }
-                        if constexpr (E4M3) {
-#pragma unroll
-                            for (int i = 0; i < 4; i++) a[i] *= unit;
-                        }
-                        if (whole) {
-                            *reinterpret_cast<uint2 *>(p.o + (at * D + half * DH + d) * 2) =
-                                make_uint2(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[2] * inv, a[3] * inv));
-                        } else {
-                            *reinterpret_cast<float4 *>(ws.acc + (part * 16 * MT + r) * D + half * DH + d) =
-                                make_float4(a[0], a[1], a[2], a[3]);
-                        }
-                    }
-                    if (half == 0 && threadIdx.x % 8 == 0) {
-                        if (!whole) ws.ml[part * 16 * MT + r] = make_float2(top, sum);
-                        else if (p.m_out) {
-                            p.m_out[at] = top * p.scale;
-                            p.l_out[at] = sum;
-                        }
+                if (threadIdx.x % 8 == 0) {
+                    if (!whole) ws.ml[part * 16 * MT + r] = make_float2(top, sum);
+                    else if (p.m_out) {
+                        p.m_out[at] = top * p.scale;
+                        p.l_out[at] = sum;
                     }
                 }
             }
