@@ -628,11 +628,23 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             const float to_max = m_max == -INFINITY ? 0.f : ex2((m_ref - m_max) * c);
             const float unit = E4M3 ? ldexpf(1.f, vref - 133 - 7) : 1.f;
             if constexpr (E4M3) l *= 0.0078125f;
-            float f = !whole ? to_max : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l, tiny = 1.f;
+            float f = !whole ? to_max : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
             if constexpr (E4M3) {
-                // their product can lie below fp32's normal numbers where the result does not
-                if (vref < 64) tiny = unit;
-                else f *= unit;
+                if (vref >= 64) {
+                    f *= unit;
+                } else if (n > 0) {
+                    // their product can lie below fp32's normal numbers where the result does not: A takes its unit first
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; cc++) {
+                        uint32_t o[32];
+                        tmem_ld32(orow + 32 * cc, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit);
+                        tmem_st32(orow + 32 * cc, o);
+                    }
+                    tmem_wait_st();
+                }
             }
             const int64_t prow = (int64_t)slot * (2 * half_rows) + x * half_rows + row;
 #pragma unroll
@@ -646,12 +658,6 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     for (int i = 0; i < 32; i++) o[i] = 0u;
                 }
                 if (!mine) continue;
-                if constexpr (E4M3) {
-                    if (tiny != 1.f) {
-#pragma unroll
-                        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * tiny);
-                    }
-                }
                 if (whole) {
                     uint32_t h[16];
 #pragma unroll
