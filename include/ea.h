@@ -509,7 +509,11 @@ ea_status ea_cache_attention_workspace(ea_cache cache, const ea_page_batch *batc
  * How it runs: sequences with few rows (n_i * g <= 16, or <= 32 when max_new
  * allows that many) and the others are served by kernels of their own, each
  * sharing its work out evenly over the GPU whatever the lengths are; a merge
- * follows where items were cut.
+ * follows where items were cut.  What depends on sizes (whether short
+ * sequences are cut, whether pages are expanded, the workspace) goes by
+ * max_pages * page, max_new and the rows, not by lens, which only the device
+ * knows: a table no wider than the longest sequence needs gives the variants
+ * for short ones.
  * Errors: as ea_cache_append; EA_ERR_ARG for a missing or small workspace. */
 ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *batch, ea_relation q, const ea_cache_attn_opts *opts,
                              void *stream, ea_relation out);

@@ -30,9 +30,9 @@
 // operands, to which the copies add 64 KB: 2000 cycles at 128 bytes a cycle.
 // They get in each other's way: a tile takes 3080 cycles, 2820 with the
 // softmax left out, which itself takes 1220 behind each product.  2048 tokens
-// after 14336, 32 heads over 8: 386 us, 1330 TFLOP/s, 0.70 of the measured
-// bf16 rate.  At head dim 64 the softmax is as long as the products (312 us
-// there, 0.43).  Short items pay for a part's ends, about 5000 cycles: prompts
+// after 14336, 32 heads over 8: 395 us, 1300 TFLOP/s, 0.68 of the measured
+// bf16 rate.  At head dim 64 the softmax is as long as the products (317 us
+// there, 0.42).  Short items pay for a part's ends, about 5000 cycles: prompts
 // of 2048 tokens with 32 heads of their own, 0.39.
 //
 // Keys at and beyond the sequence's end lie in the last tile only.  Their
@@ -45,7 +45,7 @@
 //              lane = row), its 128 scores in registers: mask by position,
 //              row maximum, p = 2^(c s - c m), row sum, P as 16 bits over the
 //              scores; A is rescaled in TMEM when the reference maximum is
-//              exceeded by more than 2^8 (P is an f16 value then, and A at
+//              exceeded by more than 2^8 (P fits f16 then, and A is at
 //              most 2^8 times what it is with the true maximum: the limit on
 //              V is that of the token kernel); at the part's end A / l to the
 //              output, or (m, l, A) to the workspace.
@@ -859,7 +859,7 @@ PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causa
     sp.group = group;
     sp.tok = 2 * tpt;
     // Short sequences are not cut: the tiles of an item cost less than the merge (2 x 64 tokens in 600 positions, 32 heads
-    // over 8: 26.2 us cut, 21.5 us whole).
+    // over 8: 30.0 us cut, 24.6 us whole).  As in the token kernel it is the table's width that says so.
     const bool whole = t.cap <= kWhole;
     sp.kt = whole ? kWhole : kKeys;
     sp.causal = causal;
@@ -880,8 +880,8 @@ PgExpand plan_cache_expand(const PgTable &t, const PgPool &c, int group, int min
     const bool by_row = t.rows / least < t.n_seqs;
     const int64_t places = by_row ? t.rows / least : t.n_seqs;
     const int64_t blocks = (t.cap + kKeys - 1) / kKeys, vectors = blocks * kKeys * places * c.heads;
-    // Up to 4 GB.  A batch that could need more has so many long sequences that few of them can have long chunks; it
-    // keeps to the 8-bit pages.
+    // Up to 4 GB.  A batch that could need more (many sequences that may have chunks, or a very wide table) keeps to the
+    // 8-bit pages.
     if (vectors * c.dim * 4 > (int64_t)1 << 32) return x;
     x.blocks = (int32_t)blocks;
     x.places = (int32_t)places;

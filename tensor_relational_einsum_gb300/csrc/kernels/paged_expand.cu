@@ -6,12 +6,11 @@
 // 256 rows, next to products that take all of shared memory's bandwidth: a
 // tile then takes 6000 cycles instead of 3080.  Writing 2 bytes and reading
 // them from L2 once for 256 rows is cheaper from about that many rows on
-// (2048 tokens after 14336, 32 heads over 8: 620 us there, 405 us with this
+// (2048 tokens after 14336, 32 heads over 8: 610 us there, 412 us with this
 // kernel).  Below, the 3 bytes more a cell cost more than the rewriting: 8
-// sequences of 8192, 8 heads, 48 / 128 / 240 rows: 123 / 122 / 128 us there,
-// 152 / 157 / 167 us expanded; at head dim 64 71 / 74 / 79 against 93 / 95 /
-// 104 us; of 22 shapes with 48 to 240 rows two were equal (4 sequences of
-// 2048, 128 rows: 47 us, 36 us at head dim 64), none clearly faster expanded.
+// sequences of 8192, 8 heads, 48 / 128 / 240 rows: 118 / 118 / 126 us there,
+// 151 / 157 / 166 us expanded; at head dim 64 69 / 71 / 80 against 93 / 96 /
+// 106 us.
 // Every cell is a bf16 value (but for bits below 2^-133, under scale bytes of
 // less than 3), so nothing is lost.  Bound by HBM and L2: one
 // byte read and two written a cell, 21 us for 31.6 million of them.

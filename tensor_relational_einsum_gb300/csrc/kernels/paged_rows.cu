@@ -20,8 +20,9 @@
 // conversion; the scaling itself is exact.
 //
 // Measured, 32768 rows of 16 heads of 128, of the measured copy rate: append
-// 0.96 (bf16 to bf16), 0.90 (to 8 bits), 0.99 (fp32 to 8 bits); read 0.95,
-// 0.90, 0.92 (8 bits to fp32).  A step's append takes 4.8 us.
+// 0.95 (bf16 to bf16, 83 us), 0.89 (to 8 bits, 67 us), 0.97 (fp32 to 8 bits,
+// 102 us); read 0.94 (84 us), 0.90 (66 us), 0.93 (8 bits to fp32, 107 us).  A
+// step's append takes 4.8 us.
 #include <algorithm>
 
 #include "paged_common.cuh"

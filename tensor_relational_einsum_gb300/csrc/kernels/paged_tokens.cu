@@ -35,11 +35,13 @@
 //     row's largest term, steps of 2^-31 of it below that.
 // Powers of two cost nothing in exactness: the f16 products are exact in fp32.
 //
-// Measured: 64 sequences of 8192 positions, 32 heads over 8 of 128: bf16 323
-// us, 6.6 TB/s (0.98 of the measured copy rate); 8-bit 188 us, 5.7 TB/s (0.85;
-// 36% of issue slots, the integer pipe at a third); head dim 64 bf16 0.93,
-// 8-bit 0.56, where a block's fixed work weighs twice.  A small call takes 6.5
-// us: a chain of reads (bounds, pages, cells), one block and the code itself.
+// Measured: 64 sequences of 8192 positions, 32 heads over 8 of 128: bf16
+// 324-330 us, 6.5-6.6 TB/s (0.96-0.98 of the measured copy rate); 8-bit 185
+// us, 5.86 TB/s (0.86; 36% of issue slots, the integer pipe at a third); head
+// dim 64 bf16 0.93, 8-bit 0.58, where a block's fixed work weighs twice; four
+// tokens each, 64 heads over 8 of 128 (two row tiles): bf16 0.96, 8-bit 0.54.
+// A small call takes 6.5 us: a chain of reads (bounds, pages, cells), one
+// block and the code itself.
 #include "attn_common.cuh"
 #include "paged_sched.cuh"
 
@@ -677,7 +679,8 @@ PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causa
     sp.causal = causal;
     sp.min_rows = 1;
     sp.max_rows = pl.rows;
-    // Short sequences are not cut: another block adds less than the merge's launch.
+    // Short sequences are not cut: another block adds less than the merge's launch.  The table's width says which they
+    // are: the lengths are known on the device only.
     const int64_t longest = t.cap;
     sp.kt = longest <= 512 ? 512 : c.fmt == EA_CACHE_E4M3 || c.dim == 64 ? 128 : 64;  // a block
     const int64_t units = (longest + sp.kt - 1) / sp.kt * t.n_seqs * c.heads;

@@ -175,7 +175,8 @@ EA_HD bool pg_seq(int32_t a, int32_t b, int32_t len, int64_t rows, int32_t max_n
 
 // ------------------------------------------------------------- work list
 
-// SUM_{i < n} floor((a i + b) / m) for a, b >= 0, m > 0 (Euclid's way: whole
+// SUM_{i < n} floor((a i + b) / m) for a, b >= 0, m > 0: the published way of
+// counting the lattice points under a line with Euclid's algorithm (whole
 // parts of a / m and b / m are summed in closed form, then i and the value
 // change places).
 template <class T>
