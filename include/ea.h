@@ -458,8 +458,8 @@ ea_status ea_cache_append(ea_cache cache, const ea_page_batch *batch, ea_relatio
 
 /* Read the batch's positions out of the pages into the rows of k and v (f32
  * or bf16 relations as in ea_cache_append, overwritten; exact, but that cells
- * with bits below 2^-133 are rounded to the nearest even bf16).  Rows before position 0 (n_i > lens[i]) stay as they were.
- * Errors: as ea_cache_append. */
+ * with bits below 2^-133 are rounded to the nearest even bf16).  Rows before
+ * position 0 (n_i > lens[i]) stay as they were.  Errors: as ea_cache_append. */
 ea_status ea_cache_read(ea_cache cache, const ea_page_batch *batch, ea_relation k, ea_relation v, void *stream);
 
 /* Options of ea_cache_attention; zero-initialise. */
@@ -532,8 +532,9 @@ ea_status ea_cache_attention_split(const ea_page_batch *batch, int32_t page, int
 
 /* The check of a batch on the host (no GPU needed): `batch` holds HOST
  * pointers, rows is the dense row count, write nonzero checks for an append
- * (positions >= 0, no slot named twice).  EA_OK, or EA_ERR_BOUNDS with a
- * message that names the first offender. */
+ * (positions >= 0, no slot named twice), zero for an attention, which needs the
+ * pages of all positions (a read needs those of its rows only).  EA_OK, or
+ * EA_ERR_BOUNDS with a message that names the first offender. */
 ea_status ea_cache_check_batch(int64_t pages, int32_t page, const ea_page_batch *batch, int64_t rows, int write);
 
 /* ------------------------------------------------------------ exchange */

@@ -562,7 +562,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     vref = rf.v;
                     // Both powers in one: each alone may lie beyond fp32's where the other brings it back.  Neither factor
                     // is 0, which would make NaN of a dropped score: below 2^-126 the exponentials take 2^-126 (scores of
-                    // less than 2^-95 either way), and the maximum a second factor.
+                    // less than 2^-88 either way), and the maximum a second factor.
                     const int e = rf.k - 133 - qe;
                     ft = pow2(min(127, max(e, -126)));
                     ft2 = pow2(min(0, max(e + 126, -126)));
