@@ -470,7 +470,8 @@ typedef struct {
     ea_relation l_out;       /* optional f32 relation: row sum of exp(score - maximum)          */
     void *workspace;         /* device memory, 16-byte aligned, apart from operands and cache   */
     size_t workspace_bytes;  /* at least what ea_cache_attention_workspace says                 */
-    int64_t reserved[4];
+    const int32_t *parents;  /* optional device array [rows]: the rows are nodes of trees       */
+    int64_t reserved[3];
 } ea_cache_attn_opts;
 
 /* Bytes of workspace an ea_cache_attention of this shape needs: partial
@@ -517,6 +518,110 @@ ea_status ea_cache_attention_workspace(ea_cache cache, const ea_page_batch *batc
  * Errors: as ea_cache_append; EA_ERR_ARG for a missing or small workspace. */
 ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *batch, ea_relation q, const ea_cache_attn_opts *opts,
                              void *stream, ea_relation out);
+
+/* Trees of drafted tokens (ea_cache_attn_opts.parents, ea_rotary_opts.parents,
+ * ea_verify_opts.parents).  The paper has no counterpart.  The n_i rows of a
+ * sequence are then the nodes of a tree: parents[r] of dense row r is the row
+ * of its parent counted from starts[i], smaller than the row's own count, or
+ * -1 (a root, behind the last of the other positions).  At most 128 nodes a
+ * sequence: max_new (or the dense rows) says so, else EA_ERR_UNSUPPORTED.  A
+ * parent out of range raises the device error word as a batch out of range
+ * does; rows of that sequence are then unspecified.
+ * In ea_cache_attention a tree's row keeps the positions before the
+ * sequence's new ones (t < lens[i] - n_i) and, of those, its own and its
+ * ancestors'; `causal` has no meaning.  Chains (parents j - 1) give what
+ * causal rows get.  A node's cells that a row drops must be finite, as above.
+ * ---------------------------------------------------------------------- */
+
+#define EA_ROTARY_INTERLEAVED 0 /* pairs (2 i, 2 i + 1) */
+#define EA_ROTARY_HALF 1        /* pairs (i, i + dims / 2) */
+
+/* Options of ea_rotary; zero-initialise. */
+typedef struct {
+    int32_t layout;           /* EA_ROTARY_INTERLEAVED or EA_ROTARY_HALF                          */
+    int32_t dims;             /* rotated columns of a head: even, 256 at most                     */
+    int32_t offset;           /* the first of them                                                */
+    int32_t backward;         /* nonzero: the transpose (the gradient of q and k from that of the results) */
+    float amplitude;          /* factor of cosine and sine; 0 = 1                                 */
+    int32_t reserved0;
+    const double *freqs;      /* host, [dims / 2]: radians a position, finite                     */
+    const int32_t *positions; /* device, [rows]: positions; instead of a batch                    */
+    const int32_t *parents;   /* optional device array [rows]: the rows are nodes of trees        */
+    int64_t reserved[3];
+} ea_rotary_opts;
+
+/* Rotary positions of q and (optional, with k_out) k at any rows of a batch.
+ * Pair i of the columns offset .. offset + dims of every head of a row at
+ * position t becomes
+ *   x' = a (x cos(t f_i) - y sin(t f_i)),  y' = a (x sin(t f_i) + y cos(t f_i)),
+ * `backward` negates the sine.  The other columns are copied.  t is
+ * lens[i] - n_i + j for row starts[i] + j, in a tree lens[i] - n_i + the
+ * node's depth (a root's is 0), or positions[r]; rows of no sequence and
+ * rows of a negative position stay as they are.  Of `batch` the pages are not
+ * read (and may be NULL), lens may be any length.
+ *   q, k, q_out, k_out  f32 or bf16, all the same, [rows.., heads, columns] as
+ *          in ea_cache_append; q and k may have different heads.  q_out may be
+ *          q (and then k_out k): in place; else no two overlap.
+ * The angle is taken in turns as a 64-bit fraction, t f_i modulo 1 exactly, so
+ * that far positions cost no accuracy; the rest in fp32, one rounding.
+ * The elementwise EA_MAP_ROPE and its epilogue form take a table and the
+ * positions of packed prompts; this takes the positions of a batch's rows.
+ * Errors: EA_ERR_ARG, EA_ERR_SHAPE, EA_ERR_PARTITION, EA_ERR_DTYPE,
+ * EA_ERR_UNSUPPORTED (more than 256 rotated columns, 65535 heads or columns). */
+ea_status ea_rotary(const ea_rotary_opts *opts, const ea_page_batch *batch, ea_relation q, ea_relation k,
+                    ea_relation q_out, ea_relation k_out, void *stream);
+
+/* Options of ea_verify_drafts; zero-initialise.  All arrays on the device. */
+typedef struct {
+    const int32_t *tokens;  /* [rows]: the drafted token of every node (a root's is not read)   */
+    const int32_t *parents; /* [rows], or NULL: chains                                          */
+    const float *accept;    /* [rows]: random numbers in [0, 1), one a node                     */
+    const float *sample;    /* [n_seqs]: random numbers in [0, 1) for the tokens that follow    */
+    int32_t *path;          /* [n_seqs][width]: receives the accepted nodes, -1 behind them     */
+    int32_t *counts;        /* [n_seqs]: receives their number                                  */
+    int32_t *picked;        /* [n_seqs]: receives the token that follows the last of them       */
+    int32_t width;          /* entries of a row of path, at least the most nodes of a sequence  */
+    int32_t reserved0;
+    int64_t reserved[4];
+} ea_verify_opts;
+
+/* Which branch of each sequence's tree the target's probabilities accept
+ * (speculative sampling: the tokens are distributed as if they had been drawn
+ * from the target one by one).  Row starts[i] is node 0, accepted always (the
+ * last certain token); target[r] are the probabilities of the token behind
+ * node r, draft[r] those that r's children were drawn from, each on its own.
+ * At an accepted node v, with r = target[v] and Z = 1, its children c are
+ * asked in row order: c, of token x, is accepted if
+ *   accept[c] * draft[v][x] * Z < r[x];
+ * if not, r becomes max(r - Z draft[v], 0) and Z the sum of r.  Where no child
+ * is left, picked is the least token whose running sum of r (of target[v], if
+ * r is 0 everywhere) exceeds sample[i] times r's sum; -1 if target[v] is 0
+ * everywhere, or the sequence has no rows (counts 0).  Nodes with another
+ * parent than an accepted node, and further roots, are not asked.
+ *   target  f32 or bf16 [rows.., vocab]: values in [0, 1] (others are taken as
+ *           0 or 1, NaN as 0), a row's sum below 2;
+ *   draft   as target, or NULL: the drafted tokens are certain (probability 1).
+ * Tests and sums are exact to 2^-53 and to 2^-61 an entry; sums do not depend
+ * on their order: the results are the same on every run.  Of `batch` only
+ * starts, n_seqs and max_new are read; at most 128 nodes a sequence.
+ * Errors: EA_ERR_ARG, EA_ERR_SHAPE, EA_ERR_PARTITION, EA_ERR_DTYPE,
+ * EA_ERR_UNSUPPORTED (trees, vocabulary). */
+ea_status ea_verify_drafts(const ea_verify_opts *opts, const ea_page_batch *batch, ea_relation target, ea_relation draft,
+                           void *stream);
+
+/* Keep the accepted rows of each sequence's new ones: position lens[i] - n_i +
+ * j takes the cells (and scales) of position lens[i] - n_i + path[i][j] for
+ * j < counts[i], in all caches of the list (the layers' caches: same format
+ * and extents, one batch).  path[i] increases, within 0 .. n_i - 1, as
+ * ea_verify_drafts gives it; width: entries of a row of path.  lens_out
+ * (optional, device, [n_seqs]) receives lens[i] - n_i + counts[i]; positions
+ * behind that hold what they held or other accepted cells.  A path or count
+ * out of range, or n_i > lens[i], raises the device error word; that sequence
+ * is left alone and its length too.  The batch needs max_new of at most 128.
+ * A sequence's new positions must not share slots with others.
+ * Errors: EA_ERR_ARG, EA_ERR_SHAPE, EA_ERR_DTYPE, EA_ERR_UNSUPPORTED. */
+ea_status ea_cache_keep(const ea_cache *caches, int32_t n_caches, const ea_page_batch *batch, const int32_t *path,
+                        int32_t width, const int32_t *counts, int32_t *lens_out, void *stream);
 
 /* The work list of the attention, computed on the host by the code that the
  * kernels run (no GPU needed): `batch` holds HOST pointers; split = {heads,
@@ -565,10 +670,10 @@ ea_status ea_exchange_agg(ea_relation in, ea_agg agg, const ea_dim_part *new_par
 /* What the last ea_joinagg_run / ea_exchange of the calling host thread
  * launched: kernel class (0 exchange, 1 elementwise, 2 row reduction,
  * 3 SIMT contraction, 4 tcgen05 contraction, 5 attention, 6 exchange with
- * aggregation, 7 cache append or read, 8 cache attention), kernel launches,
- * work tiles (CTAs, for 7 and 8),
- * aggregation groups and function specifications (tuples; 0 for 7 and 8,
- * whose work list is made on the device).  Any pointer
+ * aggregation, 7 cache append, read or keep, 8 cache attention, 9 rotary,
+ * 10 verification), kernel launches, work tiles (CTAs, from 7 on),
+ * aggregation groups and function specifications (tuples; 0 from 7 on,
+ * whose work is listed on the device).  Any pointer
  * may be NULL. */
 ea_status ea_last_plan(int32_t *kernel_class, int32_t *launches, int64_t *tiles, int64_t *groups, int64_t *tuples);
 

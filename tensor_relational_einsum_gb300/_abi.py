@@ -24,6 +24,7 @@ STATUS = {0: "EA_OK", 1: "EA_ERR_SPEC", 2: "EA_ERR_SHAPE", 3: "EA_ERR_PARTITION"
           5: "EA_ERR_ALLOC", 6: "EA_ERR_CUDA", 7: "EA_ERR_ARG", 8: "EA_ERR_UNSUPPORTED", 9: "EA_ERR_DEVICE",
           10: "EA_ERR_BOUNDS"}
 CACHE_FORMATS = {"bf16": 0, "e4m3": 1}
+ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
 
 
 class EaError(RuntimeError):
@@ -65,6 +66,20 @@ class PageBatchArgs(ctypes.Structure):
 class CacheAttnOpts(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("m_out", ctypes.c_void_p),
                 ("l_out", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("parents", ctypes.c_void_p), ("reserved", ctypes.c_int64 * 3)]
+
+
+class RotaryOpts(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("dims", ctypes.c_int32), ("offset", ctypes.c_int32),
+                ("backward", ctypes.c_int32), ("amplitude", ctypes.c_float), ("reserved0", ctypes.c_int32),
+                ("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("reserved", ctypes.c_int64 * 3)]
+
+
+class VerifyOpts(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("parents", ctypes.c_void_p), ("accept", ctypes.c_void_p),
+                ("sample", ctypes.c_void_p), ("path", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("picked", ctypes.c_void_p), ("width", ctypes.c_int32), ("reserved0", ctypes.c_int32),
                 ("reserved", ctypes.c_int64 * 4)]
 
 
@@ -129,6 +144,10 @@ def lib():
                                            ctypes.c_int64, ctypes.c_int]
         L.ea_cache_attention_split.argtypes = [ctypes.POINTER(PageBatchArgs), ctypes.c_int32, ctypes.c_int64, P32,
                                                ctypes.c_int32, ctypes.c_int64, P64, P64]
+        L.ea_rotary.argtypes = [ctypes.POINTER(RotaryOpts), ctypes.POINTER(PageBatchArgs), VP, VP, VP, VP, VP]
+        L.ea_verify_drafts.argtypes = [ctypes.POINTER(VerifyOpts), ctypes.POINTER(PageBatchArgs), VP, VP, VP]
+        L.ea_cache_keep.argtypes = [ctypes.POINTER(VP), ctypes.c_int32, ctypes.POINTER(PageBatchArgs), VP,
+                                    ctypes.c_int32, VP, VP, VP]
         for name in ("ea_check", "ea_plan_cache_clear", "ea_relation_create", "ea_relation_destroy",
                      "ea_relation_info", "ea_relation_block", "ea_relation_data", "ea_relation_bounds",
                      "ea_joinagg_run", "ea_exchange", "ea_plan_worklist", "ea_exchange_permutation",
@@ -136,7 +155,7 @@ def lib():
                      "ea_set_allocator", "ea_relation_copy_host", "ea_selftest_wait_timeout", "ea_plan_check_exchange",
                      "ea_cache_create", "ea_cache_destroy", "ea_cache_append", "ea_cache_read",
                      "ea_cache_attention_workspace", "ea_cache_attention", "ea_cache_check_batch",
-                     "ea_cache_attention_split"):
+                     "ea_cache_attention_split", "ea_rotary", "ea_verify_drafts", "ea_cache_keep"):
             getattr(L, name).restype = ctypes.c_int
         if L.ea_abi_version() != 5:
             raise ImportError("libea.so ABI version mismatch")
@@ -198,7 +217,7 @@ def index_parts(parts: dict | None):
 
 
 KERNEL_CLASS = {0: "exchange", 1: "elementwise", 2: "rowreduce", 3: "contract_simt", 4: "contract_tc", 5: "attention", 6: "exchange_agg",
-                7: "cache_rows", 8: "cache_attention"}
+                7: "cache_rows", 8: "cache_attention", 9: "rotary", 10: "verify"}
 
 
 def last_plan():

@@ -133,6 +133,17 @@ def _same_device(cache: PagedCache, batch: PageBatch, *relations):
             raise ValueError("the cache and a relation lie on different devices")
 
 
+def _rows_of(t: torch.Tensor, dtype, r: Relation, trailing: int, what: str) -> torch.Tensor:
+    """``t`` has an entry for every row of ``r``, on its device."""
+    rows = 1
+    for d in r.dims[:-trailing]:
+        rows *= d
+    _on_device(t, dtype, (rows,), what)
+    if t.device != r.storage.device:
+        raise ValueError(f"{what} and a relation lie on different devices")
+    return t
+
+
 def cache_append(cache: PagedCache, batch: PageBatch, k: Relation, v: Relation, stream=None):
     """Write the batch's rows of ``k`` and ``v`` (relations [rows.., heads,
     dim], f32 or bf16) into the pages, rounded to the cache's format."""
@@ -162,16 +173,22 @@ def cache_read(cache: PagedCache, batch: PageBatch, k: Relation | None = None, v
 
 def cache_attention(q: Relation, cache: PagedCache, batch: PageBatch, scale: float = 0.0, causal: bool = True,
                     out: Relation | None = None, m_out: Relation | None = None, l_out: Relation | None = None,
-                    stream=None) -> Relation:
+                    parents: torch.Tensor | None = None, stream=None) -> Relation:
     """Softmax attention of the batch's rows of ``q`` (bf16 relation [rows..,
     query heads, dim]) over their sequences' pages, query heads in groups that
     share a key-value head; ``causal``: a row keeps the positions up to its
     own.  ``scale`` 0 means 1/sqrt(dim).  ``m_out``/``l_out`` (f32 over q's
     dimensions without the last) receive the row maximum and the row sum of
-    exp.  Rows of no sequence stay as they are (in a new ``out``: undefined).
+    exp.  ``parents`` (int32 CUDA tensor, an entry a row): the rows of a
+    sequence are nodes of trees of drafted tokens, 128 at most; the entry is
+    the row of the node's parent counted from the sequence's first, -1 for a
+    root; a row keeps the positions before its sequence's rows, itself and its
+    ancestors.  Rows of no sequence stay as they are (in a new ``out``: undefined).
     The workspace for partial results comes from torch's allocator on the
     call's stream, one per call."""
     _same_device(cache, batch, q, out, m_out, l_out)
+    if parents is not None:
+        _rows_of(parents, torch.int32, q, 2, "parents")
     L = lib()
     shape = (cache.format, cache.pages, cache.page, cache.heads, cache.dim, q.dims)
     need = batch._workspace.get(shape)
@@ -192,7 +209,39 @@ def cache_attention(q: Relation, cache: PagedCache, batch: PageBatch, scale: flo
             if need:
                 work = torch.empty(need, dtype=torch.uint8, device=cache.device)
     o = _abi.CacheAttnOpts(scale, 1 if causal else 0, m_out.handle if m_out is not None else None,
-                           l_out.handle if l_out is not None else None, work.data_ptr() if work is not None else None, need)
+                           l_out.handle if l_out is not None else None, work.data_ptr() if work is not None else None, need,
+                           parents.data_ptr() if parents is not None else None)
     check_status(L.ea_cache_attention(cache.handle, batch.ref, q.handle, ctypes.byref(o),
                                       _raw_stream(cache.device, stream), out.handle))
     return out
+
+
+def cache_keep(caches, batch: PageBatch, path: torch.Tensor, counts: torch.Tensor,
+               lens_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Keep the accepted ones of each sequence's new rows: its row ``path[i,
+    j]`` becomes row j for j < ``counts[i]``, in every cache of ``caches`` (one,
+    or a list: the layers' caches, of one format and size), as
+    ``verify_drafts`` gives them (int32 CUDA tensors [sequences, width] and
+    [sequences]).  Returns ``lens_out`` (int32 [sequences], new by default):
+    the sequences' lengths with the kept rows only."""
+    caches = [caches] if isinstance(caches, PagedCache) else list(caches)
+    if not caches:
+        raise ValueError("give a cache")
+    n = batch.pages.shape[0]
+    if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[1] < 1:
+        raise ValueError("path must be an int32 CUDA tensor [sequences, width]")
+    _on_device(path, torch.int32, (n, path.shape[1]), "path")
+    _on_device(counts, torch.int32, (n,), "counts")
+    if lens_out is None:
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(batch.device):
+            lens_out = torch.empty(n, dtype=torch.int32, device=batch.device)
+    else:
+        _on_device(lens_out, torch.int32, (n,), "lens_out")
+    for c in caches:
+        _same_device(c, batch)
+    if any(t.device != batch.device for t in (path, counts, lens_out)):
+        raise ValueError("the batch and path, counts or lens_out lie on different devices")
+    handles = (ctypes.c_void_p * len(caches))(*[c.handle.value for c in caches])
+    check_status(lib().ea_cache_keep(handles, len(caches), batch.ref, path.data_ptr(), path.shape[1], counts.data_ptr(),
+                                     lens_out.data_ptr(), _raw_stream(batch.device, stream)))
+    return lens_out

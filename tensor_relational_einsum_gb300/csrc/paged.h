@@ -65,6 +65,7 @@ cudaError_t launch_cache_rows(const PgRows &p, int64_t *ctas, cudaStream_t st);
 struct PgAttn {
     PgTable t;
     PgPool c;
+    const int32_t *parents;  // [rows] or NULL: the rows of a sequence are the nodes of a tree
     const char *q;       // [rows][qheads][dim] bf16
     char *o;
     float *m_out, *l_out;
@@ -123,6 +124,7 @@ inline PgWork pg_work(const PgPlan &pl, char *b) {
 constexpr int kPgTokenRows = 32;     // the most rows of a sequence (tokens x group) that it takes
 PgPlan plan_cache_tokens(const PgTable &t, const PgPool &c, int group, int causal, int num_sms);
 cudaError_t launch_cache_tokens(const PgAttn &p, const PgPlan &pl, const PgWork &w, bool early, cudaStream_t st);
+cudaError_t launch_cache_tokens_tree(const PgAttn &p, const PgPlan &pl, const PgWork &w, bool early, cudaStream_t st);
 
 // 8-bit pages as bf16 vectors in the workspace, in blocks of 128 positions.
 // There are places for as many sequences as the chunk kernel can serve: one
@@ -146,6 +148,9 @@ struct PgMaps {                  // tensor maps: Q's rows; the pools as [vectors
 PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causal, int num_sms, int min_rows);
 cudaError_t launch_cache_chunks(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, const PgWork &w, bool early,
                                 cudaStream_t st);
+cudaError_t launch_cache_chunks_tree(const PgAttn &p, const PgPlan &pl, const PgMaps &maps, const PgWork &w, bool early,
+                                     cudaStream_t st);
+constexpr int kPgNodes = 128;        // the most nodes of a sequence's tree
 
 // The merge of both kernels' cut items.
 struct PgMerge {

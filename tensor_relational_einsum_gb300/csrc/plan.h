@@ -38,7 +38,7 @@ struct Blob {
     }
 };
 
-enum PlanKind { kExchange = 0, kEwise, kRowReduce, kSimt, kTc, kAttn, kExchangeAgg, kCacheRows, kCacheAttention };
+enum PlanKind { kExchange = 0, kEwise, kRowReduce, kSimt, kTc, kAttn, kExchangeAgg, kCacheRows, kCacheAttention, kRotary, kVerify };
 
 struct DevPlan {
     int kind = 0;

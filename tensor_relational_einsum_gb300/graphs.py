@@ -13,7 +13,8 @@ All arithmetic runs in libea.so.
                       merge of (max, sum of exp, weighted sum) triples in one
                       tcgen05 kernel.
 * ``CachedAttention`` the same for generation: new rows of K and V appended to
-                      a paged cache, the new rows of Q attending to it.
+                      a paged cache, the new rows of Q attending to it;
+                      with rotary positions, and over trees of drafted tokens.
 * ``SwigluFFN``       gate/up contractions (SUM over model-dim blocks),
                       SiLU(gate) * up elementwise join, down contraction.
 * ``MatrixChain``     the pages' matrix-chain workloads (chains A-E): a
@@ -36,7 +37,8 @@ import numpy as np
 import torch
 
 from . import _abi
-from .cache import PageBatch, PagedCache, cache_append, cache_attention
+from .cache import PageBatch, PagedCache, cache_append, cache_attention, cache_keep
+from .drafts import Rotary, rotary
 from .relation import Relation, attention, exchange, joinagg
 
 
@@ -178,20 +180,31 @@ class CachedAttention:
     are the relations that the projections fill on every step; ``batch`` names
     the rows' sequences.  Its tensors may change between runs, which is how one
     captured graph serves every step: lengths grow in place, pages are added to
-    the table."""
+    the table.
+
+    ``rotary``: q and k are rotated by their rows' positions first, in place.
+    ``parents``: the rows are nodes of trees of drafted tokens; once
+    ``verify_drafts`` has told which are accepted, ``keep`` leaves their keys
+    and values in the cache as the sequences' last positions."""
 
     def __init__(self, q: Relation, k: Relation, v: Relation, cache: PagedCache, batch: PageBatch, scale: float = 0.0,
-                 causal: bool = True):
+                 causal: bool = True, rotary: Rotary | None = None, parents: torch.Tensor | None = None):
         self.q, self.k, self.v, self.cache, self.batch = q, k, v, cache, batch
-        self.scale, self.causal = scale, causal
+        self.scale, self.causal, self.rotary, self.parents = scale, causal, rotary, parents
         self.O = Relation("bf16", q.dims, q.bounds, device=q.storage.device)
 
     def run(self, rec: Recorder | None = None):
         c = rec.call if rec is not None else _direct
+        if self.rotary is not None:
+            c("rotary", lambda: rotary(self.q, self.k, self.rotary, self.batch, parents=self.parents))
         c("cache.append", lambda: cache_append(self.cache, self.batch, self.k, self.v))
         c("attn.cached", lambda: cache_attention(self.q, self.cache, self.batch, scale=self.scale, causal=self.causal,
-                                                 out=self.O))
+                                                 out=self.O, parents=self.parents))
         return self.O
+
+    def keep(self, path: torch.Tensor, counts: torch.Tensor, lens_out: torch.Tensor | None = None):
+        """The sequences' lengths when the accepted rows alone are kept."""
+        return cache_keep(self.cache, self.batch, path, counts, lens_out)
 
 
 class SwigluFFN:
