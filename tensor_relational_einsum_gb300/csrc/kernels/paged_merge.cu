@@ -19,7 +19,8 @@ namespace {
 using namespace pg;
 
 constexpr int kWarps = 8;
-constexpr int kRowsPerCta = 32;  // a CTA without a cut costs too: not too many of them
+// Rows of a CTA: one a warp where items have 32 rows at most; 32 of more, because a CTA without a cut costs too.
+__host__ __device__ constexpr int rows_per_cta(int rows) { return rows <= 32 ? kWarps : 32; }
 
 template <int D>
 __device__ __forceinline__ void load_acc(const float *src, int lane, float *v) {
@@ -115,7 +116,7 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
     const PgCut c = w.cut[x];
     if (c.we == 0 || pg_first(c.total, c.parts, x - 1) > c.wi) return;  // not cut here, or merged by an earlier cut
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int r0 = group * kRowsPerCta, r1 = min(c.rows, r0 + kRowsPerCta);
+    const int r0 = group * rows_per_cta(rows), r1 = min(c.rows, r0 + rows_per_cta(rows));
     if (r0 >= r1) return;
     // parts: the last of CTA x - 1 (its only one if the item begins with it), then the first of x, x + 1, ...
     const int slot0 = 2 * (x - 1) + (pg_first(c.total, c.parts, x - 1) < c.wi ? 1 : 0);
@@ -129,35 +130,43 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
         else merge_few<D, 4>(p, w, c, n0, n1, step, r0 + 2 * warp, r1, lane);
         return;
     }
-    // many parts, eight at a time; with few rows several warps share a row's parts
+    // many parts, eight at a time; with few rows several warps share a row's parts.  Lane i holds part i's maximum and sum
+    // (of the first 32, the others are read where they are used); the first outputs are asked for along with them.
     const int left = r1 - r0, share = left <= 1 ? 8 : left <= 2 ? 4 : left <= 4 ? 2 : 1, sub = warp % share;
     for (int row0 = r0; row0 < r1; row0 += kWarps / share) {
         const int row = row0 + warp / share;
         const bool in = row < r1;
-        float m = -INFINITY;
-        for (int i = lane; in && i < count; i += 32) m = fmaxf(m, __ldcg(&w.ml[at(i, row)]).x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float base = m == -INFINITY ? 0.f : m;
-        float l = 0.f, a[C] = {};
-        for (int i0 = sub; in && i0 < count; i0 += 8 * share) {
-            float2 ml[8];
-            float v[8][C];
+        float v[8][C];
+        auto load = [&](int i0) {
 #pragma unroll
             for (int y = 0; y < 8; y++) {
                 const int i = i0 + y * share;
-                ml[y] = make_float2(-INFINITY, 0.f);
 #pragma unroll
                 for (int k = 0; k < C; k++) v[y][k] = 0.f;
-                if (i < count) {
-                    ml[y] = __ldcg(&w.ml[at(i, row)]);
-                    load_acc<D>(w.acc + at(i, row) * D, lane, v[y]);
-                }
+                if (in && i < count) load_acc<D>(w.acc + at(i, row) * D, lane, v[y]);
             }
+        };
+        load(sub);
+        const float2 mine = in && lane < count ? __ldcg(&w.ml[at(lane, row)]) : make_float2(-INFINITY, 0.f);
+        float m = mine.x;
+        for (int i = lane + 32; in && i < count; i += 32) m = fmaxf(m, __ldcg(&w.ml[at(i, row)]).x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float base = m == -INFINITY ? 0.f : m;
+        const float weight = attn::ex2((mine.x - base) * p.scale_log2);
+        float l = 0.f, a[C] = {};
+        for (int i0 = sub; i0 < count; i0 += 8 * share) {
+            if (i0 != sub) load(i0);
 #pragma unroll
             for (int y = 0; y < 8; y++) {
-                const float f = attn::ex2((ml[y].x - base) * p.scale_log2);
-                l = fmaf(f, ml[y].y, l);
+                const int i = i0 + y * share;
+                float f = __shfl_sync(0xffffffffu, weight, i & 31), sum = __shfl_sync(0xffffffffu, mine.y, i & 31);
+                if (i >= 32) {
+                    const float2 ml = in && i < count ? __ldcg(&w.ml[at(i, row)]) : make_float2(-INFINITY, 0.f);
+                    f = attn::ex2((ml.x - base) * p.scale_log2);
+                    sum = ml.y;
+                }
+                l = fmaf(f, sum, l);
 #pragma unroll
                 for (int k = 0; k < C; k++) a[k] = fmaf(f, v[y][k], a[k]);
             }
@@ -182,7 +191,7 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
 
 cudaError_t launch_cache_merge(const PgAttn &p, const PgMerge &m, cudaStream_t st) {
     PgMerge g = m;
-    for (int k = 0; k < 2; k++) g.groups[k] = std::max(1, (m.rows[k] + kRowsPerCta - 1) / kRowsPerCta);
+    for (int k = 0; k < 2; k++) g.groups[k] = std::max(1, (m.rows[k] + rows_per_cta(m.rows[k]) - 1) / rows_per_cta(m.rows[k]));
     const dim3 grid(g.cuts[0] * g.groups[0] + g.cuts[1] * g.groups[1]);
     if (p.c.dim == 64) return launch_after(cache_merge_kernel<64>, grid, 32 * kWarps, 0, st, true, p, g);
     return launch_after(cache_merge_kernel<128>, grid, 32 * kWarps, 0, st, true, p, g);
