@@ -601,8 +601,9 @@ typedef struct {
  *   target  f32 or bf16 [rows.., vocab]: values in [0, 1] (others are taken as
  *           0 or 1, NaN as 0), a row's sum below 2;
  *   draft   as target, or NULL: the drafted tokens are certain (probability 1).
- * Tests and sums are exact to 2^-53 and to 2^-61 an entry; sums do not depend
- * on their order: the results are the same on every run.  Of `batch` only
+ * Tests, and rests and sums relative to their largest terms, are exact to
+ * about 2^-45 (what lies below 2^-61 counts as 0); the results are the same on
+ * every run.  Of `batch` only
  * starts, n_seqs and max_new are read; at most 128 nodes a sequence.
  * Errors: EA_ERR_ARG, EA_ERR_SHAPE, EA_ERR_PARTITION, EA_ERR_DTYPE,
  * EA_ERR_UNSUPPORTED (trees, vocabulary). */

@@ -17,10 +17,12 @@
 //     for all: no CTA can wait for one that took another turn);
 //   - r is not kept: it follows from the target's and the draft's rows and the
 //     masses so far, and is made again where it is needed;
-//   - sums are integers in units of 2^-62: they do not depend on their order,
-//     so the running sums agree with the totals exactly, whatever the split.
+//   - a thread's sum is a pair of floats, each addition's error kept (7
+//     instructions where a fixed-point sum takes 13 and the conversion to 64
+//     bits is slower still); its total, and all sums of threads, are integers
+//     in units of 2^-62, which do not depend on their order.
 // Probabilities lie in [0, 1] (others are taken as 0 or 1) and a row's sum
-// below 4.
+// below 2.
 #include <cuda_bf16.h>
 
 #include "../drafts.h"
@@ -35,14 +37,18 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;            // the most CTAs of a sequence
 constexpr int kRuns = kCluster * kWarps;
+constexpr int kAhead = 4;              // vectors of a lane in flight
+constexpr int kResident = 4;           // CTAs of an SM
+static_assert(kRuns == 64, "a lane holds two runs' sums");
 constexpr double kUnit = 1.0 / 4611686018427387904.0;  // 2^-62
 
-// x in [0, 1] in units of 2^-62 (below 2^-39: rounded down).
-__device__ __forceinline__ uint64_t fixed(float x) {
-    const uint32_t b = __float_as_uint(fminf(fmaxf(x, 0.f), 1.f));  // NaN: 0
-    const int s = (int)(b >> 23) - 88;
+// x (|x| < 2) in units of 2^-62, below 2^-39 rounded towards 0.
+__device__ __forceinline__ int64_t fixed(float x) {
+    const uint32_t b = __float_as_uint(x);
+    const int s = (int)(b >> 23 & 255) - 88;
     const uint32_t m = (b & 0x7fffffu) | 0x800000u;
-    return s >= 0 ? (uint64_t)m << s : (uint64_t)(m >> min(31, -s));
+    const int64_t v = s >= 0 ? (int64_t)m << s : (int64_t)(m >> min(31, -s));
+    return (int)b < 0 ? -v : v;
 }
 // The product of two such numbers, rounded down.
 __device__ __forceinline__ uint64_t times(uint64_t a, uint64_t b) { return __umul64hi(a << 1, b << 1); }
@@ -63,12 +69,41 @@ __device__ __forceinline__ void put_u32(uint32_t at, uint32_t x) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
 }
 
+// Inclusive sums over the lanes.
+__device__ __forceinline__ uint64_t scan(uint64_t x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+// A number as the sum of two floats, the second below half a step of the first.
+struct alignas(8) Pair {
+    float h, l;
+};
+__device__ __forceinline__ Pair pair_of(uint64_t x) {  // units of 2^-62
+    const double d = (double)x * kUnit;
+    const float h = (float)d;
+    return Pair{h, (float)(d - (double)h)};
+}
+__device__ __forceinline__ uint64_t fixed(const Pair &x) { return (uint64_t)max((int64_t)0, fixed(x.h) + fixed(x.l)); }
+// s += x: the exact error of the first parts' sum goes to the second.
+__device__ __forceinline__ void add_to(Pair &s, const Pair &x) {
+    const float t = __fadd_rn(s.h, x.h), y = __fsub_rn(t, s.h);
+    s.l += __fadd_rn(__fsub_rn(s.h, __fsub_rn(t, y)), __fsub_rn(x.h, y)) + x.l;
+    s.h = t;
+}
+
 struct Order {                  // what the first CTA asks of all
     int node;                   // -1: nothing more
     int first;                  // the sequence's first dense row
     int rejected;               // subtractions from the target's row (with a draft)
-    uint64_t mass[kPgNodes];    // Z before each of them; the first is 1
+    Pair mass[kPgNodes];        // (8 bytes each, and aligned so) Z before each of them; the first is 1
 };
+
+static_assert(sizeof(Pair) == 8 && alignof(Order) == 8 && offsetof(Order, mass) % 8 == 0, "masses go to other CTAs as 64 bits");
 
 // A row of probabilities as 16-byte vectors from the aligned address at or
 // before its first element; `skip` elements lie before it.
@@ -85,22 +120,27 @@ struct Row {
         end = skip + vocab;
         vectors = (end + VE - 1) / VE;
     }
-    __device__ __forceinline__ void load(int64_t v, float *x) const {
-        if ((v > 0 || skip == 0) && (v + 1) * VE <= end) {
-            const uint4 u = __ldg(at + v);
-            if constexpr (BF16) {
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    // Whole vectors of the row: [first_whole, last_whole).
+    __device__ __forceinline__ int64_t first_whole() const { return skip > 0; }
+    __device__ __forceinline__ int64_t last_whole() const { return end / VE; }
+    static __device__ __forceinline__ void values(const uint4 &u, float *x) {
+        if constexpr (BF16) {
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    x[2 * i] = __uint_as_float(w[i] << 16);
-                    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-                }
-            } else {
-                x[0] = __uint_as_float(u.x);
-                x[1] = __uint_as_float(u.y);
-                x[2] = __uint_as_float(u.z);
-                x[3] = __uint_as_float(u.w);
+            for (int i = 0; i < 4; i++) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
             }
+        } else {
+            x[0] = __uint_as_float(u.x);
+            x[1] = __uint_as_float(u.y);
+            x[2] = __uint_as_float(u.z);
+            x[3] = __uint_as_float(u.w);
+        }
+    }
+    __device__ __forceinline__ void load(int64_t v, float *x) const {
+        if (v >= first_whole() && v < last_whole()) {
+            values(__ldg(at + v), x);
         } else {
 #pragma unroll
             for (int i = 0; i < VE; i++) {
@@ -114,22 +154,30 @@ struct Row {
     }
 };
 
-// r at one token.
-__device__ __forceinline__ uint64_t rest_of(float t, float d, const Order &o) {
-    uint64_t r = fixed(t);
+// r at one token, from the target's and the draft's probabilities.
+__device__ __forceinline__ Pair rest_of(float t, float d, const Order &o) {
+    Pair r{__saturatef(t), 0.f};  // NaN: 0
     if (o.rejected > 0) {
-        const uint64_t q = fixed(d);
-        r = r > q ? r - q : 0;
+        const float q = __saturatef(d);
+        const float h = __fsub_rn(r.h, q);
+        r = h > 0.f ? Pair{h, __fsub_rn(__fsub_rn(r.h, h), q)} : Pair{0.f, 0.f};  // exact: the larger first
         for (int k = 1; k < o.rejected; k++) {
-            const uint64_t x = times(o.mass[k], q);
-            r = r > x ? r - x : 0;
+            const Pair z = o.mass[k];
+            const float ph = __fmul_rn(z.h, q), pl = fmaf(z.h, q, -ph) + __fmul_rn(z.l, q);
+            const float e = __fsub_rn(r.h, ph);
+            if (!(e >= 0.f)) {
+                r = Pair{0.f, 0.f};
+                continue;
+            }
+            const float l = __fadd_rn(__fsub_rn(__fsub_rn(r.h, e), ph), __fsub_rn(r.l, pl)), g = __fadd_rn(e, l);
+            r = g > 0.f ? Pair{g, __fsub_rn(l, __fsub_rn(g, e))} : Pair{0.f, 0.f};
         }
     }
     return r;
 }
 
 template <bool BF16, bool DRAFT>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VfParams p) {
+__global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __grid_constant__ VfParams p) {
     using R = Row<BF16>;
     __shared__ Order s_order;
     __shared__ uint64_t s_runs[kRuns];          // of the first CTA: the runs' sums
@@ -140,7 +188,9 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
     const int seq = blockIdx.x / ctas, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     PgSeq s{};
+    float sample = 0.f;
     if (rank == 0) {
+        sample = __ldg(p.sample + seq);
         if (!pg_seq(__ldg(p.starts + seq), __ldg(p.starts + seq + 1), 0, p.rows, p.max_new, 0, &s) && threadIdx.x == 0) batch_fail(p.err);
         const int j = threadIdx.x;
         if (j < s.n) {
@@ -158,8 +208,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             s_t[j] = s_d[j] = 0.f;
             if (up >= 0) {
                 const int64_t at = (int64_t)(s.first + up) * p.vocab + token;
-                s_t[j] = ld_elem(p.target, BF16 ? EA_BF16 : EA_F32, at);
-                if constexpr (DRAFT) s_d[j] = ld_elem(p.draft, BF16 ? EA_BF16 : EA_F32, at);
+                s_t[j] = __saturatef(ld_elem(p.target, BF16 ? EA_BF16 : EA_F32, at));
+                if constexpr (DRAFT) s_d[j] = __saturatef(ld_elem(p.draft, BF16 ? EA_BF16 : EA_F32, at));
             }
         }
         __syncthreads();
@@ -181,7 +231,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
                     yes = u * (double)s_d[next] < (double)s_t[next];
                 } else {
                     s_order.rejected = rejected;
-                    yes = u * (double)s_d[next] * ((double)mass * kUnit) < (double)rest_of(s_t[next], s_d[next], s_order) * kUnit;
+                    const Pair r = rest_of(s_t[next], s_d[next], s_order);
+                    yes = u * (double)s_d[next] * ((double)mass * kUnit) < (double)r.h + (double)r.l;
                 }
             } else {
                 for (int i = 0; i < outs; i++) out |= s_out[i] == s_token[next];
@@ -193,13 +244,13 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
                 rejected = outs = 0;
                 have = false;
             } else if constexpr (DRAFT) {
-                s_order.mass[rejected++] = mass;
+                s_order.mass[rejected++] = pair_of(mass);
                 have = false;
             } else {
                 rejected++;
                 if (!out) {
                     s_out[outs++] = s_token[next];
-                    if (have) mass -= min(mass, fixed(s_t[next]));
+                    if (have) mass -= min(mass, (uint64_t)fixed(s_t[next]));
                 }
             }
         }
@@ -223,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
                 put_u32(shared_of(&s_order.node, c), (uint32_t)s_order.node);
                 put_u32(shared_of(&s_order.first, c), (uint32_t)s.first);
                 put_u32(shared_of(&s_order.rejected, c), (uint32_t)rejected);
-                for (int k = 1; more && k < rejected && DRAFT; k++) put_u64(shared_of(&s_order.mass[k], c), s_order.mass[k]);
+                for (int k = 1; more && k < rejected && DRAFT; k++) put_u64(shared_of(&s_order.mass[k], c), *reinterpret_cast<const uint64_t *>(&s_order.mass[k]));
             }
         }
         __syncwarp();
@@ -232,23 +283,55 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         const R t(p.target, s_order.first + s_order.node, p.vocab), d(DRAFT ? p.draft : p.target, s_order.first + s_order.node, p.vocab);
         const int64_t each = (t.vectors + ctas * kWarps - 1) / (ctas * kWarps);
         const int64_t v0 = (rank * kWarps + warp) * each, v1 = min(v0 + each, t.vectors);
-        uint64_t sum = 0;
+        Pair part{0.f, 0.f};
         const bool both = DRAFT && s_order.rejected > 0;
-        for (int64_t v = v0 + lane; v < v1; v += 32) {
-            float a[R::VE], b[R::VE];
-            t.load(v, a);
-            if (both) d.load(v, b);
+        auto add = [&](const float *a, const float *b) {
 #pragma unroll
-            for (int i = 0; i < R::VE; i++) sum += DRAFT ? rest_of(a[i], both ? b[i] : 0.f, s_order) : fixed(a[i]);
+            for (int i = 0; i < R::VE; i++) add_to(part, DRAFT ? rest_of(a[i], b[i], s_order) : Pair{__saturatef(a[i]), 0.f});
+        };
+        // whole vectors, several of a lane in flight
+        const int64_t w0 = max(v0, t.first_whole()), w1 = min(v1, t.last_whole());
+        for (int64_t v = w0 + lane; v < w1; v += 32 * kAhead) {
+            uint4 a[kAhead], b[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; k++) {
+                const bool in = v + 32 * k < w1;
+                a[k] = b[k] = make_uint4(0, 0, 0, 0);
+                if (in) a[k] = __ldg(t.at + v + 32 * k);
+                if (in && both) b[k] = __ldg(d.at + v + 32 * k);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; k++) {
+                float x[R::VE], y[R::VE];
+                R::values(a[k], x);
+                R::values(b[k], y);
+                add(x, y);
+            }
         }
+        // the row's ends: the first vector (lane 0) and the last (lane 1), where they are not whole
+        if (lane == 0 || (lane == 1 && t.vectors > 1)) {
+            const int64_t v = lane == 0 ? 0 : t.vectors - 1;
+            if (v >= v0 && v < v1 && (v < w0 || v >= w1)) {
+                float x[R::VE], y[R::VE];
+                t.load(v, x);
+#pragma unroll
+                for (int i = 0; i < R::VE; i++) y[i] = 0.f;
+                if (both) d.load(v, y);
+                add(x, y);
+            }
+        }
+        __syncwarp();
+        uint64_t sum = fixed(part);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) put_u64(shared_of(&s_runs[rank * kWarps + warp], 0), sum);
         __syncwarp();
         cluster_sync();
-        if (rank == 0 && threadIdx.x == 0) {
-            total = 0;
-            for (int i = 0; i < (int)ctas * kWarps; i++) total += s_runs[i];
+        if (rank == 0 && warp == 0) {
+            const int runs = ctas * kWarps;
+            total = (2 * lane < runs ? s_runs[2 * lane] : 0) + (2 * lane + 1 < runs ? s_runs[2 * lane + 1] : 0);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
             mass = total;
             if constexpr (!DRAFT) {
                 for (int j = 1; j < next; j++) {
@@ -256,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
                     if (s_up[j] != node) continue;
                     bool again = false;
                     for (int i = 1; i < j; i++) again |= s_up[i] == node && s_token[i] == s_token[j];
-                    if (!again) mass -= min(mass, fixed(s_t[j]));
+                    if (!again) mass -= min(mass, (uint64_t)fixed(s_t[j]));
                 }
             }
             have = true;
@@ -265,7 +348,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     if (rank != 0) return;
     // ---- the first CTA: the path, and the next token
     __shared__ int s_kept, s_node, s_outs;
-    __shared__ uint64_t s_mass;
+    __shared__ uint64_t s_mass, s_warps[kWarps];
     if (threadIdx.x == 0) {
         s_kept = s.n > 0 ? kept : 0;
         s_node = node;
@@ -277,28 +360,26 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         if constexpr (!DRAFT) {  // runs without the tokens that were rejected
             const R t(p.target, s.first + node, p.vocab);
             const int64_t each = (t.vectors + ctas * kWarps - 1) / (ctas * kWarps);
-            for (int i = 0; i < outs; i++)
-                s_runs[(t.skip + s_out[i]) / R::VE / each] -= fixed(ld_elem(p.target, BF16 ? EA_BF16 : EA_F32, (int64_t)(s.first + node) * p.vocab + s_out[i]));
+            for (int i = 0; i < outs; i++) {
+                uint64_t &run = s_runs[(t.skip + s_out[i]) / R::VE / each];
+                run -= min(run, (uint64_t)fixed(__saturatef(ld_elem(p.target, BF16 ? EA_BF16 : EA_F32, (int64_t)(s.first + node) * p.vocab + s_out[i]))));
+            }
         }
     }
     __syncthreads();
     for (int j = threadIdx.x; j < p.width; j += kThreads) p.path[(int64_t)seq * p.width + j] = j < s_kept ? s_path[j] : -1;
-    if (warp != 0 || s.n == 0 || s_mass == 0) return;
+    if (s.n == 0 || s_mass == 0) return;
     const R t(p.target, s.first + s_node, p.vocab), d(DRAFT ? p.draft : p.target, s.first + s_node, p.vocab);
     const int64_t each = (t.vectors + ctas * kWarps - 1) / (ctas * kWarps);
-    uint64_t left = min(times(fixed(__ldg(p.sample + seq)), s_mass), s_mass - 1);  // the running sum to exceed
-    // the run that holds it
+    // the run that holds the running sum to exceed
+    uint64_t left;
     int run = 0;
     {
         const int runs = ctas * kWarps;
         const uint64_t a = 2 * lane < runs ? s_runs[2 * lane] : 0, b = 2 * lane + 1 < runs ? s_runs[2 * lane + 1] : 0;
-        uint64_t incl = a + b;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-        }
-        const int l = max(0, __ffs((int)__ballot_sync(0xffffffffu, left < incl)) - 1);  // incl of the last is the mass
+        const uint64_t incl = scan(a + b, lane), all = __shfl_sync(0xffffffffu, incl, 31);
+        left = min(times((uint64_t)fixed(__saturatef(sample)), all), all - 1);
+        const int l = max(0, __ffs((int)__ballot_sync(0xffffffffu, left < incl)) - 1);
         const uint64_t before = __shfl_sync(0xffffffffu, incl - a - b, l), first = __shfl_sync(0xffffffffu, a, l);
         left -= before;
         run = 2 * l;
@@ -307,48 +388,51 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             run++;
         }
     }
-    const int64_t v0 = run * each, v1 = min(v0 + each, t.vectors);
-    for (int64_t v = v0; v < v1; v += 32) {
-        float a[R::VE], b[R::VE];
-        uint64_t r[R::VE], mine = 0;
+    // a few neighbouring vectors of it a thread, whose sums say which thread has the token
+    const int64_t mine = (each + kThreads - 1) / kThreads, v0 = run * each + threadIdx.x * mine, v1 = min(min(v0 + mine, (run + 1) * each), t.vectors);
+    // f(r, token) of the thread's tokens in order, until it says so
+    auto tokens = [&](auto f) {
+        for (int64_t v = v0; v < v1; v++) {
+            float a[R::VE], b[R::VE];
+            t.load(v, a);
 #pragma unroll
-        for (int i = 0; i < R::VE; i++) a[i] = b[i] = 0.f;
-        if (v + lane < v1) {
-            t.load(v + lane, a);
-            if (DRAFT && s_order.rejected > 0) d.load(v + lane, b);
-        }
+            for (int i = 0; i < R::VE; i++) b[i] = 0.f;
+            if (DRAFT && s_order.rejected > 0) d.load(v, b);
 #pragma unroll
-        for (int i = 0; i < R::VE; i++) {
-            r[i] = DRAFT ? rest_of(a[i], b[i], s_order) : fixed(a[i]);
-            if constexpr (!DRAFT) {
-                const int64_t x = (v + lane) * R::VE + i - t.skip;
-                for (int k = 0; k < s_outs; k++)
-                    if (s_out[k] == x) r[i] = 0;
+            for (int i = 0; i < R::VE; i++) {
+                const int64_t x = v * R::VE + i - t.skip;
+                uint64_t r = fixed(DRAFT ? rest_of(a[i], b[i], s_order) : Pair{__saturatef(a[i]), 0.f});
+                if constexpr (!DRAFT)
+                    for (int k = 0; k < s_outs; k++)
+                        if (s_out[k] == x) r = 0;
+                if (r > 0 && f(r, (int)x)) return;
             }
-            mine += r[i];
         }
-        uint64_t incl = mine;
+    };
+    uint64_t sum = 0;
+    tokens([&](uint64_t r, int) {
+        sum += r;
+        return false;
+    });
+    uint64_t incl = scan(sum, lane);
+    if (lane == 31) s_warps[warp] = incl;
+    __syncthreads();
+    uint64_t all = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-        }
-        const uint32_t found = __ballot_sync(0xffffffffu, left < incl);
-        if (found) {
-            if (lane == __ffs((int)found) - 1) {
-                uint64_t at = incl - mine;
-                int i = 0;
-#pragma unroll
-                for (int k = 0; k < R::VE - 1; k++)
-                    if (i == k && left >= at + r[k]) {
-                        at += r[k];
-                        i = k + 1;
-                    }
-                p.picked[seq] = (int32_t)((v + lane) * R::VE + i - t.skip);
-            }
-            return;
-        }
-        left -= __shfl_sync(0xffffffffu, incl, 31);
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp) incl += s_warps[w];
+        all += s_warps[w];
+    }
+    // The run's sum was made of pairs of floats, in other groups: it can be larger than this one in the last places.
+    left = min(left, all - 1);
+    if (all == 0 && threadIdx.x == 0) p.picked[seq] = -1;
+    if (left >= incl - sum && left < incl) {
+        uint64_t at = incl - sum;
+        tokens([&](uint64_t r, int x) {
+            at += r;
+            if (left < at) p.picked[seq] = x;
+            return left < at;
+        });
     }
 }
 
@@ -371,7 +455,7 @@ cudaError_t launch(const VfParams &p, int ctas, cudaStream_t st) {
 
 cudaError_t launch_verify(const VfParams &p, int num_sms, int64_t *ctas, cudaStream_t st) {
     int c = kCluster;
-    while (c > 1 && ((int64_t)p.n_seqs * c > 4 * num_sms || p.vocab < 2048 * c)) c /= 2;
+    while (c > 1 && ((int64_t)p.n_seqs * c > kResident * num_sms || p.vocab < 2048 * c)) c /= 2;
     *ctas = (int64_t)p.n_seqs * c;
     if (p.bf16) return p.draft ? launch<true, true>(p, c, st) : launch<true, false>(p, c, st);
     return p.draft ? launch<false, true>(p, c, st) : launch<false, false>(p, c, st);
