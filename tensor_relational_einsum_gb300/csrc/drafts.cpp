@@ -237,7 +237,7 @@ extern "C" ea_status ea_cache_keep(const ea_cache *caches, int32_t n_caches, con
                 p.vs[j] = caches[i + j]->vs;
             }
             int64_t ctas = 0;
-            cudaError_t e = launch_cache_keep(p, &ctas, (cudaStream_t)stream);
+            cudaError_t e = launch_cache_keep(p, f->num_sms, &ctas, (cudaStream_t)stream);
             if (e != cudaSuccess) return cuda_error(e, what);
             all += ctas;
             launches++;

@@ -44,13 +44,13 @@ struct KpParams {
     PgTable t;
     int64_t n_pages;
     int32_t page_log2, heads, row_bytes;  // row_bytes: of a vector's cells
-    int32_t n_caches, width;
+    int32_t n_caches, width, each;        // each: caches of a CTA (set by the launch)
     const int32_t *path, *counts;
     int32_t *lens_out;
     int *err;
     char *k[kKeepCaches], *v[kKeepCaches];
     uint8_t *ks[kKeepCaches], *vs[kKeepCaches];
 };
-cudaError_t launch_cache_keep(const KpParams &p, int64_t *ctas, cudaStream_t st);
+cudaError_t launch_cache_keep(const KpParams &p, int num_sms, int64_t *ctas, cudaStream_t st);
 
 }  // namespace ea

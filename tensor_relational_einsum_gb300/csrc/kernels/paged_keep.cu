@@ -19,7 +19,8 @@ constexpr int kBatch = 8;
 __global__ void __launch_bounds__(kThreads) cache_keep_kernel(const __grid_constant__ KpParams p) {
     __shared__ int64_t s_from[kPgNodes], s_to[kPgNodes];  // slots of head 0
     __shared__ int s_moves, s_bad;
-    const int seq = blockIdx.x, cache = blockIdx.y, lg = p.page_log2;
+    const int seq = blockIdx.x, lg = p.page_log2;
+    const int cache0 = blockIdx.y * p.each, caches = min(p.each, p.n_caches - cache0);
     if (threadIdx.x == 0) s_moves = s_bad = 0;
     __syncthreads();
     const PgSeq s = load_seq(p.t, seq, p.err);
@@ -50,40 +51,54 @@ __global__ void __launch_bounds__(kThreads) cache_keep_kernel(const __grid_const
     if (s_bad) {
         if (threadIdx.x == 0) {
             batch_fail(p.err);
-            if (p.lens_out && cache == 0) p.lens_out[seq] = s.len;
+            if (p.lens_out && cache0 == 0) p.lens_out[seq] = s.len;
         }
         return;
     }
-    if (p.lens_out && cache == 0 && threadIdx.x == 0) p.lens_out[seq] = base + count;
+    if (p.lens_out && cache0 == 0 && threadIdx.x == 0) p.lens_out[seq] = base + count;
     const int moves = s_moves;
     if (moves == 0) return;
+    // 16 bytes of every moved vector a thread: of a cache's K and V, head after head
     const int chunks = p.row_bytes / 16, cells = 2 * p.heads * chunks;
-    for (int c = threadIdx.x; c < cells; c += kThreads) {
-        const int w = c >= cells / 2, hc = w ? c - cells / 2 : c, head = hc / chunks;
-        char *pool = w ? p.v[cache] : p.k[cache];
+    for (int c = threadIdx.x; c < caches * cells; c += kThreads) {
+        const int x = c / cells, y = c - x * cells, w = y >= cells / 2, hc = w ? y - cells / 2 : y, head = hc / chunks;
+        char *pool = w ? p.v[cache0 + x] : p.k[cache0 + x];
         const int64_t off = ((int64_t)head << lg) * p.row_bytes + (hc - head * chunks) * 16;
         for (int j0 = 0; j0 < moves; j0 += kBatch) {
-            uint4 x[kBatch];
+            uint4 v[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; i++)
-                if (j0 + i < moves) x[i] = *reinterpret_cast<const uint4 *>(pool + s_from[j0 + i] * p.row_bytes + off);
+                if (j0 + i < moves) v[i] = *reinterpret_cast<const uint4 *>(pool + s_from[j0 + i] * p.row_bytes + off);
 #pragma unroll
             for (int i = 0; i < kBatch; i++)
-                if (j0 + i < moves) *reinterpret_cast<uint4 *>(pool + s_to[j0 + i] * p.row_bytes + off) = x[i];
+                if (j0 + i < moves && s_from[j0 + i] != s_to[j0 + i])
+                    *reinterpret_cast<uint4 *>(pool + s_to[j0 + i] * p.row_bytes + off) = v[i];
         }
     }
-    if (!p.ks[cache]) return;
-    for (int c = threadIdx.x; c < 2 * p.heads; c += kThreads) {
-        const int w = c >= p.heads, head = w ? c - p.heads : c;
-        uint8_t *pool = (w ? p.vs[cache] : p.ks[cache]) + ((int64_t)head << lg);
-        for (int j = 0; j < moves; j++) pool[s_to[j]] = pool[s_from[j]];
+    if (!p.ks[0]) return;
+    for (int c = threadIdx.x; c < caches * 2 * p.heads; c += kThreads) {
+        const int x = c / (2 * p.heads), y = c - x * 2 * p.heads, w = y >= p.heads, head = w ? y - p.heads : y;
+        uint8_t *pool = (w ? p.vs[cache0 + x] : p.ks[cache0 + x]) + ((int64_t)head << lg);
+        for (int j0 = 0; j0 < moves; j0 += kBatch) {
+            uint8_t v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; i++)
+                if (j0 + i < moves) v[i] = pool[s_from[j0 + i]];
+#pragma unroll
+            for (int i = 0; i < kBatch; i++)
+                if (j0 + i < moves) pool[s_to[j0 + i]] = v[i];
+        }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_cache_keep(const KpParams &p, int64_t *ctas, cudaStream_t st) {
-    const dim3 grid((unsigned)p.t.n_seqs, (unsigned)p.n_caches);
+cudaError_t launch_cache_keep(const KpParams &params, int num_sms, int64_t *ctas, cudaStream_t st) {
+    KpParams p = params;
+    // one look-up of the positions for several caches, as soon as the CTAs would not all be resident (8 on an SM)
+    p.each = 1;
+    while (p.each < p.n_caches && (int64_t)p.t.n_seqs * ((p.n_caches + p.each - 1) / p.each) > 8 * num_sms) p.each++;
+    const dim3 grid((unsigned)p.t.n_seqs, (unsigned)((p.n_caches + p.each - 1) / p.each));
     *ctas = (int64_t)grid.x * grid.y;
     cache_keep_kernel<<<grid, kThreads, 0, st>>>(p);
     return cudaGetLastError();
