@@ -27,10 +27,11 @@ using namespace pg;
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 16;    // rows of a CTA
 constexpr int kStaged = 1024;   // sequence bounds staged in shared memory
-constexpr int kAhead = 4;       // items in flight of a thread
+constexpr int kItems = 4;       // units that a thread takes, about
 
-// Position of dense row r; -1: the row is left as it is.
-__device__ __forceinline__ int position_of(const RoParams &p, const int32_t *starts, const int32_t *lens, int64_t r) {
+// Position of dense row r; -1: the row is left as it is.  parents: those of rows from `from` on.
+__device__ __forceinline__ int position_of(const RoParams &p, const int32_t *starts, const int32_t *lens, const int32_t *parents,
+                                           int64_t from, int64_t r) {
     if (p.positions) return __ldg(p.positions + r);
     if (r < starts[0] || r >= starts[p.n_seqs]) return -1;
     int a = 0, b = p.n_seqs - 1;  // the last i with starts[i] <= r
@@ -44,8 +45,12 @@ __device__ __forceinline__ int position_of(const RoParams &p, const int32_t *sta
     int at = (int)(r - s.first);
     if (p.parents) {
         int depth = 0;
+        if (at >= kPgNodes) {  // more nodes than max_new says: the sequence has been refused above
+            batch_fail(p.err);
+            return -1;
+        }
         for (int b = at;; depth++) {  // parents lie before their children: this ends
-            const int up = __ldg(p.parents + s.first + b);
+            const int up = parents[s.first + b - from];
             if (up >= b || up < -1) {
                 batch_fail(p.err);
                 return -1;
@@ -79,113 +84,157 @@ __device__ __forceinline__ void put(void *raw, int i, float x) {
     else reinterpret_cast<__nv_bfloat16 *>(raw)[i] = __float2bfloat16_rn(x);
 }
 
-// A unit is V pairs: two accesses of V columns (HALF, or a single pair, whose
-// columns need not lie on a boundary of two), or one of 2 V.
+// The widest access that all addresses are aligned to holds V pairs (half
+// layout: V first columns, and V second ones; else 2 V columns; a single pair
+// is always two accesses, as its columns need not lie on a boundary of two).
+// Such a run of V pairs is short where V is, and what a thread does besides
+// would weigh more than its values: so a unit is G runs, T apart (T units a
+// head, so that neighbouring threads stay neighbours in memory).  Where
+// results go elsewhere, other units copy the columns that are not rotated.
 template <bool F32, bool HALF, int V>
 struct Unit {
     static constexpr int ES = F32 ? 4 : 2;
     static constexpr bool TWO = HALF || V == 1;
-    static constexpr int COLUMNS = HALF ? V : 2 * V;    // from one unit to the next
-    static constexpr int BYTES = (TWO ? V : 2 * V) * ES;
-    Raw<BYTES> a[TWO ? 2 : 1];
+    static constexpr int RUN = TWO ? V : 2 * V;         // columns of an access
+    static constexpr int BYTES = RUN * ES;
+    // 32 bytes a unit; two runs where an access is narrower (four measured the same, eight a half slower)
+    static constexpr int G = BYTES >= 8 ? 32 / BYTES / (TWO ? 2 : 1) : 2;
+    static constexpr int N = TWO ? 2 * G : G;           // accesses
+    Raw<BYTES> a[N];
+    int off[N];                                         // byte offsets in a head; -1: none
 
-    __device__ __forceinline__ void load(const char *at, int64_t second) {
-        a[0] = *reinterpret_cast<const Raw<BYTES> *>(at);
-        if constexpr (TWO) a[1] = *reinterpret_cast<const Raw<BYTES> *>(at + second);
-    }
-    __device__ __forceinline__ void store(char *at, int64_t second) const {
-        *reinterpret_cast<Raw<BYTES> *>(at) = a[0];
-        if constexpr (TWO) *reinterpret_cast<Raw<BYTES> *>(at + second) = a[1];
-    }
-    __device__ __forceinline__ void turn(const float2 *cs) {
+    __device__ __forceinline__ void load(const char *x) {
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            const float2 f = cs[i];
-            void *px = &a[0], *py = &a[TWO ? 1 : 0];
-            const int ix = TWO ? i : 2 * i, iy = TWO ? i : 2 * i + 1;
-            const float x = get<F32>(px, ix), y = get<F32>(py, iy);
-            put<F32>(px, ix, x * f.x - y * f.y);
-            put<F32>(py, iy, x * f.y + y * f.x);
+        for (int n = 0; n < N; n++)
+            if (off[n] >= 0) a[n] = *reinterpret_cast<const Raw<BYTES> *>(x + off[n]);
+    }
+    __device__ __forceinline__ void store(char *y) const {
+#pragma unroll
+        for (int n = 0; n < N; n++)
+            if (off[n] >= 0) *reinterpret_cast<Raw<BYTES> *>(y + off[n]) = a[n];
+    }
+    // cs: (cosine, sine) of the row's pairs, V > 1: two pairs of every run, then the next two; the unit's runs are
+    // run, run + step, ..
+    __device__ __forceinline__ void turn(const float2 *cs, int run, int step, int runs) {
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            if (G > 1 && off[TWO ? 2 * g : g] < 0) break;
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                float4 f;
+                if constexpr (V == 1) {
+                    const float2 c = cs[run + g * step];
+                    f = make_float4(c.x, c.y, 0.f, 0.f);
+                } else {
+                    f = reinterpret_cast<const float4 *>(cs)[(i / 2) * runs + run + g * step];
+                }
+#pragma unroll
+                for (int j = i; j < V && j < i + 2; j++) {
+                    const float c = j == i ? f.x : f.z, s = j == i ? f.y : f.w;
+                    void *px = &a[TWO ? 2 * g : g], *py = &a[TWO ? 2 * g + 1 : g];
+                    const int ix = TWO ? j : 2 * j, iy = TWO ? j : 2 * j + 1;
+                    const float x = get<F32>(px, ix), y = get<F32>(py, iy);
+                    put<F32>(px, ix, x * c - y * s);
+                    put<F32>(py, iy, x * s + y * c);
+                }
+            }
         }
     }
 };
 
+// Units of a head: those that rotate, then those that copy.
+template <class U, int V>
+__host__ __device__ __forceinline__ void units_of(const RoParams &p, int *turned, int *copied) {
+    const int rest = p.y[0] != p.x[0] ? (p.dim - p.dims) / U::RUN : 0;
+    *turned = (p.dims / 2 / V + U::G - 1) / U::G;
+    *copied = (rest + U::N - 1) / U::N;
+}
+
 template <bool F32, bool HALF, int V>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RoParams p, const int rows_cta) {
     using U = Unit<F32, HALF, V>;
-    extern __shared__ float2 s_cs[];          // [rows][pairs]: cosine and sine
+    extern __shared__ __align__(16) float2 s_cs[];
     __shared__ int32_t s_starts[kStaged + 1], s_lens[kStaged];
-    __shared__ int32_t s_pos[kMaxRows];
-    const int pairs = p.dims / 2, units = pairs / V, heads = p.heads[0] + p.heads[1];
+    __shared__ int32_t s_pos[kMaxRows], s_up[kPgNodes + kMaxRows];
+    const int pairs = p.dims / 2, runs = pairs / V, heads = p.heads[0] + p.heads[1];
+    int turned, copied;
+    units_of<U, V>(p, &turned, &copied);
     const int64_t row0 = (int64_t)blockIdx.x * rows_cta;
     const int rows = (int)min((int64_t)rows_cta, p.rows - row0);
-    const int unit = threadIdx.x % units, lanes = kThreads / units;  // units <= 128
-    const bool works = (int)threadIdx.x < lanes * units;
-    const int64_t second = (HALF ? pairs : 1) * U::ES;
-    const int column = p.offset + unit * U::COLUMNS;
-    int row = 0, head = threadIdx.x / units;  // of the next item to load
-    U u[kAhead];
-    int r[kAhead], h[kAhead];
-    auto place = [&](int rr, int hh) {
-        const int w = hh >= p.heads[0];
-        return (((row0 + rr) * p.heads[w] + (w ? hh - p.heads[0] : hh)) * p.dim + column) * U::ES;
-    };
-    auto fetch = [&]() {
+    U u;
+    char *to;
+    // a thread's unit, and where it lies in a head; a head with more units than threads takes several turns
+    int unit, lanes, row, head;
+    bool works;
+    auto take = [&](int unit0) {
+        const int n = min(kThreads, turned + copied - unit0);
+        unit = unit0 + threadIdx.x % n;
+        lanes = kThreads / n;
+        works = (int)threadIdx.x < lanes * n;
+        row = 0;
+        head = threadIdx.x / n;
 #pragma unroll
-        for (int i = 0; i < kAhead; i++) {
-            while (head >= heads) {
-                head -= heads;
-                row++;
+        for (int i = 0; i < U::N; i++) {
+            if (unit < turned) {
+                const int run = unit + (U::TWO ? i / 2 : i) * turned, col = p.offset + run * (HALF ? V : 2 * V);
+                u.off[i] = run < runs ? (col + (U::TWO && (i & 1) ? (HALF ? pairs : 1) : 0)) * U::ES : -1;
+            } else {
+                const int col = (unit - turned + i * copied) * U::RUN;
+                u.off[i] = col < p.dim - p.dims ? (col < p.offset ? col : col + p.dims) * U::ES : -1;
             }
-            r[i] = works && row < rows ? row : -1;
-            h[i] = head;
-            if (r[i] >= 0) u[i].load(p.x[head >= p.heads[0]] + place(row, head), second);
-            head += lanes;
         }
     };
-    fetch();
+    // The next item of the thread: false if there is none.
+    auto fetch = [&]() {
+        while (head >= heads) {
+            head -= heads;
+            row++;
+        }
+        if (!works || row >= rows) return false;
+        const int w = head >= p.heads[0];
+        const int64_t at = ((row0 + row) * p.heads[w] + (w ? head - p.heads[0] : head)) * p.dim * U::ES;
+        u.load(p.x[w] + at);
+        to = p.y[w] + at;
+        return true;
+    };
+    take(0);
+    bool any = fetch();
     const bool staged = !p.positions && p.n_seqs <= kStaged;
+    const int64_t from = max((int64_t)0, row0 - (kPgNodes - 1));  // a row's tree begins there at the earliest
+    if (p.parents && threadIdx.x < row0 + rows - from) s_up[threadIdx.x] = __ldg(p.parents + from + threadIdx.x);
     if (staged) {
         for (int i = threadIdx.x; i <= p.n_seqs; i += kThreads) {
             s_starts[i] = __ldg(p.starts + i);
             if (i < p.n_seqs) s_lens[i] = __ldg(p.lens + i);
         }
-        __syncthreads();
     }
+    if (staged || p.parents) __syncthreads();
     if ((int)threadIdx.x < rows)
-        s_pos[threadIdx.x] = position_of(p, staged ? s_starts : p.starts, staged ? s_lens : p.lens, row0 + threadIdx.x);
+        s_pos[threadIdx.x] = position_of(p, staged ? s_starts : p.starts, staged ? s_lens : p.lens, s_up, from, row0 + threadIdx.x);
     __syncthreads();
     for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
-        const int rr = i / pairs, pos = s_pos[rr];
+        const int rr = i / pairs, pair = i - rr * pairs, pos = s_pos[rr];
         if (pos < 0) continue;
-        const uint64_t turn = (uint64_t)pos * p.turn[i - rr * pairs];
+        const uint64_t turn = (uint64_t)pos * p.turn[pair];
         float s, c;
         sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);  // half turns, in [-1, 1]
-        s_cs[i] = make_float2(c * p.amplitude, s * p.sign);
+        const int x = V == 1 ? pair : ((pair % V / 2) * runs + pair / V) * 2 + (pair & 1);
+        s_cs[rr * pairs + x] = make_float2(c * p.amplitude, s * p.sign);
     }
     __syncthreads();
-    while (r[0] >= 0) {
-#pragma unroll
-        for (int i = 0; i < kAhead; i++) {
-            if (r[i] < 0 || s_pos[r[i]] < 0) continue;
-            u[i].turn(s_cs + r[i] * pairs + unit * V);
-            u[i].store(p.y[h[i] >= p.heads[0]] + place(r[i], h[i]), second);
-        }
-        fetch();
-    }
-    // results elsewhere: the columns that are not rotated
-    if (p.y[0] != p.x[0] && p.dims < p.dim) {
-        const int rest = p.dim - p.dims;
-        for (int w = 0; w < 2; w++) {
-            if (!p.x[w]) continue;
-            for (int i = threadIdx.x; i < rows * p.heads[w] * rest; i += kThreads) {
-                const int rh = i / rest, col = i - rh * rest, rr = rh / p.heads[w];
-                if (s_pos[rr] < 0) continue;
-                const int64_t at = (row0 * p.heads[w] + rh) * p.dim + (col < p.offset ? col : col + p.dims);
-                if constexpr (F32) reinterpret_cast<float *>(p.y[w])[at] = reinterpret_cast<const float *>(p.x[w])[at];
-                else reinterpret_cast<uint16_t *>(p.y[w])[at] = reinterpret_cast<const uint16_t *>(p.x[w])[at];
+    for (int unit0 = 0;;) {
+        while (any) {
+            if (s_pos[row] >= 0) {
+                if (unit < turned) u.turn(s_cs + row * pairs, unit, turned, runs);
+                u.store(to);
             }
+            head += lanes;
+            any = fetch();
         }
+        unit0 += kThreads;
+        if (unit0 >= turned + copied) break;
+        take(unit0);
+        any = fetch();
     }
     // a sequence out of range is reported whether or not a row led to it
     if (!p.positions) {
@@ -199,8 +248,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 
 template <bool F32, bool HALF, int V>
 cudaError_t launch(const RoParams &p, int64_t *ctas, cudaStream_t st) {
-    int rows_cta = kMaxRows;
-    while (rows_cta > 1 && (p.rows + rows_cta - 1) / rows_cta < 4 * 152) rows_cta /= 2;
+    int turned, copied;
+    units_of<Unit<F32, HALF, V>, V>(p, &turned, &copied);
+    const int64_t items = (int64_t)(p.heads[0] + p.heads[1]) * (turned + copied);  // of a row
+    int rows_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRows, kItems * kThreads / items));
+    while (rows_cta > 1 && (p.rows + rows_cta - 1) / rows_cta < 2 * 152) rows_cta--;
     *ctas = (p.rows + rows_cta - 1) / rows_cta;
     rotary_kernel<F32, HALF, V><<<(unsigned)*ctas, kThreads, (size_t)rows_cta * (p.dims / 2) * sizeof(float2), st>>>(p, rows_cta);
     return cudaGetLastError();
