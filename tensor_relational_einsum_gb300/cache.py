@@ -23,8 +23,7 @@ _CELLS = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
 
 
 def _on_device(t: torch.Tensor, dtype, shape, what: str) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
-            not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype}, {tuple(shape)}")
     return t
 
@@ -68,7 +67,7 @@ class PagedCache:
         with torch.cuda.device(self.device):
             check_status(lib().ea_cache_create(CACHE_FORMATS[format], self.pages, self.page, self.heads, self.dim, *ptr,
                                                ctypes.byref(h)))
-        self.handle = h
+        self.handle, self._at, self._raw = h, self.device.index, h.value
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -121,16 +120,27 @@ class PageBatch:
 
 def _raw_stream(device, stream) -> ctypes.c_void_p:
     """The CUDA stream of a call: ``stream``, or the device's current one."""
-    return ctypes.c_void_p(stream.cuda_stream if stream is not None else
-                           torch._C._cuda_getCurrentRawStream(device.index))
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _same_device(cache: PagedCache, batch: PageBatch, *relations):
-    if batch.device != cache.device:
+    device = cache.device
+    if batch.device != device:
         raise ValueError("the cache and the batch lie on different devices")
     for r in relations:
-        if r is not None and r.storage.device != cache.device:
+        if r is not None and r.device != device:
             raise ValueError("the cache and a relation lie on different devices")
+
+
+def _call(f, device, *args):
+    """``f(*args)`` of the library, on ``device``."""
+    if torch._C._cuda_getDevice() == device.index:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args)
+    if rc:
+        check_status(rc)
 
 
 def _rows_of(t: torch.Tensor, dtype, r: Relation, trailing: int, what: str) -> torch.Tensor:
@@ -139,7 +149,7 @@ def _rows_of(t: torch.Tensor, dtype, r: Relation, trailing: int, what: str) -> t
     for d in r.dims[:-trailing]:
         rows *= d
     _on_device(t, dtype, (rows,), what)
-    if t.device != r.storage.device:
+    if t.get_device() != r.device.index:
         raise ValueError(f"{what} and a relation lie on different devices")
     return t
 
@@ -224,24 +234,27 @@ def cache_keep(caches, batch: PageBatch, path: torch.Tensor, counts: torch.Tenso
     ``verify_drafts`` gives them (int32 CUDA tensors [sequences, width] and
     [sequences]).  Returns ``lens_out`` (int32 [sequences], new by default):
     the sequences' lengths with the kept rows only."""
-    caches = [caches] if isinstance(caches, PagedCache) else list(caches)
+    if isinstance(caches, PagedCache):
+        caches = (caches,)
     if not caches:
         raise ValueError("give a cache")
-    n = batch.pages.shape[0]
+    device, n = batch.device, batch.lens.shape[0]
     if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[1] < 1:
         raise ValueError("path must be an int32 CUDA tensor [sequences, width]")
-    _on_device(path, torch.int32, (n, path.shape[1]), "path")
+    width = path.shape[1]
+    _on_device(path, torch.int32, (n, width), "path")
     _on_device(counts, torch.int32, (n,), "counts")
     if lens_out is None:
-        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(batch.device):
-            lens_out = torch.empty(n, dtype=torch.int32, device=batch.device)
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device):
+            lens_out = torch.empty(n, dtype=torch.int32, device=device)
     else:
         _on_device(lens_out, torch.int32, (n,), "lens_out")
-    for c in caches:
-        _same_device(c, batch)
-    if any(t.device != batch.device for t in (path, counts, lens_out)):
+    at = device.index
+    if any([c._at != at for c in caches]):
+        raise ValueError("the caches and the batch lie on different devices")
+    if path.get_device() != at or counts.get_device() != at or lens_out.get_device() != at:
         raise ValueError("the batch and path, counts or lens_out lie on different devices")
-    handles = (ctypes.c_void_p * len(caches))(*[c.handle.value for c in caches])
-    check_status(lib().ea_cache_keep(handles, len(caches), batch.ref, path.data_ptr(), path.shape[1], counts.data_ptr(),
-                                     lens_out.data_ptr(), _raw_stream(batch.device, stream)))
+    handles = (ctypes.c_void_p * len(caches))(*[c._raw for c in caches])
+    _call(lib().ea_cache_keep, device, handles, len(caches), batch.ref, path.data_ptr(), width, counts.data_ptr(),
+          lens_out.data_ptr(), _raw_stream(device, stream))
     return lens_out

@@ -517,7 +517,8 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         while (ok) {
             int n, u0, slot, whole;  // what the loop over key tiles needs of the part
             int hi;                  // last key the row keeps
-            int node = 0, nodes_at = 0, nodes_row = 0;  // tree: the row's node; position and dense row of node 0
+            int node = 0;            // tree: the row's node
+            uint32_t ups = 0;        // tree: parents of nodes 4 lane .. 4 lane + 3, a byte each (255: none)
             int64_t at;              // the row's place in O; -1: no token of the sequence
             const uint32_t gt0 = gt;
             {
@@ -535,10 +536,19 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 const int pos = P.pos0 + x * half_tok + min(rtok, ntok - 1);
                 hi = sp.causal ? min(pos, P.len - 1) : P.len - 1;
                 if constexpr (TREE) {
-                    nodes_at = P.pos0 - P.tok0;
-                    nodes_row = P.row0 - P.tok0;
-                    node = pos - nodes_at;
-                    hi = nodes_at - 1;  // the last key that all rows keep
+                    const int first = P.pos0 - P.tok0, nodes = P.tok0 + P.ntok;
+                    node = pos - first;
+                    hi = first - 1;  // the last key that all rows keep
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int b = 4 * lane + i;
+                        int up = b < nodes ? __ldg(p.parents + P.row0 - P.tok0 + b) : -1;
+                        if (up >= b || up < -1) {
+                            batch_fail(p.err);
+                            up = -1;
+                        }
+                        ups |= (uint32_t)(up & 255) << (8 * i);
+                    }
                 }
                 at = row < half_rows && rtok < ntok
                          ? (int64_t)(P.row0 + x * half_tok + rtok) * p.qheads + P.head * sp.group + rhead : -1;
@@ -563,17 +573,14 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         const int before = jhi + 1 - 32 * q;
                         keep[q] = before >= 32 ? 0xffffffffu : before <= 0 ? 0u : (1u << before) - 1u;
                     }
-                    for (int b = node; b >= 0;) {  // up the tree: parents lie before their children, so this ends
+                    // up the tree, by shuffles: the warp holds all parents.  They lie before their children, so this ends.
+                    for (int b = node; __any_sync(0xffffffffu, b >= 0);) {
                         const int key = jhi + 1 + b;
 #pragma unroll
                         for (int q = 0; q < kKeys / 32; q++)
-                            if (key >> 5 == q) keep[q] |= 1u << (key & 31);
-                        const int up = __ldg(p.parents + nodes_row + b);
-                        if (up >= b || up < -1) {
-                            batch_fail(p.err);
-                            break;
-                        }
-                        b = up;
+                            if (b >= 0 && key >> 5 == q) keep[q] |= 1u << (key & 31);
+                        const uint32_t four = __shfl_sync(0xffffffffu, ups, (b >> 2) & 31);
+                        b = b < 0 ? -1 : (int)(int8_t)(four >> (8 * (b & 3)));
                     }
                 }
                 float hm0, hm1, hm2, hm3;

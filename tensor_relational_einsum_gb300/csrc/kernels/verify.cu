@@ -37,7 +37,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;            // the most CTAs of a sequence
 constexpr int kRuns = kCluster * kWarps;
-constexpr int kAhead = 4;              // vectors of a lane in flight
 constexpr int kResident = 4;           // CTAs of an SM
 static_assert(kRuns == 64, "a lane holds two runs' sums");
 constexpr double kUnit = 1.0 / 4611686018427387904.0;  // 2^-62
@@ -182,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
     __shared__ Order s_order;
     __shared__ uint64_t s_runs[kRuns];          // of the first CTA: the runs' sums
     __shared__ int s_up[kPgNodes], s_token[kPgNodes], s_path[kPgNodes], s_out[kPgNodes];
-    __shared__ float s_t[kPgNodes], s_d[kPgNodes], s_u[kPgNodes];
+    __shared__ float s_t[kPgNodes], s_d[kPgNodes], s_u[kPgNodes], s_was[kPgNodes];
+    constexpr int kAhead = DRAFT ? 4 : 8;       // vectors of a lane and row in flight
     uint32_t rank, ctas;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
             } else {
                 rejected++;
                 if (!out) {
+                    s_was[outs] = s_t[next];
                     s_out[outs++] = s_token[next];
                     if (have) mass -= min(mass, (uint64_t)fixed(s_t[next]));
                 }
@@ -334,13 +335,8 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
             for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
             mass = total;
             if constexpr (!DRAFT) {
-                for (int j = 1; j < next; j++) {
-                    // the tokens that were rejected at this node, each once
-                    if (s_up[j] != node) continue;
-                    bool again = false;
-                    for (int i = 1; i < j; i++) again |= s_up[i] == node && s_token[i] == s_token[j];
-                    if (!again) mass -= min(mass, (uint64_t)fixed(s_t[j]));
-                }
+                if (lane == 0)  // the tokens that were rejected at this node, each once
+                    for (int i = 0; i < outs; i++) mass -= min(mass, (uint64_t)fixed(s_was[i]));
             }
             have = true;
         }
@@ -362,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
             const int64_t each = (t.vectors + ctas * kWarps - 1) / (ctas * kWarps);
             for (int i = 0; i < outs; i++) {
                 uint64_t &run = s_runs[(t.skip + s_out[i]) / R::VE / each];
-                run -= min(run, (uint64_t)fixed(__saturatef(ld_elem(p.target, BF16 ? EA_BF16 : EA_F32, (int64_t)(s.first + node) * p.vocab + s_out[i]))));
+                run -= min(run, (uint64_t)fixed(s_was[i]));
             }
         }
     }

@@ -17,8 +17,8 @@ import math
 import torch
 
 from . import _abi
-from ._abi import ROTARY_LAYOUTS, check_status, lib
-from .cache import PageBatch, _on_device, _raw_stream, _rows_of
+from ._abi import ROTARY_LAYOUTS, lib
+from .cache import PageBatch, _call, _on_device, _raw_stream, _rows_of
 from .relation import Relation
 
 
@@ -60,6 +60,7 @@ class Rotary:
         if not math.isfinite(self.amplitude) or self.amplitude == 0.0:
             raise ValueError("amplitude must be finite and not 0")
         self._freqs = (ctypes.c_double * len(self.freqs))(*self.freqs)
+        self._address = ctypes.addressof(self._freqs)
 
 
 def rotary(q: Relation, k: Relation | None, plan: Rotary, batch: PageBatch | None = None,
@@ -74,25 +75,23 @@ def rotary(q: Relation, k: Relation | None, plan: Rotary, batch: PageBatch | Non
     sequence and of negative positions stay as they are.  ``backward``: the
     transposed rotation, which takes the gradients of the results to those of
     q and k.  Returns the results."""
-    if (q_out is None) != (k_out is None) and k is not None:
+    if k is not None and (q_out is None) != (k_out is None):
         raise ValueError("give both q_out and k_out, or neither")
     q_out = q if q_out is None else q_out
     k_out = k if k_out is None else k_out
-    device = q.storage.device
-    for t, what in ((positions, "positions"), (parents, "parents")):
-        if t is not None:
-            _rows_of(t, torch.int32, q, 2, what)
-    if any(r is not None and r.storage.device != device for r in (k, q_out, k_out)) or (batch is not None and batch.device != device):
+    device = q.device
+    o = _abi.RotaryOpts(ROTARY_LAYOUTS[plan.layout], plan.dims, plan.offset, 1 if backward else 0, plan.amplitude, 0,
+                        plan._address)
+    if positions is not None:
+        o.positions = _rows_of(positions, torch.int32, q, 2, "positions").data_ptr()
+    if parents is not None:
+        o.parents = _rows_of(parents, torch.int32, q, 2, "parents").data_ptr()
+    if q_out.device != device or (k is not None and (k.device != device or k_out.device != device)) or \
+            (batch is not None and batch.device != device):
         raise ValueError("q, k, their results and the batch lie on different devices")
-    o = _abi.RotaryOpts()
-    o.layout, o.dims, o.offset, o.backward = ROTARY_LAYOUTS[plan.layout], plan.dims, plan.offset, 1 if backward else 0
-    o.amplitude, o.freqs = plan.amplitude, ctypes.addressof(plan._freqs)
-    o.positions = positions.data_ptr() if positions is not None else None
-    o.parents = parents.data_ptr() if parents is not None else None
-    with torch.cuda.device(device):
-        check_status(lib().ea_rotary(ctypes.byref(o), batch.ref if batch is not None else None, q.handle,
-                                     k.handle if k is not None else None, q_out.handle,
-                                     k_out.handle if k is not None else None, _raw_stream(device, stream)))
+    _call(lib().ea_rotary, device, ctypes.byref(o), batch.ref if batch is not None else None, q.handle,
+          k.handle if k is not None else None, q_out.handle, k_out.handle if k is not None else None,
+          _raw_stream(device, stream))
     return q_out, k_out
 
 
@@ -112,12 +111,12 @@ def verify_drafts(target: Relation, batch: PageBatch, tokens: torch.Tensor, acce
     Returns (``path`` [sequences, width], the accepted rows counted from the
     sequence's first, -1 behind them; ``counts``, their number; ``picked``, the
     token that follows): int32, new ones by default, width then max_new."""
-    device = target.storage.device
+    device = target.device
     _rows_of(tokens, torch.int32, target, 1, "tokens")
     _rows_of(accept, torch.float32, target, 1, "accept")
     if parents is not None:
         _rows_of(parents, torch.int32, target, 1, "parents")
-    n = batch.starts.shape[0] - 1
+    n = batch.lens.shape[0]
     _on_device(sample, torch.float32, (n,), "sample")
     if path is not None and (not isinstance(path, torch.Tensor) or path.dim() != 2):
         raise ValueError("path must be an int32 CUDA tensor [sequences, width]")
@@ -127,15 +126,16 @@ def verify_drafts(target: Relation, batch: PageBatch, tokens: torch.Tensor, acce
             path = torch.empty(n, width, dtype=torch.int32, device=device) if path is None else path
             counts = torch.empty(n, dtype=torch.int32, device=device) if counts is None else counts
             picked = torch.empty(n, dtype=torch.int32, device=device) if picked is None else picked
-    _on_device(path, torch.int32, (n, path.shape[1]), "path")
+    width = path.shape[1]
+    _on_device(path, torch.int32, (n, width), "path")
     _on_device(counts, torch.int32, (n,), "counts")
     _on_device(picked, torch.int32, (n,), "picked")
-    if any(t.device != device for t in (sample, path, counts, picked, batch.starts)) or \
-            (draft is not None and draft.storage.device != device):
+    at = device.index
+    if sample.get_device() != at or path.get_device() != at or counts.get_device() != at or picked.get_device() != at or \
+            batch.device != device or (draft is not None and draft.device != device):
         raise ValueError("the operands of verify_drafts lie on different devices")
     o = _abi.VerifyOpts(tokens.data_ptr(), parents.data_ptr() if parents is not None else None, accept.data_ptr(),
-                        sample.data_ptr(), path.data_ptr(), counts.data_ptr(), picked.data_ptr(), path.shape[1])
-    with torch.cuda.device(device):
-        check_status(lib().ea_verify_drafts(ctypes.byref(o), batch.ref, target.handle,
-                                            draft.handle if draft is not None else None, _raw_stream(device, stream)))
+                        sample.data_ptr(), path.data_ptr(), counts.data_ptr(), picked.data_ptr(), width)
+    _call(lib().ea_verify_drafts, device, ctypes.byref(o), batch.ref, target.handle,
+          draft.handle if draft is not None else None, _raw_stream(device, stream))
     return path, counts, picked

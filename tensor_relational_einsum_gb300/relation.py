@@ -45,6 +45,7 @@ class Relation:
             if not storage.is_contiguous():
                 raise ValueError("storage must be contiguous")
         self.storage = storage
+        self.device = storage.device
         arr, keep, bounds = _abi.dim_parts(self.dims, parts)
         self.bounds = bounds
         h = ctypes.c_void_p()
