@@ -19,8 +19,7 @@ namespace {
 using namespace pg;
 
 constexpr int kWarps = 8;
-// Rows of a CTA: one a warp where items have 32 rows at most; 32 of more, because a CTA without a cut costs too.
-__host__ __device__ constexpr int rows_per_cta(int rows) { return rows <= 32 ? kWarps : 32; }
+constexpr int kCtas = 1280;      // a CTA without a cut costs too: about so many at most
 
 template <int D>
 __device__ __forceinline__ void load_acc(const float *src, int lane, float *v) {
@@ -116,7 +115,7 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
     const PgCut c = w.cut[x];
     if (c.we == 0 || pg_first(c.total, c.parts, x - 1) > c.wi) return;  // not cut here, or merged by an earlier cut
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int r0 = group * rows_per_cta(rows), r1 = min(c.rows, r0 + rows_per_cta(rows));
+    const int r0 = group * mg.each[k], r1 = min(c.rows, r0 + mg.each[k]);
     if (r0 >= r1) return;
     // parts: the last of CTA x - 1 (its only one if the item begins with it), then the first of x, x + 1, ...
     const int slot0 = 2 * (x - 1) + (pg_first(c.total, c.parts, x - 1) < c.wi ? 1 : 0);
@@ -191,7 +190,11 @@ cache_merge_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ PgM
 
 cudaError_t launch_cache_merge(const PgAttn &p, const PgMerge &m, cudaStream_t st) {
     PgMerge g = m;
-    for (int k = 0; k < 2; k++) g.groups[k] = std::max(1, (m.rows[k] + rows_per_cta(m.rows[k]) - 1) / rows_per_cta(m.rows[k]));
+    for (int k = 0; k < 2; k++) {
+        // a row a warp, or two or four
+        for (g.each[k] = kWarps; g.each[k] < 4 * kWarps && (int64_t)g.cuts[k] * ((m.most[k] + g.each[k] - 1) / g.each[k]) > kCtas;) g.each[k] *= 2;
+        g.groups[k] = std::max(1, (m.most[k] + g.each[k] - 1) / g.each[k]);
+    }
     const dim3 grid(g.cuts[0] * g.groups[0] + g.cuts[1] * g.groups[1]);
     if (p.c.dim == 64) return launch_after(cache_merge_kernel<64>, grid, 32 * kWarps, 0, st, true, p, g);
     return launch_after(cache_merge_kernel<128>, grid, 32 * kWarps, 0, st, true, p, g);

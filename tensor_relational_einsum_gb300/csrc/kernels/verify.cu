@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
     __shared__ uint64_t s_runs[kRuns];          // of the first CTA: the runs' sums
     __shared__ int s_up[kPgNodes], s_token[kPgNodes], s_path[kPgNodes], s_out[kPgNodes];
     __shared__ float s_t[kPgNodes], s_d[kPgNodes], s_u[kPgNodes], s_was[kPgNodes];
-    constexpr int kAhead = DRAFT ? 4 : 8;       // vectors of a lane and row in flight
+    constexpr int kAhead = DRAFT ? 2 : 4;       // vectors of a lane and row in flight
     uint32_t rank, ctas;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));

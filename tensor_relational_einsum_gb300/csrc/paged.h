@@ -81,7 +81,7 @@ struct PgSplit {
     int32_t kt;                  // keys of a unit
     int32_t causal;
     int32_t min_rows, max_rows;  // the sequences served: min_rows <= n * group <= max_rows
-    int32_t solo;                // token kernel: a warp, not a CTA, takes a share
+    int32_t solo;                // token kernel: a warp, not a CTA, takes a share; chunk kernel: no item has a second tile of rows
 };
 
 // What a CTA whose range begins inside an item says to the merge.
@@ -157,7 +157,8 @@ struct PgMerge {
     PgWork w[2];
     int32_t cuts[2];             // CTAs - 1; 0: none
     int32_t rows[2];
-    int32_t groups[2];           // CTAs of a cut (set by the launch)
+    int32_t most[2];             // rows of an item at most
+    int32_t groups[2], each[2];  // CTAs of a cut, and their rows (set by the launch)
 };
 cudaError_t launch_cache_merge(const PgAttn &p, const PgMerge &m, cudaStream_t st);
 

@@ -138,6 +138,22 @@ def test_tree_behind_a_long_axis(n, t, group, fmt):
         tree_attention(b, c, held, group, trees, parents, rng, max_new=n)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_many_trees_in_a_wide_table(fmt, dim):
+    """More items than CTAs, of one tile of rows and of two, over tables that allow cutting: whole items, cut ones, and
+    items without or with a single key tile, in one call."""
+    rng = np.random.default_rng(14)
+    seqs = [(int(n), int(t)) for n, t in zip(rng.integers(9, 17, 66), rng.integers(20, 1400, 66))]
+    seqs[3:6] = [(40, 300), (64, 900), (33, 33)]       # two tiles of rows
+    seqs[10:13] = [(12, 12), (11, 5), (0, 700)]
+    b = cu.Batch(seqs, 64, before=1, behind=1, seed=15, extra_pages=4)
+    c = nan_cache(b, 4, dim, fmt)
+    held = fill(c, b, rng)
+    trees, parents = parents_of(b, "random")
+    tree_attention(b, c, held, 4, trees, parents, rng, max_new=64)
+
+
 @pytest.mark.parametrize("kind", ["star", "roots", "pairs"])
 def test_tree_without_a_bound_and_a_scale(kind):
     """max_new 0: the dense rows say how many nodes there can be; peaked scores."""
