@@ -148,7 +148,7 @@ def lib():
                                                ctypes.c_int32, ctypes.c_int64, P64, P64]
         L.ea_rotary.argtypes = [ctypes.POINTER(RotaryOpts), ctypes.POINTER(PageBatchArgs), VP, VP, VP, VP, VP]
         L.ea_verify_drafts.argtypes = [ctypes.POINTER(VerifyOpts), ctypes.POINTER(PageBatchArgs), VP, VP, VP]
-        L.ea_cache_keep.argtypes = [ctypes.POINTER(VP), ctypes.c_int32, ctypes.POINTER(PageBatchArgs), VP,
+        L.ea_cache_keep.argtypes = [VP, ctypes.c_int32, ctypes.POINTER(PageBatchArgs), VP,
                                     ctypes.c_int32, VP, VP, VP]
         for name in ("ea_check", "ea_plan_cache_clear", "ea_relation_create", "ea_relation_destroy",
                      "ea_relation_info", "ea_relation_block", "ea_relation_data", "ea_relation_bounds",

@@ -12,6 +12,8 @@ out on the device and reported by ``check()``.
 from __future__ import annotations
 
 import ctypes
+from array import array
+from operator import attrgetter
 
 import torch
 
@@ -19,6 +21,7 @@ from . import _abi
 from ._abi import CACHE_FORMATS, check_status, lib
 from .relation import Relation
 
+_AT, _RAW = attrgetter("_at"), attrgetter("_raw")
 _CELLS = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
 
 
@@ -250,11 +253,11 @@ def cache_keep(caches, batch: PageBatch, path: torch.Tensor, counts: torch.Tenso
     else:
         _on_device(lens_out, torch.int32, (n,), "lens_out")
     at = device.index
-    if any([c._at != at for c in caches]):
+    if set(map(_AT, caches)) != {at}:
         raise ValueError("the caches and the batch lie on different devices")
     if path.get_device() != at or counts.get_device() != at or lens_out.get_device() != at:
         raise ValueError("the batch and path, counts or lens_out lie on different devices")
-    handles = (ctypes.c_void_p * len(caches))(*[c._raw for c in caches])
-    _call(lib().ea_cache_keep, device, handles, len(caches), batch.ref, path.data_ptr(), width, counts.data_ptr(),
+    handles = array("Q", map(_RAW, caches))
+    _call(lib().ea_cache_keep, device, handles.buffer_info()[0], len(handles), batch.ref, path.data_ptr(), width, counts.data_ptr(),
           lens_out.data_ptr(), _raw_stream(device, stream))
     return lens_out

@@ -314,7 +314,7 @@ extern "C" ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *bat
         }
         PgMerge m{{wc, wt}, {wc.cut ? a.chunks.ctas - 1 : 0, wt.cut ? a.tokens.ctas - 1 : 0},
                   {a.chunks.rows, a.tokens.rows},
-                  {a.chunks.split.solo ? a.chunks.rows / 2 : a.chunks.rows, a.tokens.rows}};
+                  {(int32_t)std::min<int64_t>(a.chunks.rows, (int64_t)p.t.max_new * p.group), a.tokens.rows}};
         if (m.cuts[0] + m.cuts[1] > 0) {
             e = launch_cache_merge(p, m, (cudaStream_t)stream);
             if (e != cudaSuccess) return cuda_error(e, "ea_cache_attention");

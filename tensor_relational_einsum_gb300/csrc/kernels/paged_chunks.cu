@@ -19,7 +19,6 @@ PgPlan plan_cache_chunks(const PgTable &t, const PgPool &c, int group, int causa
     sp.causal = causal;
     sp.min_rows = min_rows;
     sp.max_rows = INT32_MAX;
-    sp.solo = t.max_new <= tpt;
     pl.rows = sp.tok * group;
     const int64_t items = std::min<int64_t>((int64_t)t.n_seqs * ((t.max_new + sp.tok - 1) / sp.tok), t.rows / sp.tok + t.n_seqs);
     const int64_t units = (t.cap + sp.kt - 1) / sp.kt * items * c.heads;

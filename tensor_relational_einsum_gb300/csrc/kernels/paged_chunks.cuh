@@ -77,7 +77,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;   // S_0 [0, 128), S_1 [128, 256), A_0 [256, 256 + D), A_1 [256 + D, ..)
 constexpr float kLazy = 8.f;      // a running maximum moves when it is exceeded by this much (log2)
 constexpr int kParts = 4;         // ring of parts
-constexpr int kMaxStages = 5;
+constexpr int kMaxStages = 4;
 constexpr int kWhole = 1024;      // sequences of up to so many positions are not cut
 
 // Register split (setmaxnreg): the softmax threads keep a row of 128 scores.
@@ -201,10 +201,6 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
     const Seqs seqs{p.t, p.err};
     const int half_tok = sp.tok / 2;      // tokens of a tile
     const int half_rows = half_tok * sp.group;
-    // V's ring.  A V tile waits for its scores' softmax, so its place is taken longer than K's; where no item has a second
-    // tile of rows, that tile's Q makes room for one more.
-    const uint32_t v_stages = C::ST + (sp.solo ? 1 : 0);
-    auto v_at = [](uint32_t st) { return st < C::ST ? C::V_OFF + st * C::TILE : (uint32_t)C::TILE; };
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; b++) {
@@ -215,7 +211,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             mbar_init(&ctl->p_full[b], 4);
             mbar_init(&ctl->o_fin[b], 1);
         }
-        for (int b = 0; b <= C::ST; b++) {
+        for (int b = 0; b < C::ST; b++) {
             mbar_init(&ctl->k_full[b], E4M3 ? 4 : 1);
             mbar_init(&ctl->k_empty[b], 1);
             mbar_init(&ctl->v_full[b], E4M3 ? 4 : 1);
@@ -261,7 +257,6 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         // ------------------------------------------------ copies (the whole warp; a lane looks up and copies a page)
         uint32_t ct = 0, qx0 = 0, qx1 = 0;  // key tiles, items per X
         uint32_t q_armed = 0, q_par = 0, k_armed = 0, k_par = 0, v_armed = 0, v_par = 0, raw_armed = 0, raw_par = 0;
-        uint32_t vs = 0, vp = 0;  // V's stage, and its pass over the ring
         bool ok = true;
         const int lg = p.c.page_log2, page = 1 << lg;
         Part P;
@@ -309,33 +304,29 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     const uint32_t ph = (ct / C::ST) & 1;
                     const int np = (nv + page - 1) >> lg;
                     const int row = (int)pg_vec(p.c, g, P.head, 0);
-                    auto load = [&](const CUtensorMap *map, uint32_t off, uint64_t *full, uint64_t *empty, uint32_t phase) {
-                        if (!warp_wait(empty, phase ^ 1, abort, p.err, kDevTimeoutProducer)) return false;
-                        if (lane == 0) mbar_expect_tx(full, np * page * D * 2);
+                    auto load = [&](const CUtensorMap *map, uint32_t off, uint64_t *full, uint64_t *empty) {
+                        if (!warp_wait(&empty[st], ph ^ 1, abort, p.err, kDevTimeoutProducer)) return false;
+                        if (lane == 0) mbar_expect_tx(&full[st], np * page * D * 2);
                         __syncwarp();
                         if (lane < np) {
-                            const uint32_t dst = smem_u32(smem + off) + lane * page * 128;
+                            const uint32_t dst = smem_u32(smem + off + st * C::TILE) + lane * page * 128;
 #pragma unroll
-                            for (int c = 0; c < C::CH; c++) tma_load_3d(dst + c * (kKeys * 128), map, full, 64 * c, row, 0);
+                            for (int c = 0; c < C::CH; c++) tma_load_3d(dst + c * (kKeys * 128), map, &full[st], 64 * c, row, 0);
                         }
                         return true;
                     };
-                    if (!load(&k_map, C::K_OFF + st * C::TILE, &ctl->k_full[st], &ctl->k_empty[st], ph)) {
+                    if (!load(&k_map, C::K_OFF, ctl->k_full, ctl->k_empty)) {
                         ok = false;
                         break;
                     }
                     k_armed |= 1u << st;
                     k_par = (k_par & ~(1u << st)) | (ph << st);
-                    if (!load(&v_map, v_at(vs), &ctl->v_full[vs], &ctl->v_empty[vs], vp)) {
+                    if (!load(&v_map, C::V_OFF, ctl->v_full, ctl->v_empty)) {
                         ok = false;
                         break;
                     }
-                    v_armed |= 1u << vs;
-                    v_par = (v_par & ~(1u << vs)) | (vp << vs);
-                    if (++vs == v_stages) {
-                        vs = 0;
-                        vp ^= 1;
-                    }
+                    v_armed |= 1u << st;
+                    v_par = (v_par & ~(1u << st)) | (ph << st);
                 } else {
                     const int rs = ct % C::NR, np = (nv + page - 1) >> lg;
                     const uint32_t ph = (ct / C::NR) & 1;
@@ -368,7 +359,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             // Let our own copies land before the CTA can exit.
             for (int s = 0; s < 2; s++)
                 if (q_armed & (1u << s)) mbar_wait(&ctl->q_full[s], (q_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
-            for (int s = 0; s <= C::ST; s++) {
+            for (int s = 0; s < C::ST; s++) {
                 if (k_armed & (1u << s)) mbar_wait(&ctl->k_full[s], (k_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
                 if (v_armed & (1u << s)) mbar_wait(&ctl->v_full[s], (v_par >> s) & 1, abort, p.err, 0, kDrainNs, false);
             }
@@ -396,10 +387,9 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             }
             __syncwarp();
         };
-        uint32_t vs = 0, vp = 0;  // V's stage, and its pass over the ring
-        // A_x (+)= P_x V over the first `steps` runs of 16 keys
-        auto mma_o = [&](int x, bool first, int steps) {
-            const uint64_t vd = sdesc(smem_u32(smem + v_at(vs)), kKeys * 128, 1024);
+        // A_x (+)= P_x V_t over the first `steps` runs of 16 keys
+        auto mma_o = [&](int x, uint32_t t, bool first, int steps) {
+            const uint64_t vd = sdesc(smem_u32(smem + C::V_OFF + (t % C::ST) * C::TILE), kKeys * 128, 1024);
             const uint32_t pa = tmem + (uint32_t)(x * kKeys);
             const uint32_t d = tmem + kOCol + (uint32_t)(x * D);
             if (elect_one()) {
@@ -415,12 +405,12 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
             __syncwarp();
         };
         auto k_wait = [&](uint32_t t) { return warp_wait(&ctl->k_full[t % C::ST], (t / C::ST) & 1, abort, p.err, kDevTimeoutMma); };
-        // The next V is there, with the last rows of a partial tile cleared
-        auto v_wait = [&](int nv) {
-            if (!warp_wait(&ctl->v_full[vs], vp, abort, p.err, kDevTimeoutMma)) return false;
+        // V of tile t is there, with the last rows of a partial tile cleared
+        auto v_wait = [&](uint32_t t, int nv) {
+            if (!warp_wait(&ctl->v_full[t % C::ST], (t / C::ST) & 1, abort, p.err, kDevTimeoutMma)) return false;
             const int to = (nv + 15) & ~15;
             if (!E4M3 && nv < to) {
-                uint8_t *v = smem + v_at(vs);
+                uint8_t *v = smem + C::V_OFF + (t % C::ST) * C::TILE;
                 for (int i = lane; i < (to - nv) * 8; i += 32)
 #pragma unroll
                     for (int c = 0; c < C::CH; c++)
@@ -458,7 +448,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 for (int x = 0; x < 2; x++) {
                     const int ntx = x == 0 ? nt0 : nt1;
                     if (j >= ntx) continue;  // the rest of the part is beyond what x keeps
-                    if (!v_now && !v_wait(nv)) {
+                    if (!v_now && !v_wait(t, nv)) {
                         ok = false;
                         break;
                     }
@@ -468,9 +458,9 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         break;
                     }
                     tc_fence_after();
-                    mma_o(x, j == 0, (nv + 15) >> 4);
+                    mma_o(x, t, j == 0, (nv + 15) >> 4);
                     if (j == ntx - 1) commit1(&ctl->o_fin[x]);
-                    if (x == 1 || j >= nt1) commit1(&ctl->v_empty[vs]);  // the tile's last product
+                    if (x == 1 || j >= nt1) commit1(&ctl->v_empty[t % C::ST]);  // the tile's last product
                     if (j + 1 < ntx) {
                         if (!k_next && !k_wait(t + 1)) {
                             ok = false;
@@ -481,10 +471,6 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         if (j + 1 == ntx - 1) commit1(&ctl->q_empty[x]);
                         if (x == 1 || j + 1 >= nt1) commit1(&ctl->k_empty[(t + 1) % C::ST]);
                     }
-                }
-                if (++vs == v_stages) {
-                    vs = 0;
-                    vp ^= 1;
                 }
             }
             ct += n;
@@ -747,7 +733,6 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
         const int tid = threadIdx.x - 384;
         constexpr int CPR = D / 16;  // 16-byte chunks (16 codes) of a row
         uint32_t ct = 0, qx0 = 0, qx1 = 0;
-        uint32_t vs = 0, vp = 0;  // V's stage, and its pass over the ring
         int vref = 0;
         bool ok = true;
         // Q of both tiles, a row a thread, in place: bf16 to f16, brought to [2^14, 2^15) by a power of two
@@ -794,7 +779,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                 uint32_t fv = 0, fk = 0;  // factors of row row0 + lane of K and V, f16 twice
 #pragma unroll
                 for (int h = 0; h < 2; h++) {  // K, V
-                    if (!warp_wait(h ? &ctl->v_empty[vs] : &ctl->k_empty[st], (h ? vp : (ct / C::ST) & 1) ^ 1, abort, p.err, kDevTimeoutProducer) ||
+                    if (!warp_wait(h ? &ctl->v_empty[st] : &ctl->k_empty[st], ((ct / C::ST) & 1) ^ 1, abort, p.err, kDevTimeoutProducer) ||
                         !warp_wait(&ctl->raw_full[h][rs], (ct / C::NR) & 1, abort, p.err, kDevTimeoutProducer)) {
                         ok = false;
                         break;
@@ -846,7 +831,7 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         for (int i = 0; i < CPR; i++)
                             if (row0 + (i * 32 + lane) / CPR >= nv) v[i] = make_uint4(0, 0, 0, 0);
                     }
-                    uint8_t *dst = smem + (h ? v_at(vs) : C::K_OFF + st * C::TILE) + row0 * 128;
+                    uint8_t *dst = smem + (h ? C::V_OFF : C::K_OFF) + st * C::TILE + row0 * 128;
 #pragma unroll
                     for (int i = 0; i < CPR; i++) {
                         const int r = (i * 32 + lane) / CPR, ch = lane % CPR;
@@ -867,16 +852,12 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                     }
                     fence_proxy_async();  // the operand tiles are read by the tensor cores (async proxy)
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(h ? &ctl->v_full[vs] : &ctl->k_full[st]);
+                    if (lane == 0) mbar_arrive(h ? &ctl->v_full[st] : &ctl->k_full[st]);
                     // the part's Q between its first K and V: it arrives when the part before has done its last scores
                     if (j == 0 && h == 0 && !rewrite_q(P)) {
                         ok = false;
                         break;
                     }
-                }
-                if (++vs == v_stages) {
-                    vs = 0;
-                    vp ^= 1;
                 }
             }
         }

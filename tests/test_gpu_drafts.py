@@ -154,6 +154,32 @@ def test_many_trees_in_a_wide_table(fmt, dim):
     tree_attention(b, c, held, 4, trees, parents, rng, max_new=64)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group,n", [(3, 85), (4, 16), (4, 8), (1, 127)])
+def test_every_run_gives_the_same_bits(group, n, fmt, dim):
+    """Trees and rows in order, many parts a CTA: 40 runs of one call."""
+    from tensor_relational_einsum_gb300 import cache_attention
+    from tensor_relational_einsum_gb300.relation import check
+    rng = np.random.default_rng(37)
+    seqs = [(int(x), int(x + t)) for x, t in zip(rng.integers(max(1, n // 2), n + 1, size=16), rng.integers(0, 1300, size=16))]
+    seqs[3] = (n, 2500)
+    b = cu.Batch(seqs, 32, before=1)
+    c = nan_cache(b, 8, dim, fmt)
+    fill(c, b, rng)
+    q = relation(torch.from_numpy(values(rng, (b.rows, 8 * group, dim))).to(torch.bfloat16).cuda())
+    _, parents = parents_of(b, "random")
+    batch = on_gpu(b, max_new=n)
+    for tree in (parents, None):
+        first = None
+        for _ in range(40):
+            out = torch.zeros(b.rows, 8 * group, dim, dtype=torch.bfloat16, device="cuda")
+            cache_attention(q, c, batch, out=relation(out), parents=tree)
+            first = out if first is None else first
+            assert torch.equal(out, first)
+    check()
+
+
 @pytest.mark.parametrize("kind", ["star", "roots", "pairs"])
 def test_tree_without_a_bound_and_a_scale(kind):
     """max_new 0: the dense rows say how many nodes there can be; peaked scores."""
