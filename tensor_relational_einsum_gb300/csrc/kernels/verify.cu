@@ -25,6 +25,8 @@
 // below 2.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "../drafts.h"
 #include "paged_common.cuh"
 
@@ -39,7 +41,7 @@ constexpr int kCluster = 8;            // the most CTAs of a sequence
 constexpr int kRuns = kCluster * kWarps;
 constexpr int kResident = 4;           // CTAs of an SM
 static_assert(kRuns == 64, "a lane holds two runs' sums");
-constexpr double kUnit = 1.0 / 4611686018427387904.0;  // 2^-62
+constexpr float kUnit = 0x1p-62f;
 
 // x (|x| < 2) in units of 2^-62, below 2^-39 rounded towards 0.
 __device__ __forceinline__ int64_t fixed(float x) {
@@ -83,10 +85,16 @@ struct alignas(8) Pair {
     float h, l;
 };
 __device__ __forceinline__ Pair pair_of(uint64_t x) {  // units of 2^-62
-    const double d = (double)x * kUnit;
-    const float h = (float)d;
-    return Pair{h, (float)(d - (double)h)};
+    const float h = __ull2float_rn(x);
+    return Pair{h * kUnit, __ll2float_rn((int64_t)(x - __float2ull_rn(h))) * kUnit};
 }
+// z q, rounded to about 2^-47.
+__device__ __forceinline__ Pair times(const Pair &z, float q) {
+    const float h = __fmul_rn(z.h, q);
+    return Pair{h, fmaf(z.h, q, -h) + __fmul_rn(z.l, q)};
+}
+// a < b, exactly for the two pairs (differences of neighbouring floats are exact; else the first parts decide).
+__device__ __forceinline__ bool less(const Pair &a, const Pair &b) { return __fsub_rn(a.h, b.h) < __fsub_rn(b.l, a.l); }
 __device__ __forceinline__ uint64_t fixed(const Pair &x) { return (uint64_t)max((int64_t)0, fixed(x.h) + fixed(x.l)); }
 // s += x: the exact error of the first parts' sum goes to the second.
 __device__ __forceinline__ void add_to(Pair &s, const Pair &x) {
@@ -162,13 +170,13 @@ __device__ __forceinline__ Pair rest_of(float t, float d, const Order &o) {
         r = h > 0.f ? Pair{h, __fsub_rn(__fsub_rn(r.h, h), q)} : Pair{0.f, 0.f};  // exact: the larger first
         for (int k = 1; k < o.rejected; k++) {
             const Pair z = o.mass[k];
-            const float ph = __fmul_rn(z.h, q), pl = fmaf(z.h, q, -ph) + __fmul_rn(z.l, q);
-            const float e = __fsub_rn(r.h, ph);
+            const Pair x = times(z, q);
+            const float e = __fsub_rn(r.h, x.h);
             if (!(e >= 0.f)) {
                 r = Pair{0.f, 0.f};
                 continue;
             }
-            const float l = __fadd_rn(__fsub_rn(__fsub_rn(r.h, e), ph), __fsub_rn(r.l, pl)), g = __fadd_rn(e, l);
+            const float l = __fadd_rn(__fsub_rn(__fsub_rn(r.h, e), x.h), __fsub_rn(r.l, x.l)), g = __fadd_rn(e, l);
             r = g > 0.f ? Pair{g, __fsub_rn(l, __fsub_rn(g, e))} : Pair{0.f, 0.f};
         }
     }
@@ -182,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
     __shared__ uint64_t s_runs[kRuns];          // of the first CTA: the runs' sums
     __shared__ int s_up[kPgNodes], s_token[kPgNodes], s_path[kPgNodes], s_out[kPgNodes];
     __shared__ float s_t[kPgNodes], s_d[kPgNodes], s_u[kPgNodes], s_was[kPgNodes];
-    constexpr int kAhead = DRAFT ? 2 : 4;       // vectors of a lane and row in flight
+    constexpr int kAhead = 2;                   // vectors of a lane in flight of two rows; twice as many of one
     uint32_t rank, ctas;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
@@ -223,20 +231,22 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
         for (; next < s.n; next++) {
             if (s_up[next] != node) continue;
             if (rejected > 0 && !have) return true;
-            const double u = s_u[next];
+            const float u = s_u[next];
             bool yes;
             bool out = false;                   // certain tokens: one that was rejected before
             if constexpr (DRAFT) {
+                const Pair d = times(Pair{u, 0.f}, s_d[next]);
+                s_order.rejected = rejected;
+                const Pair r = rest_of(s_t[next], s_d[next], s_order);
                 if (rejected == 0) {
-                    yes = u * (double)s_d[next] < (double)s_t[next];
+                    yes = less(d, r);
                 } else {
-                    s_order.rejected = rejected;
-                    const Pair r = rest_of(s_t[next], s_d[next], s_order);
-                    yes = u * (double)s_d[next] * ((double)mass * kUnit) < (double)r.h + (double)r.l;
+                    const Pair z = pair_of(mass), h = times(z, d.h);
+                    yes = less(Pair{h.h, h.l + __fmul_rn(z.h, d.l)}, r);
                 }
             } else {
                 for (int i = 0; i < outs; i++) out |= s_out[i] == s_token[next];
-                yes = !out && u * (rejected == 0 ? 1.0 : (double)mass * kUnit) < (double)s_t[next];
+                yes = !out && less(rejected == 0 ? Pair{u, 0.f} : times(pair_of(mass), u), Pair{s_t[next], 0.f});
             }
             if (yes) {
                 node = next;
@@ -292,22 +302,32 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
         };
         // whole vectors, several of a lane in flight
         const int64_t w0 = max(v0, t.first_whole()), w1 = min(v1, t.last_whole());
-        for (int64_t v = w0 + lane; v < w1; v += 32 * kAhead) {
-            uint4 a[kAhead], b[kAhead];
+        auto whole = [&](auto ahead, auto drafts) {
+            constexpr int A = decltype(ahead)::value;
+            constexpr bool B = decltype(drafts)::value;
+            for (int64_t v = w0 + lane; v < w1; v += 32 * A) {
+                uint4 a[A], b[B ? A : 1];
 #pragma unroll
-            for (int k = 0; k < kAhead; k++) {
-                const bool in = v + 32 * k < w1;
-                a[k] = b[k] = make_uint4(0, 0, 0, 0);
-                if (in) a[k] = __ldg(t.at + v + 32 * k);
-                if (in && both) b[k] = __ldg(d.at + v + 32 * k);
-            }
+                for (int k = 0; k < A; k++) {
+                    const bool in = v + 32 * k < w1;
+                    a[k] = in ? __ldg(t.at + v + 32 * k) : make_uint4(0, 0, 0, 0);
+                    if constexpr (B) b[k] = in ? __ldg(d.at + v + 32 * k) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-            for (int k = 0; k < kAhead; k++) {
-                float x[R::VE], y[R::VE];
-                R::values(a[k], x);
-                R::values(b[k], y);
-                add(x, y);
+                for (int k = 0; k < A; k++) {
+                    float x[R::VE], y[R::VE];
+                    R::values(a[k], x);
+                    if constexpr (B) R::values(b[k], y);
+#pragma unroll
+                    for (int i = 0; i < R::VE; i++) add_to(part, B ? rest_of(x[i], y[i], s_order) : Pair{__saturatef(x[i]), 0.f});
+                }
             }
+        };
+        if constexpr (DRAFT) {
+            if (both) whole(std::integral_constant<int, kAhead>{}, std::true_type{});
+            else whole(std::integral_constant<int, 2 * kAhead>{}, std::false_type{});
+        } else {
+            whole(std::integral_constant<int, 2 * kAhead>{}, std::false_type{});
         }
         // the row's ends: the first vector (lane 0) and the last (lane 1), where they are not whole
         if (lane == 0 || (lane == 1 && t.vectors > 1)) {
