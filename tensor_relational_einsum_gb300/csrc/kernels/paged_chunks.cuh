@@ -55,6 +55,16 @@
 //              run while the other's softmax does.
 //   warp 10    hands the CTA's parts of items to the others through a ring.
 //   warps 12-15 (e4m3) rewrite the raw tiles and Q as f16, 32 rows a warp.
+//
+// TREE: the rows of a sequence are the nodes of a tree (128 at most).  Items
+// have all keys of the sequence; in the one or two tiles that hold nodes a row
+// walks up from its own node and sets a bit for each on the way.  The parents
+// sit in the warp's lanes, four bytes each, so a step is a shuffle (read from
+// memory it took 270 cycles).  16 / 32 / 64 nodes in 32 sequences of 5000
+// positions, 32 heads over 8: 134 / 144 / 178 us, 132 / 139 / 163 us as causal
+// chains, whose first tile of rows has fewer keys; one sequence of 200001
+// positions, 32 nodes: 152 us, 0.79 of the measured copy rate.
+//
 // Every mbarrier wait is bounded (2 s); on time-out the kernel raises the
 // device error word, all roles leave their loops, the copies and MMAs in
 // flight are waited for and TMEM is freed before the CTA exits.

@@ -8,6 +8,9 @@
 // latency of reading the partial results, which are in L2, so all that a row
 // needs is asked for together: with few parts a warp takes two rows, with many
 // one row and eight parts at a time, and rows that leave warps idle are shared.
+// Eight rows of one sequence, 32 heads over 8: 2000 positions 18.5 us with the
+// attention, 8000 positions 26 us (35 and 43 us with four rows a warp and the
+// maxima in a round trip of their own).
 #include <algorithm>
 
 #include "attn_common.cuh"

@@ -10,8 +10,15 @@
 //     at any position, and its upper 32 bits are the angle to 2^-33 of a turn;
 //   - cosine and sine of a row are computed once, for all of its heads, in
 //     shared memory;
-//   - a thread keeps to one run of pairs of a head, so that its addresses need
-//     no division.
+//   - a thread keeps to one unit of a head, so that its addresses need no
+//     division; a CTA takes as many rows as give its threads four units each
+//     (more rows leave the last CTAs alone: 46 and 52 us with 8 and 16 units
+//     where 4 take 42.5).
+//
+// Measured: q and k of 12800 rows, 32 + 8 heads of 128, bf16, half layout, 262
+// MB: 42.5 us, 0.91 of the measured copy rate (interleaved 0.75; fp32 0.98 and
+// 0.91); accesses of 2 bytes (33 pairs in 100 columns) 0.38, of 4 0.6 to 0.76:
+// those are bound by instructions; a step of 128 rows 4.1 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -10,8 +10,10 @@
 //
 // The walk itself needs two numbers a node, which are read at once.  A whole
 // row is read only for the sum after a rejection and for the last token, and
-// those rows are the kernel's bytes: HBM bounds it, and for few sequences the
-// chain from reads to sums to the next decision.  So
+// those rows are the kernel's bytes.  What bounds it is the chain: reads, sums,
+// the next decision, as often as a sequence has rejections, and the call lasts
+// as long as its longest sequence (64 trees: 14% of DRAM's rate, 29% of the
+// warps active).  So
 //   - a cluster of CTAs takes a sequence, a warp of it a run of the row; the
 //     sums of all runs go to the first CTA, which alone decides (one decision
 //     for all: no CTA can wait for one that took another turn);
@@ -19,10 +21,17 @@
 //     masses so far, and is made again where it is needed;
 //   - a thread's sum is a pair of floats, each addition's error kept (7
 //     instructions where a fixed-point sum takes 13 and the conversion to 64
-//     bits is slower still); its total, and all sums of threads, are integers
-//     in units of 2^-62, which do not depend on their order.
+//     bits is slower still: 69 us that way, 75 with the hardware's conversion,
+//     54 with pairs); its total, and all sums of threads, are integers in units
+//     of 2^-62, which do not depend on their order.  No fp64: this GPU has
+//     little of it.
 // Probabilities lie in [0, 1] (others are taken as 0 or 1) and a row's sum
 // below 2.
+//
+// Measured: one chain of 5 over 32000 tokens, fp32: 8.4 us (5.8 us with one
+// node and 1000 tokens: launch, two round trips of scalars, a row, the token);
+// 64 trees of up to 16 nodes over 131072, fp32: 46 us; 200 certain trees of up
+// to 7 over 50021, bf16: 20.5 us.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -37,10 +46,10 @@ using namespace pg;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;            // the most CTAs of a sequence
+constexpr int kCluster = 16;           // the most CTAs of a sequence
 constexpr int kRuns = kCluster * kWarps;
 constexpr int kResident = 4;           // CTAs of an SM
-static_assert(kRuns == 64, "a lane holds two runs' sums");
+constexpr int kLaneRuns = kRuns / 32;  // runs whose sums a lane holds
 constexpr float kUnit = 0x1p-62f;
 
 // x (|x| < 2) in units of 2^-62, below 2^-39 rounded towards 0.
@@ -350,7 +359,9 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
         cluster_sync();
         if (rank == 0 && warp == 0) {
             const int runs = ctas * kWarps;
-            total = (2 * lane < runs ? s_runs[2 * lane] : 0) + (2 * lane + 1 < runs ? s_runs[2 * lane + 1] : 0);
+            total = 0;
+#pragma unroll
+            for (int i = 0; i < kLaneRuns; i++) total += kLaneRuns * lane + i < runs ? s_runs[kLaneRuns * lane + i] : 0;
 #pragma unroll
             for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
             mass = total;
@@ -392,16 +403,26 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
     int run = 0;
     {
         const int runs = ctas * kWarps;
-        const uint64_t a = 2 * lane < runs ? s_runs[2 * lane] : 0, b = 2 * lane + 1 < runs ? s_runs[2 * lane + 1] : 0;
-        const uint64_t incl = scan(a + b, lane), all = __shfl_sync(0xffffffffu, incl, 31);
+        uint64_t mine[kLaneRuns], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kLaneRuns; i++) {
+            mine[i] = kLaneRuns * lane + i < runs ? s_runs[kLaneRuns * lane + i] : 0;
+            sum += mine[i];
+        }
+        const uint64_t incl = scan(sum, lane), all = __shfl_sync(0xffffffffu, incl, 31);
         left = min(times((uint64_t)fixed(__saturatef(sample)), all), all - 1);
         const int l = max(0, __ffs((int)__ballot_sync(0xffffffffu, left < incl)) - 1);
-        const uint64_t before = __shfl_sync(0xffffffffu, incl - a - b, l), first = __shfl_sync(0xffffffffu, a, l);
-        left -= before;
-        run = 2 * l;
-        if (left >= first) {
-            left -= first;
-            run++;
+        left -= __shfl_sync(0xffffffffu, incl - sum, l);
+        run = kLaneRuns * l;
+        bool on = true;
+#pragma unroll
+        for (int i = 0; i < kLaneRuns - 1; i++) {
+            const uint64_t one = __shfl_sync(0xffffffffu, mine[i], l);
+            on &= left >= one;
+            if (on) {
+                left -= one;
+                run++;
+            }
         }
     }
     // a few neighbouring vectors of it a thread, whose sums say which thread has the token
@@ -454,6 +475,15 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
 
 template <bool BF16, bool DRAFT>
 cudaError_t launch(const VfParams &p, int ctas, cudaStream_t st) {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(verify_kernel<BF16, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.n_seqs * ctas));
     cfg.blockDim = dim3(kThreads);
@@ -470,8 +500,14 @@ cudaError_t launch(const VfParams &p, int ctas, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_verify(const VfParams &p, int num_sms, int64_t *ctas, cudaStream_t st) {
+    // As many CTAs a sequence as are resident at once, with 2048 tokens each at least: one chain over 32000 tokens takes 8.4
+    // us with 8 CTAs, 9.0 with 16; 16 trees of 16 nodes over 131072 25.5 us with 16, 29 with 8.  Trees with a draft's
+    // probabilities have several rejections one after the other in some sequences, whose rounds then are the time that the
+    // call takes: twice as many CTAs shorten those (64 such trees 46 against 52 us; 64 chains, which mostly end at
+    // their first rejection, 36 against 22 us the other way).
+    const int waves = p.draft && p.parents ? 2 : 1;
     int c = kCluster;
-    while (c > 1 && ((int64_t)p.n_seqs * c > kResident * num_sms || p.vocab < 2048 * c)) c /= 2;
+    while (c > 1 && ((int64_t)p.n_seqs * c > waves * kResident * num_sms || p.vocab < 2048 * c)) c /= 2;
     *ctas = (int64_t)p.n_seqs * c;
     if (p.bf16) return p.draft ? launch<true, true>(p, c, st) : launch<true, false>(p, c, st);
     return p.draft ? launch<false, true>(p, c, st) : launch<false, false>(p, c, st);
