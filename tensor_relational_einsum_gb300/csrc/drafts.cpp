@@ -204,30 +204,36 @@ extern "C" ea_status ea_cache_keep(const ea_cache *caches, int32_t n_caches, con
             if (c->n_pages != f->n_pages || c->page != f->page || c->heads != f->heads || c->dim != f->dim)
                 return set_error(EA_ERR_SHAPE, "%s: caches of different extents", what);
             if (c->device != f->device) return set_error(EA_ERR_ARG, "%s: caches on different devices", what);
-            if (in_batch(batch, c) || in_cache(c, path, path_bytes) || in_cache(c, counts, n * 4) || in_cache(c, lens_out, n * 4))
-                return set_error(EA_ERR_ARG, "%s: the batch, the path or the lengths lie in a cache", what);
         }
-        if (n_caches > 1) {
-            // All arrays by address, so that neighbours tell of overlaps: layers are mostly made in order, and then this
-            // insertion moves nothing.
-            struct Span {
-                const char *at;
-                size_t bytes;
-            };
-            std::vector<Span> by;
-            by.reserve(4 * (size_t)n_caches);
-            const size_t cells = cache_bytes(f), scales = f->ks ? cells / f->dim : 0;
-            auto put = [&](const void *p, size_t bytes) {
-                size_t i = by.size();
-                by.push_back({(const char *)p, bytes});
-                for (; i > 0 && by[i - 1].at > (const char *)p; i--) std::swap(by[i - 1], by[i]);
-            };
-            for (int i = 0; i < n_caches; i++) put(caches[i]->k, cells);
-            for (int i = 0; i < n_caches; i++) put(caches[i]->v, cells);
-            for (int i = 0; scales && i < n_caches; i++) put(caches[i]->ks, scales);
-            for (int i = 0; scales && i < n_caches; i++) put(caches[i]->vs, scales);
-            for (size_t i = 1; i < by.size(); i++)
-                if (by[i - 1].at + by[i - 1].bytes > by[i].at) return set_error(EA_ERR_ARG, "%s: caches overlap", what);
+        // All arrays of the caches by address, so that neighbours tell of overlaps: layers are mostly made in order, and then
+        // this insertion moves nothing.
+        struct Span {
+            const char *at;
+            size_t bytes;
+        };
+        std::vector<Span> by;
+        by.reserve(4 * (size_t)n_caches);
+        const size_t cells = cache_bytes(f), scales = f->ks ? cells / (size_t)f->dim / (f->format == EA_CACHE_BF16 ? 2 : 1) : 0;
+        auto put = [&](const void *p, size_t bytes) {
+            size_t i = by.size();
+            by.push_back({(const char *)p, bytes});
+            for (; i > 0 && by[i - 1].at > (const char *)p; i--) std::swap(by[i - 1], by[i]);
+        };
+        for (int i = 0; i < n_caches; i++) put(caches[i]->k, cells);
+        for (int i = 0; i < n_caches; i++) put(caches[i]->v, cells);
+        for (int i = 0; scales && i < n_caches; i++) put(caches[i]->ks, scales);
+        for (int i = 0; scales && i < n_caches; i++) put(caches[i]->vs, scales);
+        for (size_t i = 1; i < by.size(); i++)
+            if (by[i - 1].at + by[i - 1].bytes > by[i].at) return set_error(EA_ERR_ARG, "%s: caches overlap", what);
+        const Span apart[] = {{(const char *)batch->pages, ((n - 1) * batch->page_stride + batch->max_pages) * 4},
+                              {(const char *)batch->starts, (n + 1) * 4}, {(const char *)batch->lens, n * 4},
+                              {(const char *)path, path_bytes}, {(const char *)counts, n * 4}, {(const char *)lens_out, n * 4}};
+        for (const Span &x : apart) {
+            if (!x.at) continue;
+            // the first array that ends beyond x's beginning
+            const auto i = std::partition_point(by.begin(), by.end(), [&](const Span &y) { return y.at + y.bytes <= x.at; });
+            if (i != by.end() && i->at < x.at + x.bytes)
+                return set_error(EA_ERR_ARG, "%s: the batch, the path or the lengths lie in a cache", what);
         }
         if (lens_out && (in_batch(batch, lens_out, n * 4) || overlap(lens_out, n * 4, path, path_bytes) || overlap(lens_out, n * 4, counts, n * 4)))
             return set_error(EA_ERR_ARG, "%s: lens_out overlaps the batch, the path or the counts", what);

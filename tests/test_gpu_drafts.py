@@ -258,6 +258,8 @@ ROTARY = [
     (9, 3, 256, 256, 0),
     (2, 1, 100, 66, 34),
     (65, 1, 16, 12, 4),
+    (2, 1, 1501, 10, 3),    # more columns to copy than a CTA has threads for
+    (1, 2, 2056, 256, 1800),
 ]
 
 
