@@ -63,8 +63,11 @@ __device__ __forceinline__ int64_t fixed(float x) {
 // The product of two such numbers, rounded down.
 __device__ __forceinline__ uint64_t times(uint64_t a, uint64_t b) { return __umul64hi(a << 1, b << 1); }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // The address of a shared variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t shared_of(const void *p, uint32_t rank) {
@@ -200,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
     __shared__ int s_up[kPgNodes], s_token[kPgNodes], s_path[kPgNodes], s_out[kPgNodes];
     __shared__ float s_t[kPgNodes], s_d[kPgNodes], s_u[kPgNodes], s_was[kPgNodes];
     constexpr int kAhead = 2;                   // vectors of a lane in flight of two rows; twice as many of one
+    cluster_arrive();                           // waited for before the first store to another CTA: that CTA has begun
     uint32_t rank, ctas;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
@@ -283,6 +287,8 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
         }
         return false;
     };
+    __syncwarp();
+    cluster_wait();  // behind the scalars' reads: all CTAs have long arrived
     for (;;) {
         if (rank == 0 && threadIdx.x == 0) {
             s_path[0] = 0;

@@ -1,0 +1,42 @@
+"""GPU tests of the operators around drafted tokens at the ends of their
+ranges: clusters of every size with many rejections at a node, sequences
+without rows, sums and scales out of the ordinary.  Definitions and tolerances
+as in test_gpu_drafts.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import cache_util as cu
+import drafts_util as du
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+from test_gpu_cache import relation  # noqa: E402
+from test_gpu_drafts import expect, run_verify, verify_batch  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from tensor_relational_einsum_gb300.build import build
+    build()
+    yield
+    from tensor_relational_einsum_gb300.relation import check
+    check()
+
+
+# ------------------------------------------------------------ verification
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("vocab", [2048, 4097, 20011, 40000])
+def test_verify_sequences_without_rows_in_clusters(vocab, drafts):
+    """Empty sequences, whose first CTA has its first order for the others at once, among others: clusters of 1 to 16."""
+    from tensor_relational_einsum_gb300.relation import check
+    b, trees, parents, target, draft, tokens, accept, sample = verify_batch([0, 0, 3, 0, 1, 0, 0, 5, 0], vocab, torch.float32, drafts,
+                                                                            "random", 31)
+    for _ in range(5):
+        got = run_verify(b, parents, target, draft, tokens, accept, sample)
+        check()
+        expect(b, trees, target, draft, tokens, accept, sample, got)
