@@ -40,3 +40,24 @@ def test_verify_sequences_without_rows_in_clusters(vocab, drafts):
         got = run_verify(b, parents, target, draft, tokens, accept, sample)
         check()
         expect(b, trees, target, draft, tokens, accept, sample, got)
+
+
+def rejections(parents, path):
+    """How many children of each accepted node are asked in vain."""
+    path = list(path)
+    return [sum(p == v and c < after for c, p in enumerate(parents)) for v, after in zip(path, path[1:] + [len(parents)])]
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ns", [[24, 17, 30], [128, 64]])
+@pytest.mark.parametrize("vocab", [9000, 20011, 40000])
+def test_verify_with_many_rejections_in_clusters(vocab, ns, dtype, drafts):
+    """Drafts unlike the target, in clusters of 4, 8 and 16 CTAs: masses of many subtractions go from CTA to CTA."""
+    from tensor_relational_einsum_gb300.relation import check
+    b, trees, parents, target, draft, tokens, accept, sample = verify_batch(ns, vocab, dtype, drafts, "star", 41, branch_noise=4.0, sharp=0.5)
+    got = run_verify(b, parents, target, draft, tokens, accept, sample)
+    check()
+    expect(b, trees, target, draft, tokens, accept, sample, got)
+    path, counts = got[0].cpu().numpy(), got[1].tolist()
+    assert max(max(rejections(trees[i], path[i, :counts[i]])) for i in range(len(ns))) >= 16
