@@ -599,7 +599,9 @@ typedef struct {
  * everywhere, or the sequence has no rows (counts 0).  Nodes with another
  * parent than an accepted node, and further roots, are not asked.
  *   target  f32 or bf16 [rows.., vocab]: values in [0, 1] (others are taken as
- *           0 or 1, NaN as 0), a row's sum below 2;
+ *           0 or 1, NaN as 0).  Where a row has to be summed and its sum is 2
+ *           or more, the device error word is raised; the sequence keeps what
+ *           it has accepted before and picked is -1;
  *   draft   as target, or NULL: the drafted tokens are certain (probability 1).
  * Tests, and rests and sums relative to their largest terms, are exact to
  * about 2^-45 (what lies below 2^-61 counts as 0); the results are the same on

@@ -25,8 +25,9 @@
 //     54 with pairs); its total, and all sums of threads, are integers in units
 //     of 2^-62, which do not depend on their order.  No fp64: this GPU has
 //     little of it.
-// Probabilities lie in [0, 1] (others are taken as 0 or 1) and a row's sum
-// below 2.
+// Probabilities lie in [0, 1] (others are taken as 0 or 1).  A row's sum has
+// room below 2; from 2 on (logits, say) all additions stop at kTop, whatever
+// their order, the walk ends and the error word is raised.
 //
 // Measured: one chain of 5 over 32000 tokens, fp32: 8.4 us (5.8 us with one
 // node and 1000 tokens: launch, two round trips of scalars, a row, the token);
@@ -51,6 +52,7 @@ constexpr int kRuns = kCluster * kWarps;
 constexpr int kResident = 4;           // CTAs of an SM
 constexpr int kLaneRuns = kRuns / 32;  // runs whose sums a lane holds
 constexpr float kUnit = 0x1p-62f;
+constexpr uint64_t kTop = ((uint64_t)1 << 63) - 1;  // a sum of 2 or more
 
 // x (|x| < 2) in units of 2^-62, below 2^-39 rounded towards 0.
 __device__ __forceinline__ int64_t fixed(float x) {
@@ -238,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
     // the first CTA's first thread: where the walk is
     int node = 0, next = 1, kept = 1, rejected = 0, outs = 0;
     bool have = false;                          // the runs' sums are those of (node, rejected)
+    bool over = false;                          // a row's sum was out of range: nothing more
     uint64_t mass = 0, total = 0;
     // Goes on until a row's sums are needed (true) or the next token is to be taken (false).
     auto walk = [&]() {
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
     for (;;) {
         if (rank == 0 && threadIdx.x == 0) {
             s_path[0] = 0;
-            const bool more = s.n > 0 && walk();
+            const bool more = s.n > 0 && !over && walk();
             s_order.node = more ? node : -1;
             s_order.first = s.first;
             s_order.rejected = rejected;
@@ -357,9 +360,9 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
             }
         }
         __syncwarp();
-        uint64_t sum = fixed(part);
+        uint64_t sum = part.h < 2.f && part.h + part.l < 2.f ? fixed(part) : kTop;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = 16; o; o >>= 1) sum = min(sum + __shfl_xor_sync(0xffffffffu, sum, o), kTop);
         if (lane == 0) put_u64(shared_of(&s_runs[rank * kWarps + warp], 0), sum);
         __syncwarp();
         cluster_sync();
@@ -367,10 +370,12 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
             const int runs = ctas * kWarps;
             total = 0;
 #pragma unroll
-            for (int i = 0; i < kLaneRuns; i++) total += kLaneRuns * lane + i < runs ? s_runs[kLaneRuns * lane + i] : 0;
+            for (int i = 0; i < kLaneRuns; i++) total = min(total + (kLaneRuns * lane + i < runs ? s_runs[kLaneRuns * lane + i] : 0), kTop);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-            mass = total;
+            for (int o = 16; o; o >>= 1) total = min(total + __shfl_xor_sync(0xffffffffu, total, o), kTop);
+            over = total == kTop;
+            if (over && lane == 0) batch_fail(p.err);
+            mass = over ? 0 : total;
             if constexpr (!DRAFT) {
                 if (lane == 0)  // the tokens that were rejected at this node, each once
                     for (int i = 0; i < outs; i++) mass -= min(mass, (uint64_t)fixed(s_was[i]));

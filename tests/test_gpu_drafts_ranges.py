@@ -61,3 +61,40 @@ def test_verify_with_many_rejections_in_clusters(vocab, ns, dtype, drafts):
     expect(b, trees, target, draft, tokens, accept, sample, got)
     path, counts = got[0].cpu().numpy(), got[1].tolist()
     assert max(max(rejections(trees[i], path[i, :counts[i]])) for i in range(len(ns))) >= 16
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab,value", [(64, 0.5), (300, 1.0), (20011, 1.0), (40000, 2.0 ** -12), (131072, 7.0), (5000, 4.0 / 5000)])
+def test_verify_reports_sums_out_of_range(vocab, value, dtype):
+    """Rows that add up to 2 and more, to multiples of 4 among them (logits by mistake): the error word, no token, what was
+    accepted before stays; the sequence beside it as it should be."""
+    from tensor_relational_einsum_gb300 import EaError
+    from tensor_relational_einsum_gb300.relation import check
+    for kind in ("chain", "star"):
+        for drafts in (True, False):
+            b, trees, parents, target, draft, tokens, accept, sample = verify_batch([3, 2, 4], vocab, dtype, drafts, kind, 44)
+            want, ahead = run_verify(b, parents, target, draft, tokens, accept, sample), int(b.starts[1])
+            check()
+            accept[ahead + 1] = 1.0
+            tokens[ahead + 1] = 5
+            if drafts:
+                draft[ahead, 5] = 1.0  # u d = 1 >= r: a rejection
+            target[ahead:ahead + 2] = value
+            target[ahead, 5] = 0.0
+            path, counts, picked = run_verify(b, parents, target, draft, tokens, accept, sample)
+            with pytest.raises(EaError):
+                check()
+            assert path[1].tolist() == [0] + [-1] * (path.shape[1] - 1) and counts[1].item() == 1 and picked[1].item() == -1
+            for i in (0, 2):
+                assert torch.equal(path[i], want[0][i]) and counts[i] == want[1][i] and picked[i] == want[2][i]
+
+
+def test_verify_sums_just_below_two():
+    """1.5 and 1.96875 are in range (two halves more than the distribution that they are scaled from)."""
+    from tensor_relational_einsum_gb300.relation import check
+    from test_gpu_drafts import one
+    for n, x in ((3, 0.5), (63, 0.03125)):
+        row = [x] * n + [0.0] * (70 - n)
+        for s in (0.0, 0.25, 0.5, 0.99609375):
+            assert one([row], None, [0], [-1], [0.0], s) == ([0], int(s * n))
+    check()
