@@ -109,7 +109,7 @@ extern "C" ea_status ea_rotary(const ea_rotary_opts *opts, const ea_page_batch *
         p.err = c->err;
         int64_t ctas = 0;
         if (rows > 0) {
-            cudaError_t e = launch_rotary(p, &ctas, (cudaStream_t)stream);
+            cudaError_t e = launch_rotary(p, c->num_sms, &ctas, (cudaStream_t)stream);
             if (e != cudaSuccess) return cuda_error(e, what);
         }
         note_launch(kRotary, ctas > 0, ctas);

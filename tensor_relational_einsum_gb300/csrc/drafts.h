@@ -24,7 +24,7 @@ struct RoParams {
     int *err;
     uint64_t turn[kRoPairs];   // turns a position, in units of 2^-64
 };
-cudaError_t launch_rotary(const RoParams &p, int64_t *ctas, cudaStream_t st);
+cudaError_t launch_rotary(const RoParams &p, int num_sms, int64_t *ctas, cudaStream_t st);
 
 struct VfParams {
     const char *target, *draft;    // [rows][vocab]; draft NULL: tokens that are certain

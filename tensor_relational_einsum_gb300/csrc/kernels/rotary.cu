@@ -254,36 +254,36 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 }
 
 template <bool F32, bool HALF, int V>
-cudaError_t launch(const RoParams &p, int64_t *ctas, cudaStream_t st) {
+cudaError_t launch(const RoParams &p, int num_sms, int64_t *ctas, cudaStream_t st) {
     int turned, copied;
     units_of<Unit<F32, HALF, V>, V>(p, &turned, &copied);
     const int64_t items = (int64_t)(p.heads[0] + p.heads[1]) * (turned + copied);  // of a row
     int rows_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRows, kItems * kThreads / items));
-    while (rows_cta > 1 && (p.rows + rows_cta - 1) / rows_cta < 2 * 152) rows_cta--;
+    while (rows_cta > 1 && (p.rows + rows_cta - 1) / rows_cta < 2 * num_sms) rows_cta--;
     *ctas = (p.rows + rows_cta - 1) / rows_cta;
     rotary_kernel<F32, HALF, V><<<(unsigned)*ctas, kThreads, (size_t)rows_cta * (p.dims / 2) * sizeof(float2), st>>>(p, rows_cta);
     return cudaGetLastError();
 }
 
 template <bool F32, bool HALF>
-cudaError_t launch_v(const RoParams &p, int64_t *ctas, cudaStream_t st) {
+cudaError_t launch_v(const RoParams &p, int num_sms, int64_t *ctas, cudaStream_t st) {
     // the widest accesses that all units' addresses are aligned to
     constexpr int most = 16 / (F32 ? 4 : 2) / (HALF ? 1 : 2);
     const int run = HALF ? 1 : 2;  // columns of a pair that lie together
     int v = most;
     while (v > 1 && ((p.dims / 2) % v || p.offset % (run * v) || p.dim % (run * v))) v /= 2;
     if constexpr (most >= 8)
-        if (v == 8) return launch<F32, HALF, 8>(p, ctas, st);
+        if (v == 8) return launch<F32, HALF, 8>(p, num_sms, ctas, st);
     if constexpr (most >= 4)
-        if (v == 4) return launch<F32, HALF, 4>(p, ctas, st);
-    return v == 2 ? launch<F32, HALF, 2>(p, ctas, st) : launch<F32, HALF, 1>(p, ctas, st);
+        if (v == 4) return launch<F32, HALF, 4>(p, num_sms, ctas, st);
+    return v == 2 ? launch<F32, HALF, 2>(p, num_sms, ctas, st) : launch<F32, HALF, 1>(p, num_sms, ctas, st);
 }
 
 }  // namespace
 
-cudaError_t launch_rotary(const RoParams &p, int64_t *ctas, cudaStream_t st) {
-    if (p.f32) return p.half ? launch_v<true, true>(p, ctas, st) : launch_v<true, false>(p, ctas, st);
-    return p.half ? launch_v<false, true>(p, ctas, st) : launch_v<false, false>(p, ctas, st);
+cudaError_t launch_rotary(const RoParams &p, int num_sms, int64_t *ctas, cudaStream_t st) {
+    if (p.f32) return p.half ? launch_v<true, true>(p, num_sms, ctas, st) : launch_v<true, false>(p, num_sms, ctas, st);
+    return p.half ? launch_v<false, true>(p, num_sms, ctas, st) : launch_v<false, false>(p, num_sms, ctas, st);
 }
 
 }  // namespace ea

@@ -15,3 +15,10 @@ def test_no_store_to_another_cta_before_the_first_cluster_barrier():
     arrive, wait = (body.find(f"cluster_{x}()") for x in ("arrive", "wait"))
     sync = body.find("cluster_sync()")
     assert 0 <= sync < store or 0 <= arrive < wait < store
+
+
+def test_no_launch_assumes_a_number_of_sms():
+    """Launches take the number of SMs from the device, not one GPU's as a constant."""
+    for name in sorted(os.listdir(CSRC)):
+        code = re.sub(r"//.*", "", open(os.path.join(CSRC, name)).read())
+        assert not re.search(r"\b(148|152|160)\b", code), name
