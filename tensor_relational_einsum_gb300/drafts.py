@@ -75,6 +75,8 @@ def rotary(q: Relation, k: Relation | None, plan: Rotary, batch: PageBatch | Non
     sequence and of negative positions stay as they are.  ``backward``: the
     transposed rotation, which takes the gradients of the results to those of
     q and k.  Returns the results."""
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
     if k is not None and (q_out is None) != (k_out is None):
         raise ValueError("give both q_out and k_out, or neither")
     q_out = q if q_out is None else q_out

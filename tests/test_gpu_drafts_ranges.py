@@ -98,3 +98,13 @@ def test_verify_sums_just_below_two():
         for s in (0.0, 0.25, 0.5, 0.99609375):
             assert one([row], None, [0], [-1], [0.0], s) == ([0], int(s * n))
     check()
+
+
+# ------------------------------------------------------------------ rotary
+
+def test_rotary_refuses_a_result_without_its_operand():
+    from tensor_relational_einsum_gb300 import Rotary, rotary
+    q, o = (relation(torch.zeros(2, 1, 64, device="cuda")) for _ in range(2))
+    at = torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        rotary(q, None, Rotary(64), positions=at, q_out=q, k_out=o)
