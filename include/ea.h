@@ -530,8 +530,10 @@ ea_status ea_cache_attention(ea_cache cache, const ea_page_batch *batch, ea_rela
  * In ea_cache_attention a tree's row keeps the positions before the
  * sequence's new ones (t < lens[i] - n_i) and, of those, its own and its
  * ancestors'; `causal` has no meaning.  Chains (parents j - 1) give what
- * causal rows get.  A dropped node's key may hold anything, its value must be
- * finite, as above. */
+ * causal rows get.  A dropped node's key may be an infinity or NaN (8-bit: NaN
+ * codes, scale byte 255), its value must be finite, as above.  Over 8-bit
+ * cells it is one of the keys of its tile: a scale more than 2^21 times a kept
+ * key's costs that key bits, as above. */
 
 #define EA_ROTARY_INTERLEAVED 0 /* pairs (2 i, 2 i + 1) */
 #define EA_ROTARY_HALF 1        /* pairs (i, i + dims / 2) */

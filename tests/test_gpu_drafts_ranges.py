@@ -14,8 +14,8 @@ import drafts_util as du
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
-from test_gpu_cache import relation  # noqa: E402
-from test_gpu_drafts import expect, run_verify, verify_batch  # noqa: E402
+from test_gpu_cache import fill, nan_cache, on_gpu, relation, values  # noqa: E402
+from test_gpu_drafts import expect, parents_of, run_verify, verify_batch  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -98,6 +98,48 @@ def test_verify_sums_just_below_two():
         for s in (0.0, 0.25, 0.5, 0.99609375):
             assert one([row], None, [0], [-1], [0.0], s) == ([0], int(s * n))
     check()
+
+
+# ---------------------------------------------------------- tree attention
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,group", [(3, 4), (7, 4), (40, 1), (40, 4), (63, 4), (70, 4)])
+@pytest.mark.parametrize("spoil", ["codes", "byte", "large"])
+def test_dropped_keys_of_8_bit_cells(spoil, n, group, dim):
+    """Leaves whose keys are NaN, or 2^18 times larger than the others: no other row is touched.  12 to 280 rows: both
+    kernels, and expanded pages."""
+    from tensor_relational_einsum_gb300 import cache_attention
+    from tensor_relational_einsum_gb300.relation import check
+    b = cu.Batch([(n, 150), (n, n + 90)], 16, seed=10)
+    c = nan_cache(b, 1, dim, "e4m3")
+    rng = np.random.default_rng(11)
+    held = fill(c, b, rng)
+    trees, parents = parents_of(b, "star")
+    # the kept keys' scales differ by less than 2^3: 2^20 times the largest would lie beyond the 2^21 that are exact
+    large = int(c.k_scale[c.k_scale < 255].max()) + 18
+    for i, t in enumerate(b.lens):
+        pg, sl = b.places(i)
+        for j in (n - 1, n // 2):
+            at = (int(pg[t - n + j]), slice(None), int(sl[t - n + j]))
+            if spoil == "codes":
+                c.k.view(torch.uint8)[at] = 0x7F
+            elif spoil == "byte":
+                c.k_scale[at] = 255
+            else:
+                c.k_scale[at] = large
+    q = values(rng, (b.rows, group, dim))
+    out = cache_attention(relation(torch.from_numpy(q).to(torch.bfloat16).cuda()), c, on_gpu(b, max_new=n), parents=parents)
+    check()
+    got = out.to_dense().double().cpu().numpy()
+    for i, t in enumerate(b.lens):
+        for j in range(n):
+            if j in (n - 1, n // 2):
+                continue
+            keep = du.kept_positions(trees[i], j, n, int(t))
+            for h in range(group):
+                o, _, _, big, slack = cu.softmax_attention(q[i * n + j:i * n + j + 1, h], held[i][0][keep, 0], held[i][1][keep, 0], None,
+                                                           1 / math.sqrt(dim), False)
+                assert np.all(np.abs(got[i * n + j, h] - o[0]) <= cu.out_bound(o, big, slack, len(keep))[0]), (i, j, h)
 
 
 # ------------------------------------------------------------------ rotary
