@@ -65,6 +65,29 @@
 // chains, whose first tile of rows has fewer keys; one sequence of 200001
 // positions, 32 nodes: 152 us, 0.79 of the measured copy rate.
 //
+// e4m3: what orders the last read of a shared place before its next write, for
+// parts of any lengths, n[0] and n[1] different or 0 too (t: key tiles in the
+// CTA's order; p: parts):
+//   raw K, raw V, raw scales  read into registers before the four arrivals on
+//              raw_empty (volatile reads); the next copy waits for those
+//   K, V stage converted behind k_empty, v_empty: a commit behind the tile's
+//              last product of either X, which tracks all earlier ones
+//   top        two tiles' worth: written at t + 2 behind top_full of t + 1,
+//              on which every warp arrives after its reads at t
+//   references of t, in a ring of 2 ST: written at t + 2 ST behind k_empty of
+//              t + ST, whose scores are issued behind P of all tiles before;
+//              each X reads its tile's before it arrives with P
+//   Q          copied behind q_empty (the part's last scores of X), rewritten
+//              behind q_full, multiplied behind q_ready
+//   Q's powers of p, by the parity of X's parts: written at X's next but one,
+//              behind q_full and so behind the last scores of X's next, which
+//              are issued behind P of p's first tile, where they are read
+//   S / P of X scores are issued behind the product that reads P, in order
+//   A of X     the first product of the next part waits for its P, which X
+//              writes behind the output; a rescale waits for the next scores,
+//              whose commit tracks the product before them too
+//   parts      a ring of kParts, freed by all 14 warps that read them
+//
 // Every mbarrier wait is bounded (2 s); on time-out the kernel raises the
 // device error word, all roles leave their loops, the copies and MMAs in
 // flight are waited for and TMEM is freed before the CTA exits.
@@ -91,14 +114,19 @@ constexpr int kMaxStages = 4;
 constexpr int kWhole = 1024;      // sequences of up to so many positions are not cut
 
 // Register split (setmaxnreg): the softmax threads keep a row of 128 scores.
-// The shares add up to the launch's registers exactly.
+// The shares add up to the launch's registers exactly.  e4m3: 168 / 72 / 104
+// and 176 / 72 / 88 take the same time within 6% either way (at head dim 128
+// 40 sequences of 2400, 64 rows: 175 and 187 us; at 64 115 and 113 us).  A ring
+// of V that kept its stage in a register of its own gave results that
+// differed from run to run with 80 and 88 for the converting warps and none
+// that did with 96 and 104, so they have 104, with room to spare.
 template <bool E4M3>
 struct Regs {
     static constexpr int THREADS = E4M3 ? 512 : 384;
     static constexpr int LAUNCH = E4M3 ? 128 : 168;
-    static constexpr int SOFTMAX = E4M3 ? 176 : 208;
+    static constexpr int SOFTMAX = E4M3 ? 168 : 208;
     static constexpr int CTL = E4M3 ? 72 : 88;
-    static constexpr int CONV = 88;
+    static constexpr int CONV = 104;
     static_assert(128 * (2 * SOFTMAX + CTL + (E4M3 ? CONV : 0)) <= THREADS * LAUNCH, "register split");
 };
 
@@ -188,6 +216,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
+}
+
+// Reads of raw tiles, in order with the arrivals that give them back.
+__device__ __forceinline__ uint4 lds_16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_1(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -794,15 +834,16 @@ cache_chunks_kernel(const __grid_constant__ PgAttn p, const __grid_constant__ Pg
                         ok = false;
                         break;
                     }
-                    // all of the lane's codes first: the raw tile is free, and no load waits behind a store
-                    const uint8_t *raw = smem + C::RAW_OFF + (h * C::NR + rs) * C::RAW + row0 * D;
+                    // all of the lane's codes first: then the raw tile is free, and no load waits behind a store
+                    const uint32_t raw = smem_u32(smem + C::RAW_OFF + (h * C::NR + rs) * C::RAW + row0 * D);
                     uint4 v[CPR];
 #pragma unroll
-                    for (int i = 0; i < CPR; i++) v[i] = *reinterpret_cast<const uint4 *>(raw + (i * 32 + lane) * 16);
+                    for (int i = 0; i < CPR; i++) v[i] = lds_16(raw + (i * 32 + lane) * 16);
                     uint32_t kb = 0, vb = 0;
                     if (h == 0) {
-                        kb = smem[C::RSC_OFF + rs * 2 * kKeys + row0 + lane];
-                        vb = smem[C::RSC_OFF + rs * 2 * kKeys + kKeys + row0 + lane];
+                        const uint32_t sc = smem_u32(smem + C::RSC_OFF + rs * 2 * kKeys + row0 + lane);
+                        kb = lds_1(sc);
+                        vb = lds_1(sc + kKeys);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->raw_empty[h][rs]);

@@ -15,6 +15,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from test_gpu_cache import fill, nan_cache, on_gpu, relation, values  # noqa: E402
+from test_gpu_cache_ranges import scaled_fill  # noqa: E402
 from test_gpu_drafts import expect, parents_of, run_verify, verify_batch  # noqa: E402
 
 
@@ -140,6 +141,40 @@ def test_dropped_keys_of_8_bit_cells(spoil, n, group, dim):
                 o, _, _, big, slack = cu.softmax_attention(q[i * n + j:i * n + j + 1, h], held[i][0][keep, 0], held[i][1][keep, 0], None,
                                                            1 / math.sqrt(dim), False)
                 assert np.all(np.abs(got[i * n + j, h] - o[0]) <= cu.out_bound(o, big, slack, len(keep))[0]), (i, j, h)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group,n,kv", [(3, 85, 8), (4, 16, 8), (4, 63, 8), (8, 31, 4), (1, 127, 4)])
+def test_8_bit_runs_give_the_same_bits(group, n, kv, dim):
+    """Raw 8-bit pages, scales that differ between sequences, items of one and two row tiles: 150 runs of one call, next to
+    copies on another stream, give the same outputs, maxima and sums; trees and rows in order."""
+    from tensor_relational_einsum_gb300 import cache_attention
+    from tensor_relational_einsum_gb300.relation import check
+    rng = np.random.default_rng(38)
+    seqs = [(int(x), int(x + t)) for x, t in zip(rng.integers(max(1, n // 2), n + 1, size=16), rng.integers(0, 1500, size=16))]
+    seqs[3] = (n, 2500)
+    b = cu.Batch(seqs, 32, before=1)
+    c = nan_cache(b, kv, dim, "e4m3")
+    scaled_fill(c, b, rng)
+    q = relation(torch.from_numpy(values(rng, (b.rows, kv * group, dim))).to(torch.bfloat16).cuda())
+    _, parents = parents_of(b, "random")
+    batch, side = on_gpu(b, max_new=n), torch.cuda.Stream()
+    other = [torch.zeros(1 << 24, device="cuda") for _ in range(2)]
+    for tree in (parents, None):
+        out = torch.zeros(b.rows, kv * group, dim, dtype=torch.bfloat16, device="cuda")
+        m, l = (torch.zeros(b.rows, kv * group, device="cuda") for _ in range(2))
+        got, first, differ = [relation(t) for t in (out, m, l)], None, torch.zeros((), dtype=torch.bool, device="cuda")
+        for i in range(150):
+            if i % 8 == 0:
+                with torch.cuda.stream(side):
+                    other[0].copy_(other[1])
+            cache_attention(q, c, batch, out=got[0], m_out=got[1], l_out=got[2], parents=tree)
+            if first is None:
+                first = [t.clone() for t in (out, m, l)]
+            for t, w in zip((out, m, l), first):
+                differ |= (t != w).any()
+        assert not differ.item()
+    check()
 
 
 # ------------------------------------------------------------------ rotary
