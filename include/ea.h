@@ -606,8 +606,8 @@ typedef struct {
  *           it has accepted before and picked is -1;
  *   draft   as target, or NULL: the drafted tokens are certain (probability 1).
  * Tests, and rests and sums relative to their largest terms, are exact to
- * about 2^-45 (what lies below 2^-61 counts as 0); the results are the same on
- * every run.  Of `batch` only
+ * about 2^-45 for each rejection before them at the node (what lies below
+ * 2^-61 counts as 0); the results are the same on every run.  Of `batch` only
  * starts, n_seqs and max_new are read; at most 128 nodes a sequence.
  * Errors: EA_ERR_ARG, EA_ERR_SHAPE, EA_ERR_PARTITION, EA_ERR_DTYPE,
  * EA_ERR_UNSUPPORTED (trees, vocabulary). */

@@ -12,8 +12,8 @@
 // row is read only for the sum after a rejection and for the last token, and
 // those rows are the kernel's bytes.  What bounds it is the chain: reads, sums,
 // the next decision, as often as a sequence has rejections, and the call lasts
-// as long as its longest sequence (64 trees: 14% of DRAM's rate, 29% of the
-// warps active).  So
+// as long as its longest sequence (64 trees: 16% of DRAM's rate, 38% of the
+// warps active, which wait at a barrier half of their time).  So
 //   - a cluster of CTAs takes a sequence, a warp of it a run of the row; the
 //     sums of all runs go to the first CTA, which alone decides (one decision
 //     for all: no CTA can wait for one that took another turn);
@@ -29,10 +29,13 @@
 // room below 2; from 2 on (logits, say) all additions stop at kTop, whatever
 // their order, the walk ends and the error word is raised.
 //
-// Measured: one chain of 5 over 32000 tokens, fp32: 8.4 us (5.8 us with one
-// node and 1000 tokens: launch, two round trips of scalars, a row, the token);
-// 64 trees of up to 16 nodes over 131072, fp32: 46 us; 200 certain trees of up
-// to 7 over 50021, bf16: 20.5 us.
+// Measured, in a graph on the same inputs: one chain of 5 over 32000 tokens,
+// fp32: 8.7 us (6.1 us with one node and 1000 tokens: launch, two round trips
+// of scalars, a row, the token); 64 trees of up to 16 nodes over 131072, fp32:
+// 47 us (56 us with inputs that change, whose rows L2 does not hold); 200
+// certain trees of up to 7 over 50021, bf16: 21 us: 8 with one node and 1000
+// tokens, 7 more for the row's sum and the search, 7 for the walk over the
+// nodes.  The first barrier is 0.3 to 0.8 us of these.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -511,7 +514,8 @@ cudaError_t launch(const VfParams &p, int ctas, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_verify(const VfParams &p, int num_sms, int64_t *ctas, cudaStream_t st) {
-    // As many CTAs a sequence as are resident at once, with 2048 tokens each at least: one chain over 32000 tokens takes 8.4
+    // As many CTAs a sequence as are resident at once, with 2048 tokens each at least (figures without the kernel's first
+    // barrier, which costs both sides the same): one chain over 32000 tokens takes 8.4
     // us with 8 CTAs, 9.0 with 16; 16 trees of 16 nodes over 131072 25.5 us with 16, 29 with 8.  Trees with a draft's
     // probabilities have several rejections one after the other in some sequences, whose rounds then are the time that the
     // call takes: twice as many CTAs shorten those (64 such trees 46 against 52 us; 64 chains, which mostly end at
