@@ -12,6 +12,7 @@ namespace {
 // The batch's rows, without its pages: what rotation and verification read.
 ea_status rows_args(const char *what, const ea_page_batch *b, int64_t rows, bool lens) {
     if (!b || !b->starts || (lens && !b->lens)) return set_error(EA_ERR_ARG, "%s: NULL batch or batch array", what);
+    if (off_4({b->starts, b->lens})) return set_error(EA_ERR_ARG, "%s: the batch's arrays must be aligned to 4 bytes", what);
     if (b->n_seqs < 1 || b->n_seqs > 65536) return set_error(EA_ERR_ARG, "%s: n_seqs %d out of [1, 65536]", what, b->n_seqs);
     if (b->max_new < 0) return set_error(EA_ERR_ARG, "%s: max_new %d", what, b->max_new);
     if (rows > INT32_MAX - 8191) return set_error(EA_ERR_UNSUPPORTED, "%s: more than %d rows", what, INT32_MAX - 8191);
@@ -43,6 +44,7 @@ extern "C" ea_status ea_rotary(const ea_rotary_opts *opts, const ea_page_batch *
         const ea_rotary_opts &o = *opts;
         if ((batch != nullptr) == (o.positions != nullptr)) return set_error(EA_ERR_ARG, "%s: give a batch or positions", what);
         if (o.parents && !batch) return set_error(EA_ERR_ARG, "%s: parents belong to a batch", what);
+        if (off_4({o.positions})) return set_error(EA_ERR_ARG, "%s: positions must be aligned to 4 bytes", what);
         if (o.layout != EA_ROTARY_INTERLEAVED && o.layout != EA_ROTARY_HALF) return set_error(EA_ERR_ARG, "%s: layout %d", what, o.layout);
         if (!std::isfinite(o.amplitude)) return set_error(EA_ERR_ARG, "%s: amplitude", what);
         RoParams p{};
@@ -124,6 +126,8 @@ extern "C" ea_status ea_verify_drafts(const ea_verify_opts *opts, const ea_page_
         if (!opts || !target || !opts->sample || !opts->path || !opts->counts || !opts->picked)
             return set_error(EA_ERR_ARG, "%s: NULL argument", what);
         const ea_verify_opts &o = *opts;
+        if (off_4({o.tokens, o.parents, o.accept, o.sample, o.path, o.counts, o.picked}))
+            return set_error(EA_ERR_ARG, "%s: arrays must be aligned to 4 bytes", what);
         int64_t rows, vocab;
         ea_status s = dense_rows(target, what, 1, &rows, &vocab, nullptr);
         if (s) return s;
@@ -197,6 +201,7 @@ extern "C" ea_status ea_cache_keep(const ea_cache *caches, int32_t n_caches, con
         if (batch->max_new < 1 || batch->max_new > kPgNodes)
             return set_error(EA_ERR_UNSUPPORTED, "%s: max_new %d (1 to %d nodes)", what, batch->max_new, kPgNodes);
         if (width < 1) return set_error(EA_ERR_ARG, "%s: paths of %d entries", what, width);
+        if (off_4({path, counts, lens_out})) return set_error(EA_ERR_ARG, "%s: arrays must be aligned to 4 bytes", what);
         const size_t n = batch->n_seqs, path_bytes = n * width * 4;
         for (int i = 0; i < n_caches; i++) {
             const ea_cache_s *c = caches[i];

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <exception>
+#include <initializer_list>
 
 #include "paged.h"
 #include "plan.h"
@@ -29,8 +30,16 @@ inline ea_status dense_rows(const ea_relation_s *r, const char *what, int traili
     return EA_OK;
 }
 
+// Some of the arrays is off a boundary of its 4-byte elements, which a kernel's access would fault on.
+inline bool off_4(std::initializer_list<const void *> arrays) {
+    for (const void *p : arrays)
+        if (((uintptr_t)p & 3) != 0) return true;
+    return false;
+}
+
 inline ea_status batch_args(const ea_page_batch *b, int32_t page, int64_t rows) {
     if (!b || !b->pages || !b->starts || !b->lens) return set_error(EA_ERR_ARG, "cache: NULL batch or batch array");
+    if (off_4({b->pages, b->starts, b->lens})) return set_error(EA_ERR_ARG, "cache: the batch's arrays must be aligned to 4 bytes");
     if (b->n_seqs < 1 || b->n_seqs > 65536) return set_error(EA_ERR_ARG, "cache: n_seqs %d out of [1, 65536]", b->n_seqs);
     if (b->max_pages < 1 || b->page_stride < b->max_pages)
         return set_error(EA_ERR_ARG, "cache: max_pages %d, page_stride %lld", b->max_pages, (long long)b->page_stride);
@@ -44,7 +53,7 @@ inline ea_status batch_args(const ea_page_batch *b, int32_t page, int64_t rows) 
 
 // The parents of a batch's rows (device array of `rows` entries).
 inline ea_status tree_args(const char *what, const ea_page_batch *b, const int32_t *parents, int64_t rows) {
-    if (((uintptr_t)parents & 3) != 0) return set_error(EA_ERR_ARG, "%s: parents must be aligned to 4 bytes", what);
+    if (off_4({parents})) return set_error(EA_ERR_ARG, "%s: parents must be aligned to 4 bytes", what);
     const int64_t most = b->max_new > 0 && b->max_new < rows ? b->max_new : rows;
     if (most > kPgNodes)
         return set_error(EA_ERR_UNSUPPORTED, "%s: trees of up to %lld nodes (%d at most; give max_new)", what, (long long)most, kPgNodes);
