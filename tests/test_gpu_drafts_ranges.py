@@ -16,7 +16,7 @@ torch = pytest.importorskip("torch")
 
 from test_gpu_cache import fill, nan_cache, on_gpu, relation, values  # noqa: E402
 from test_gpu_cache_ranges import scaled_fill  # noqa: E402
-from test_gpu_drafts import expect, parents_of, run_verify, verify_batch  # noqa: E402
+from test_gpu_drafts import expect, parents_of, rotary_bound, run_verify, verify_batch  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -185,3 +185,121 @@ def test_rotary_refuses_a_result_without_its_operand():
     at = torch.zeros(2, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         rotary(q, None, Rotary(64), positions=at, q_out=q, k_out=o)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("rows,heads,dim,dims,offset", [(3, 65535, 2, 2, 0), (2, 1, 65535, 256, 65279), (300001, 1, 6, 4, 2), (1, 1, 2, 2, 0)])
+def test_rotary_largest_and_smallest(rows, heads, dim, dims, offset, layout, dtype):
+    """The most heads, columns and many rows, in place and into new rows; positions up to the last one there is."""
+    from tensor_relational_einsum_gb300 import PageBatch, Rotary, rotary
+    from tensor_relational_einsum_gb300.relation import check
+    rng = np.random.default_rng(90)
+    plan = Rotary(dims, layout=layout, offset=offset)
+    n = min(rows, 128)
+    x = torch.from_numpy(rng.normal(size=(rows, heads, dim))).to(dtype)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = PageBatch(torch.zeros(1, 1, **i32), torch.tensor([rows - n, rows], **i32), torch.tensor([2 ** 31 - 1], **i32), max_new=n)
+    # at t f = 2^31 half a step of fp64 is 2^-22: t f and 2 pi here, f / 2 pi and its factor there, 4 * 2^-22 of an angle
+    at = np.full(rows, -1, dtype=np.int64)
+    at[rows - n:] = np.arange(2 ** 31 - 1 - n, 2 ** 31 - 1)
+    some = np.unique(np.concatenate([[0], np.arange(max(0, rows - n - 1), rows)]))
+    want, big = du.rotate(x[some].double().numpy(), at[some], plan.freqs, layout, offset)
+    for place in (True, False):
+        d = x.cuda()
+        o = d if place else torch.full_like(d, -3.0)
+        rotary(relation(d), None, plan, batch, q_out=relation(o))
+        check()
+        still = at[some] < 0
+        got = o[torch.from_numpy(some).cuda()].double().cpu().numpy()
+        assert np.array_equal(got[still], x[some].double().numpy()[still] if place else np.full_like(got[still], -3.0))
+        assert np.all(np.abs(got - want)[~still] <= (rotary_bound(want, big, dtype) + 1e-6 * big)[~still])
+
+
+# ------------------------------------------------------------ ends of ranges
+
+def test_a_chain_of_128_accepted_nodes_is_kept_where_it_is():
+    """Every node accepted: the longest path; the keep that follows moves nothing."""
+    from tensor_relational_einsum_gb300 import cache_keep
+    from tensor_relational_einsum_gb300.relation import check
+    b, trees, parents, target, draft, tokens, accept, sample = verify_batch([128, 127], 501, torch.float32, True, "chain", 45)
+    accept[:] = 0.0
+    for p in (None, parents):
+        got = run_verify(b, p, target, draft, tokens, accept, sample)
+        check()
+        expect(b, trees, target, draft, tokens, accept, sample, got)
+        assert got[1].tolist() == [128, 127]
+    c = nan_cache(b, 1, 64, "bf16")
+    fill(c, b, np.random.default_rng(46))
+    was = c.k.view(torch.int16).clone()
+    lens = cache_keep(c, on_gpu(b, max_new=128), got[0], got[1])
+    check()
+    assert torch.equal(c.k.view(torch.int16), was) and lens.tolist() == [t for _, t in b.seqs]
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+def test_verify_tokens_twice_and_tiny_vocabularies(drafts):
+    """Siblings of one token, and more children than tokens."""
+    from tensor_relational_einsum_gb300.relation import check
+    for vocab, seed in ((3, 47), (4, 48), (40, 49)):
+        b, trees, parents, target, draft, tokens, accept, sample = verify_batch([12, 7, 30, 2], vocab, torch.float32, drafts, "star", seed,
+                                                                                branch_noise=1.5)
+        accept[:] = np.sqrt(accept)
+        got = run_verify(b, parents, target, draft, tokens, accept, sample)
+        check()
+        expect(b, trees, target, draft, tokens, accept, sample, got)
+
+
+def test_verify_many_sequences_and_a_wide_vocabulary():
+    from tensor_relational_einsum_gb300.relation import check
+    for ns, vocab in (([1, 2, 0] * 3000, 5), ([2], (1 << 22) + 5)):
+        b, trees, parents, target, draft, tokens, accept, sample = verify_batch(ns, vocab, torch.float32, True, "chain", 51)
+        got = run_verify(b, parents, target, draft, tokens, accept, sample)
+        check()
+        expect(b, trees, target, draft, tokens, accept, sample, got)
+
+
+def test_keep_many_sequences():
+    from tensor_relational_einsum_gb300 import PagedCache, cache_keep
+    from tensor_relational_einsum_gb300.relation import check
+    rng = np.random.default_rng(52)
+    seqs = [(3, 3 + int(t)) for t in rng.integers(0, 14, size=5000)]
+    b = cu.Batch(seqs, 16, seed=53)
+    pools = [[torch.randint(-9999, 9999, (b.pages_total, 1, 16, 64), dtype=torch.int16, device="cuda") for _ in range(2)] for _ in range(3)]
+    was = [[t.clone() for t in p] for p in pools]
+    caches = [PagedCache(b.pages_total, 16, 1, 64, "bf16", k=p[0].view(torch.bfloat16), v=p[1].view(torch.bfloat16)) for p in pools]
+    path = torch.tensor([0, 2, -1], dtype=torch.int32, device="cuda").repeat(5000, 1)
+    lens = cache_keep(caches, on_gpu(b, max_new=3), path, torch.full((5000,), 2, dtype=torch.int32, device="cuda"))
+    check()
+    assert lens.tolist() == [t - 1 for _, t in seqs]
+    t = b.lens.astype(np.int64)
+    pages = torch.from_numpy(b.pages).long().cuda()
+    i = torch.arange(5000, device="cuda")
+    src, dst = torch.from_numpy(t - 1).cuda(), torch.from_numpy(t - 2).cuda()
+    for got, old in zip(pools, was):
+        for g, w in zip(got, old):
+            w[pages[i, dst // 16], :, dst % 16] = w[pages[i, src // 16], :, src % 16]
+            assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group,n", [(128, 128), (31, 77), (7, 128), (5, 6), (33, 1)])
+def test_trees_under_wide_groups(group, n, fmt):
+    from tensor_relational_einsum_gb300 import cache_attention
+    from tensor_relational_einsum_gb300.relation import check
+    b = cu.Batch([(n, n + 130), (max(1, n // 2), n)], 32, before=1, seed=54)
+    c = nan_cache(b, 1, 64, fmt)
+    rng = np.random.default_rng(55)
+    held = fill(c, b, rng)
+    trees, parents = parents_of(b, "random")
+    q = values(rng, (b.rows, group, 64))
+    out = cache_attention(relation(torch.from_numpy(q).to(torch.bfloat16).cuda()), c, on_gpu(b, max_new=n), parents=parents)
+    check()
+    got = out.to_dense().double().cpu().numpy()
+    for i, (rows, t) in enumerate(b.seqs):
+        k, v = (x[:, 0] for x in held[i])
+        for j in range(rows):
+            keep = du.kept_positions(trees[i], j, rows, t)
+            r = int(b.starts[i]) + j
+            o, _, _, big, slack = cu.softmax_attention(q[r], k[keep], v[keep], None, 0.125, False)
+            assert np.all(np.abs(got[r] - o) <= cu.out_bound(o, big, slack, len(keep))), (i, j)
